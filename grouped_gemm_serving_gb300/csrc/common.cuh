@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "moe.h"
@@ -21,11 +22,16 @@
 namespace moe {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned_to(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // Device address of the current device's error word (defined in errors.cu).
 int* device_error_word();
 // Number of SMs of the current device (cached per device).
 int sm_count();
+// Blocks of `threads` threads of the kernel that the current device holds at
+// once (0 on failure).  `cache` is the kernel's own, one entry per device.
+constexpr int kMaxDevices = 64;
+int resident_blocks(const void* kernel, int threads, size_t smem, std::atomic<int> (&cache)[kMaxDevices]);
 
 __device__ __forceinline__ void raise_device_error(int* err, int code) {
     atomicCAS(err, 0, code);
@@ -399,6 +405,31 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// The gated block's activation and its gradient, from the pre-activations g and
+// u and the gradient d of h = silu(g) * u:  with s = 1 / (1 + exp(-g)),
+//   du = d g s,   dg = d u s (1 + g (1 - s)).
+// For g far below zero exp(-g) overflows to infinity and s is 0, so all three
+// are 0 (times a finite factor), their limits.
+__device__ __forceinline__ void swiglu_grad(float d, float g, float u, float& dg, float& du, float& h) {
+    const float s = 1.0f / (1.0f + __expf(-g));
+    const float a = g * s;
+    h = a * u;
+    du = d * a;
+    dg = d * u * (s * fmaf(g, 1.0f - s, 1.0f));
+}
+
+// Order-preserving map of a float to an unsigned key: a larger float gives a
+// larger key and +0 and -0 the same key.  NaN maps to 0, below every number,
+// so it is never picked; 0 also marks a logit already picked.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);   // -0 + 0 = +0
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
 }  // namespace moe

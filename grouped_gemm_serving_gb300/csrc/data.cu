@@ -5,6 +5,7 @@
 #include <climits>
 
 #include "common.cuh"
+#include "internal.h"
 
 namespace {
 
@@ -102,8 +103,9 @@ swiglu_kernel(const uint4* __restrict__ Y1, const int32_t* __restrict__ offsets,
     }
 }
 
-// out[t] = sum_j w[t,j] * Y2[row_pos[t*k+j]] over non-sentinel slots, fp32 in
-// j order; one warp per token, 8 columns (one 16-byte vector) per lane step.
+// out[t] = sum_j w[t,j] * Y2[row_pos[t*k+j]] over non-sentinel slots (w NULL:
+// unit weights, the permute's gradient), fp32 in j order; one warp per token,
+// 8 columns (one 16-byte vector) per lane step.
 // KG slots are loaded at a time.  With KG = 4 (top-k up to 4) the kernel
 // fits 64 registers, so four blocks share an SM: a 4096-token grid then runs
 // in one wave with 32 warps per SM, where KG = 8 (118 registers) allows two
@@ -128,7 +130,7 @@ combine_kernel(const uint4* __restrict__ Y2, const int32_t* __restrict__ ids,
                 moe::raise_device_error(err, MOE_DEVERR_ROUTE);
             } else {
                 my_row = pos;
-                my_w = w[f];
+                my_w = w ? w[f] : 1.0f;
             }
         }
     }
@@ -209,7 +211,7 @@ combine_split_kernel(const uint4* __restrict__ Y2, const int32_t* __restrict__ i
                 if (seg == 0) moe::raise_device_error(err, MOE_DEVERR_ROUTE);
             } else {
                 my_row = pos;
-                my_w = w[f];
+                my_w = w ? w[f] : 1.0f;
             }
         }
     }
@@ -327,10 +329,9 @@ extern "C" moe_status_t moe_swiglu(const void* Y1, const int32_t* offsets, int E
     return MOE_OK;
 }
 
-extern "C" moe_status_t moe_combine(const void* Y2, const int32_t* topk_ids, const float* topk_w,
-                                    const int32_t* row_pos, int T, int k, int H, int E, void* out,
-                                    moe_stream_t stream) {
-    MOE_CHECK_ARG(Y2 && topk_ids && topk_w && row_pos && out);
+moe_status_t moe::combine_rows(const void* Y2, const int32_t* topk_ids, const float* topk_w,
+                               const int32_t* row_pos, int T, int k, int H, int E, void* out, cudaStream_t s) {
+    MOE_CHECK_ARG(Y2 && topk_ids && row_pos && out);
     MOE_CHECK_ARG(T >= 1 && k >= 1 && k <= 32 && E >= 1 && H >= 8 && H % 8 == 0);
     MOE_CHECK_ARG(moe::aligned16(Y2) && moe::aligned16(out));
     int* err = moe::device_error_word();
@@ -339,7 +340,7 @@ extern "C" moe_status_t moe_combine(const void* Y2, const int32_t* topk_ids, con
     if (T >= sm * kWarpsPerBlock) {   // at least a block of tokens per SM: one warp per token
         const int blocks = (T + kWarpsPerBlock - 1) / kWarpsPerBlock;
         auto kern = k <= 4 ? combine_kernel<4, 4> : combine_kernel<8, 1>;
-        kern<<<blocks, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        kern<<<blocks, kThreads, 0, s>>>(
             static_cast<const uint4*>(Y2), topk_ids, topk_w, row_pos, T, k, H / 8, E,
             static_cast<int64_t>(T) * k, static_cast<uint4*>(out), err);
         MOE_CHECK_LAUNCH();
@@ -352,9 +353,16 @@ extern "C" moe_status_t moe_combine(const void* Y2, const int32_t* topk_ids, con
     const int segs = static_cast<int>(want < max_segs ? (want > 1 ? want : 1) : max_segs);
     const int seg_vecs = ((row_vecs + segs - 1) / segs + step - 1) / step * step;
     const int64_t blocks = (static_cast<int64_t>(T) * segs + kWarpsPerBlock - 1) / kWarpsPerBlock;
-    combine_split_kernel<<<static_cast<int>(blocks), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+    combine_split_kernel<<<static_cast<int>(blocks), kThreads, 0, s>>>(
         static_cast<const uint4*>(Y2), topk_ids, topk_w, row_pos, T, k, row_vecs, segs, seg_vecs, E,
         static_cast<int64_t>(T) * k, static_cast<uint4*>(out), err);
     MOE_CHECK_LAUNCH();
     return MOE_OK;
+}
+
+extern "C" moe_status_t moe_combine(const void* Y2, const int32_t* topk_ids, const float* topk_w,
+                                    const int32_t* row_pos, int T, int k, int H, int E, void* out,
+                                    moe_stream_t stream) {
+    MOE_CHECK_ARG(topk_w);
+    return moe::combine_rows(Y2, topk_ids, topk_w, row_pos, T, k, H, E, out, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -5,7 +5,7 @@
 #include "common.cuh"
 
 namespace {
-constexpr int kMaxDevices = 64;
+using moe::kMaxDevices;
 __device__ int g_device_error;             // one word per device context
 std::atomic<int*> g_err_ptr[kMaxDevices];  // its device address, per device
 std::atomic<int> g_sm_count[kMaxDevices];
@@ -37,6 +37,20 @@ int sm_count() {
     if (n > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     g_sm_count[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+int resident_blocks(const void* kernel, int threads, size_t smem, std::atomic<int> (&cache)[kMaxDevices]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    n *= sm_count();
+    cache[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -88,7 +88,10 @@ constexpr int kThreads = 128 + kEpiThreads;  // warpgroup 0: TMA, MMA, 2 idle wa
 constexpr uint32_t kTmemCols = 2 * BN;
 constexpr int kStageA = BM * 128;
 constexpr int kStageB = BN * 128;
-enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_Q = 2 };
+// EPI_SWIGLU_KEEP: EPI_SWIGLU that also stores the pre-activations (swapped
+// bf16 only; an instance of its own, so that the inference kernel carries none
+// of it).
+enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_Q = 2, EPI_SWIGLU_KEEP = 3 };
 
 // Stage ring: a single-CTA tile stages 128 A + 256 B rows (48 KB) four deep;
 // a CTA of a pair stages up to 128 + 128 rows (32 KB) seven deep: its
@@ -154,6 +157,7 @@ struct Params {
     int* counters;
     int nfb;
     void* cout;   // out bf16 [T, out_cols]
+    void* keep;   // EPI_SWIGLU_KEEP: the pre-activations, bf16 [M_cap, N]
 };
 
 // Shared memory after the stage ring: barriers and the tile list (every
@@ -809,11 +813,24 @@ __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti,
     }
 }
 
+// Pre-activations kept for the backward pass: a lane's 32 tokens of its own
+// gate (r = 0) or up (r = 1) row of feature f.  Eight neighbouring lanes hold
+// eight neighbouring features of one, so a warp store fills two 32-byte
+// sectors, one of the gate half and one of the up half.
+__device__ __forceinline__ void keep_chunk(const Params& p, int64_t row, int f, int r, int n, const uint32_t (&v)[32]) {
+    if (f >= p.out_cols) return;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.keep) + row * p.N + r * p.half + f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j < n) o[static_cast<int64_t>(j) * p.N] = __float2bfloat16_rn(__uint_as_float(v[j]));
+}
+
 // SwiGLU M = 128 tile: lane l of this CTA holds weight row l % 64 (its 32
 // features' gate and up rows, interleaved in groups of 8 as in a full tile)
 // for token (l / 64) * nh + column, columns below nh = N/2.  Each half of the
 // epilogue takes 64 columns; gate and up lanes swap halves of each 32-column
 // chunk as in a full tile.
+template <bool KEEP>
 __device__ __forceinline__ void swiglu_half_tile(const Params& p, const Tile& ti, uint32_t ta, int q, int hsel,
                                                  int lane, uint32_t rank) {
     const int nh = swap_n(ti) / 2, tok0 = (q >> 1) * nh, ntok = ti.rows;
@@ -835,6 +852,7 @@ __device__ __forceinline__ void swiglu_half_tile(const Params& p, const Tile& ti
             h[j] = r ? silu_mul(o, hi) : silu_mul(lo, o);
         }
         const int f = ti.col0 + static_cast<int>(rank) * 32 + 16 * (q & 1) + 8 * (lane >> 4) + (lane & 7);
+        if (KEEP) keep_chunk(p, ti.row0 + tok0 + col, f, r, jmax, v);
         const int t0 = 16 * r;   // within the chunk
         if (f < p.out_cols) {
             __nv_bfloat16* o = out + static_cast<int64_t>(ti.row0 + tok0 + col + t0) * p.out_cols + f;
@@ -877,7 +895,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
                                  (WG ? static_cast<int64_t>(ti.e) * p.wg_rows * p.out_cols : 0);
             if (EPI != EPI_STORE && ti.half) {
-                swiglu_half_tile(p, ti, ta, q, hsel, lane, rank);
+                swiglu_half_tile<EPI == EPI_SWIGLU_KEEP>(p, ti, ta, q, hsel, lane, rank);
             } else if (EPI == EPI_STORE && ti.half) {
                 store_half_tile(p, ti, ta, q, hsel, lane, rank);
             } else {
@@ -918,6 +936,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
                             h[j] = r ? silu_mul(o, hi) : silu_mul(lo, o);
                         }
                         const int f = ti.col0 + static_cast<int>(rank) * 64 + 16 * q + 8 * (lane >> 4) + (lane & 7);
+                        if (EPI == EPI_SWIGLU_KEEP) keep_chunk(p, ti.row0 + col, f, r, min(32, ntok - col), v);
                         const int t0 = col + 16 * r;
                         if (f < p.out_cols) {
                             __nv_bfloat16* o = out + static_cast<int64_t>(ti.row0 + t0) * p.out_cols + f;
@@ -1123,6 +1142,11 @@ __device__ void zero_sentinel_rows(const Params& p) {
             const int64_t g = i / rows, rr = i - g * rows;
             p.out_scales[g * p.M_cap + L + rr] = 1.0f;
         }
+    }
+    if (EPI == EPI_SWIGLU_KEEP) {
+        const int64_t kv = static_cast<int64_t>(p.N) * 2 / 16;
+        uint4* kept = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.keep) + static_cast<int64_t>(L) * p.N);
+        for (int64_t i = tid; i < rows * kv; i += nthr) kept[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -1355,12 +1379,13 @@ struct FusedCombine {
 };
 
 // With weights_mn (bf16 store only) B is [E, K, N], read MN-major.  With fc
-// (bf16 store only) the weighted combine is fused into the epilogue.
+// (bf16 store only) the weighted combine is fused into the epilogue.  With keep
+// (bf16 SwiGLU only) the pre-activations are stored too, bf16 [M_cap, N].
 moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_scales, const void* gx,
                               const int32_t* sorted_rows, int T, int topk, const void* B,
                               const float* B_scales, const int32_t* offsets, int E, int M_cap, int N, int K,
                               moe_epilogue_t epilogue, void* C, float* C_scales, moe_stream_t stream,
-                              bool weights_mn = false, const FusedCombine* fc = nullptr) {
+                              bool weights_mn = false, const FusedCombine* fc = nullptr, void* keep = nullptr) {
     MOE_CHECK_ARG(A && B && offsets && C && E >= 1 && E <= kMaxE && M_cap >= 1 && N >= 8 && K >= 8);
     MOE_CHECK_ARG(moe::aligned16(A) && moe::aligned16(B) && moe::aligned16(C));
     const bool fp8 = dtype == MOE_FP8_E4M3_B128;
@@ -1471,6 +1496,8 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
     p.wg_rows = 0;
     p.mn_a = weights_mn ? 1 : 0;
     p.fc = 0;
+    p.keep = keep;
+    if (keep && (fp8 || !swiglu || gx)) return MOE_ERR_UNSUPPORTED;
     if (fc) {
         if (fp8 || swiglu || gx || weights_mn) return MOE_ERR_UNSUPPORTED;
         p.fc = 1;
@@ -1492,6 +1519,7 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
     }
     if (swap) {
         if (epilogue == MOE_EPI_STORE) return launch<false, EPI_STORE, true>(tmA, tmB, tmX, p, s);
+        if (keep) return launch<false, EPI_SWIGLU_KEEP, true>(tmA, tmB, tmX, p, s);
         return launch<false, EPI_SWIGLU, true>(tmA, tmB, tmX, p, s);
     }
     if (epilogue == MOE_EPI_STORE) return launch<false, EPI_STORE>(tmA, tmB, tmX, p, s);
@@ -1507,6 +1535,12 @@ moe_status_t moe::dgrad_gemm(const void* dC, const void* B, const int32_t* offse
     // MN-major in place
     return run_grouped_gemm(MOE_BF16, dC, nullptr, nullptr, nullptr, 0, 0, B, nullptr, offsets, E, M_cap, K, N,
                             MOE_EPI_STORE, dA, nullptr, reinterpret_cast<moe_stream_t>(s), true);
+}
+
+moe_status_t moe::swiglu_keep_gemm(const void* x, const void* W1, const int32_t* offsets, int E, int M_cap, int N,
+                                   int K, void* Y1, void* h, cudaStream_t s) {
+    return run_grouped_gemm(MOE_BF16, x, nullptr, nullptr, nullptr, 0, 0, W1, nullptr, offsets, E, M_cap, N, K,
+                            MOE_EPI_SWIGLU, h, nullptr, reinterpret_cast<moe_stream_t>(s), false, nullptr, Y1);
 }
 
 moe_status_t moe::wgrad_gemm(const void* dC, const void* A, const void* tails, const int32_t* offsets, int E,

@@ -1,6 +1,8 @@
 // Declarations shared between translation units of libmoe.so (not exported).
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include "moe.h"
 
 namespace moe {
@@ -22,5 +24,16 @@ moe_status_t dgrad_gemm(const void* dC, const void* B, const int32_t* offsets, i
 // expert without rows gets zeros.
 moe_status_t wgrad_gemm(const void* dC, const void* A, const void* tails, const int32_t* offsets, int E,
                         int M_cap, int N, int K, void* dB, cudaStream_t stream);
+
+// Launches the bf16 gate_up GEMM with SwiGLU that also keeps its
+// pre-activations (grouped_gemm.cu): Y1 = [gate | up] bf16 [M_cap, N] rounded
+// from the fp32 accumulators, h bf16 [M_cap, N/2] computed from them unrounded;
+// rows p >= offsets[E] of both are zeros.
+moe_status_t swiglu_keep_gemm(const void* x, const void* W1, const int32_t* offsets, int E, int M_cap, int N, int K,
+                              void* Y1, void* h, cudaStream_t stream);
+
+// The weighted combine (data.cu); topk_w NULL: unit weights.
+moe_status_t combine_rows(const void* Y2, const int32_t* topk_ids, const float* topk_w, const int32_t* row_pos,
+                          int T, int k, int H, int E, void* out, cudaStream_t stream);
 
 }  // namespace moe

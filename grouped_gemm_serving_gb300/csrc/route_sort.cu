@@ -49,17 +49,8 @@ SortGeometry geometry(int T, int k) {
     return g;
 }
 
-// Order-preserving map of a float to an unsigned key: a larger float gives a
-// larger key and +0 and -0 the same key.  NaN maps to 0, below every number,
-// so it is never picked; 0 also marks a logit already picked.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t u = __float_as_uint(v + 0.0f);   // -0 + 0 = +0
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t key) {
-    return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
-}
+using moe::key_value;
+using moe::order_key;
 
 // Ids outside [0, E] cannot be placed: they are sorted as sentinels and the
 // error word records the bad input.

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_DEVICE_CHECK, MOE_ERR_TIMEOUT = 4, 5, 6
-MOE_BF16, MOE_FP8_E4M3_B128 = 0, 1
+MOE_BF16, MOE_FP8_E4M3_B128, MOE_F32 = 0, 1, 2
 MOE_EPI_STORE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_QUANT_FP8 = 0, 1, 2
 MOE_DEVERR_NONE, MOE_DEVERR_OFFSETS, MOE_DEVERR_TIMEOUT, MOE_DEVERR_ROUTE = 0, 1, 2, 3
 MOE_FWD_HOST_IO = 1
@@ -44,6 +44,7 @@ class ForwardArgs(C.Structure):
 
 
 _P, _I, _S, _Z = C.c_void_p, C.c_int, C.c_int, C.c_size_t
+_L, _F = C.c_int64, C.c_float
 _SIGS = {
     "moe_abi_version": (C.c_int, []),
     "moe_status_string": (C.c_char_p, [_I]),
@@ -66,6 +67,15 @@ _SIGS = {
     "moe_batched_matmul": (_S, [_I, _P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _Z, _P]),
     "moe_grouped_gemm_combine_workspace_size": (_Z, [_I, _I]),
     "moe_grouped_gemm_combine": (_S, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _P]),
+    "moe_ffn_forward": (_S, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_ffn_backward_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "moe_ffn_backward": (_S, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
+    "moe_combine_backward": (_S, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_permute_backward": (_S, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_route_backward": (_S, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_layer_norm_forward": (_S, [_I, _P, _L, _I, _I, _I, _P, _P, _F, _P, _L, _P, _P, _P]),
+    "moe_layer_norm_backward_workspace_size": (_Z, [_I, _I]),
+    "moe_layer_norm_backward": (_S, [_I, _P, _L, _P, _L, _I, _I, _I, _P, _P, _P, _P, _L, _P, _P, _P, _Z, _P]),
     "moe_swiglu": (_S, [_P, _P, _I, _I, _I, _P, _P]),
     "moe_combine": (_S, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_forward_workspace_size": (_Z, [C.POINTER(ForwardArgs)]),
@@ -231,6 +241,51 @@ def moe_grouped_gemm_combine(h, W2, offsets, E, M_cap, H, I, topk_ids, topk_w, s
     _check(lib().moe_grouped_gemm_combine(_p(h), _p(W2), _p(offsets), E, M_cap, H, I, _p(topk_ids), _p(topk_w),
                                           _p(sorted_rows), _p(row_pos), T, k, _p(Y2), _p(out), _p(ws), ws_bytes,
                                           _stream(stream)), "moe_grouped_gemm_combine")
+
+
+def moe_ffn_forward(x, W1, W2, offsets, E, M_cap, H, I, Y1, h, y, stream=None):
+    _check(lib().moe_ffn_forward(_p(x), _p(W1), _p(W2), _p(offsets), E, M_cap, H, I, _p(Y1), _p(h), _p(y),
+                                 _stream(stream)), "moe_ffn_forward")
+
+
+def moe_ffn_backward_workspace_size(E, M_cap, H, I) -> int:
+    return lib().moe_ffn_backward_workspace_size(E, M_cap, H, I)
+
+
+def moe_ffn_backward(x, W1, W2, Y1, dy, offsets, E, M_cap, H, I, dx, dW1, dW2, ws, ws_bytes, stream=None):
+    _check(lib().moe_ffn_backward(_p(x), _p(W1), _p(W2), _p(Y1), _p(dy), _p(offsets), E, M_cap, H, I, _p(dx),
+                                  _p(dW1), _p(dW2), _p(ws), ws_bytes, _stream(stream)), "moe_ffn_backward")
+
+
+def moe_combine_backward(dout, Y2, topk_ids, topk_w, row_pos, T, k, H, E, dY2, dtopk_w, stream=None):
+    _check(lib().moe_combine_backward(_p(dout), _p(Y2), _p(topk_ids), _p(topk_w), _p(row_pos), T, k, H, E,
+                                      _p(dY2), _p(dtopk_w), _stream(stream)), "moe_combine_backward")
+
+
+def moe_permute_backward(dxp, topk_ids, row_pos, T, k, H, E, dx, stream=None):
+    _check(lib().moe_permute_backward(_p(dxp), _p(topk_ids), _p(row_pos), T, k, H, E, _p(dx), _stream(stream)),
+           "moe_permute_backward")
+
+
+def moe_route_backward(logits, expert_bias, dtopk_w, T, E, k, renormalize, dlogits, stream=None):
+    _check(lib().moe_route_backward(_p(logits), _p(expert_bias), _p(dtopk_w), T, E, k, int(renormalize),
+                                    _p(dlogits), _stream(stream)), "moe_route_backward")
+
+
+def moe_layer_norm_forward(dtype, x, ldx, rows, H, w_dtype, weight, bias, eps, y, ldy, mean, rstd, stream=None):
+    _check(lib().moe_layer_norm_forward(dtype, _p(x), ldx, rows, H, w_dtype, _p(weight), _p(bias), eps, _p(y), ldy,
+                                        _p(mean), _p(rstd), _stream(stream)), "moe_layer_norm_forward")
+
+
+def moe_layer_norm_backward_workspace_size(rows, H) -> int:
+    return lib().moe_layer_norm_backward_workspace_size(rows, H)
+
+
+def moe_layer_norm_backward(dtype, dy, lddy, x, ldx, rows, H, w_dtype, weight, mean, rstd, dx, lddx, dweight, dbias,
+                            ws, ws_bytes, stream=None):
+    _check(lib().moe_layer_norm_backward(dtype, _p(dy), lddy, _p(x), ldx, rows, H, w_dtype, _p(weight), _p(mean),
+                                         _p(rstd), _p(dx), lddx, _p(dweight), _p(dbias), _p(ws), ws_bytes,
+                                         _stream(stream)), "moe_layer_norm_backward")
 
 
 def moe_swiglu(Y1, offsets, E, M_cap, I, h, stream=None):

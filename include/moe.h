@@ -77,8 +77,9 @@ typedef enum {
 
 typedef enum {
     MOE_BF16 = 0,          /* bf16 operands, fp32 accumulation */
-    MOE_FP8_E4M3_B128 = 1  /* e4m3 operands; activations scaled per row per 128
+    MOE_FP8_E4M3_B128 = 1, /* e4m3 operands; activations scaled per row per 128
                               columns, weights per 128x128 block; fp32 scales */
+    MOE_F32 = 2            /* fp32 (layer norm only) */
 } moe_dtype_t;
 
 typedef enum {
@@ -361,6 +362,107 @@ size_t moe_grouped_gemm_wgrad_workspace_size(int E, int M_cap, int N, int K);
 moe_status_t moe_grouped_gemm_wgrad(const void* A, const void* dC, const int32_t* offsets, int E,
                                     int M_cap, int N, int K, void* dB, void* ws, size_t ws_bytes,
                                     moe_stream_t stream);
+
+/*
+ * moe_ffn_forward, moe_ffn_backward -- the gated feed-forward block of the
+ * experts as a differentiable block (MoE training on grouped GEMMs, "Mixture
+ * of Experts in transformers"; fc1 -> silu(gate) * up -> fc2 of section 1 of
+ * the LlamaFactory write-up).  bf16 in and out, fp32 accumulation.  For every
+ * row p of expert e (offsets as in moe_grouped_gemm):
+ *   [g | u] = W1[e] x[p],   h = silu(g) * u,   y[p] = W2[e] h.
+ * E = 1 with offsets {0, rows} is a dense block (a shared expert).
+ *
+ * moe_ffn_forward:  x bf16 [M_cap, H] (permuted rows); W1 bf16 [E, 2I, H]
+ *   (gate rows, then up rows); W2 bf16 [E, H, I]; y bf16 [M_cap, H] out;
+ *   h bf16 [M_cap, I] scratch (holds h afterwards).  Y1 bf16 [M_cap, 2I] out:
+ *   the pre-activations [g | u], which moe_ffn_backward needs; NULL for
+ *   inference.  h is computed from the unrounded g and u, as in
+ *   moe_grouped_gemm, whose results h and y equal bit for bit.
+ *   Rows p >= offsets[E] of x are never read; those of y, h and Y1 are zeros.
+ * moe_ffn_backward:  from x, W1, W2, Y1 and the gradient dy of y:
+ *   dx bf16 [M_cap, H], dW1 bf16 [E, 2I, H], dW2 bf16 [E, H, I], the
+ *   gradients (not accumulated into what was there).  Each of the three may be
+ *   NULL and is then not computed (frozen weights); x may be NULL when dW1
+ *   is.  h is computed again from Y1.  Rows p >= offsets[E] of x, Y1 and dy
+ *   are never read, those of dx are zeros; an expert without rows gets zero
+ *   weight gradients.
+ *   ws: moe_ffn_backward_workspace_size(E, M_cap, H, I) bytes.
+ * Limits: 1 <= E <= 256, M_cap >= 1, H and I positive multiples of 8.
+ * Invalid offsets: MOE_DEVERR_OFFSETS, nothing computed.
+ */
+moe_status_t moe_ffn_forward(const void* x, const void* W1, const void* W2, const int32_t* offsets, int E,
+                             int M_cap, int H, int I, void* Y1, void* h, void* y, moe_stream_t stream);
+size_t moe_ffn_backward_workspace_size(int E, int M_cap, int H, int I);
+moe_status_t moe_ffn_backward(const void* x, const void* W1, const void* W2, const void* Y1, const void* dy,
+                              const int32_t* offsets, int E, int M_cap, int H, int I, void* dx, void* dW1,
+                              void* dW2, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Gradients of the routing's data path, for training the whole layer
+ * ("Mixture of Experts in transformers", MoE basics: the router's weights
+ * scale the experts' outputs, so the router learns through them).  T, k, H, E
+ * and the arrays are those of the forward calls.
+ *
+ * moe_combine_backward (of moe_combine):  for every slot f = t*k + j with
+ *   p = row_pos[f]:  dY2[p, :] = topk_w[f] * dout[t, :] rounded to bf16 and
+ *   dtopk_w[f] = sum_h dout[t, h] * Y2[p, h] in fp32.  A sentinel slot (id E)
+ *   gets dtopk_w = 0 and its row of dY2 zeros; its row of Y2 is never read.
+ *   dout bf16 [T, H]; Y2, dY2 bf16 [T*k, H] (rows of a larger M_cap past T*k
+ *   are not touched); topk_ids int32, topk_w, dtopk_w fp32 [T, k]; row_pos
+ *   int32 [T*k].  A row_pos outside [0, T*k): MOE_DEVERR_ROUTE, the slot is
+ *   skipped.
+ * moe_permute_backward (of moe_permute):  dx[t, :] = sum over j with
+ *   topk_ids[t, j] != E of dxp[row_pos[t*k + j], :], in fp32 in j order,
+ *   rounded to bf16 (moe_combine with unit weights).  dxp bf16 [T*k, H]; dx
+ *   bf16 [T, H].
+ * moe_route_backward (of moe_route_sort's weights):  dlogits fp32 [T, E], the
+ *   gradient of the logits (and, summed over t, of expert_bias) from that of
+ *   the weights.  The picks are found again from logits and expert_bias, by
+ *   moe_route_sort's rule, so slots that a sentinel mask took out (their
+ *   dtopk_w is 0) still count in the softmax as they did forward.  With p the
+ *   softmax over the picks (renormalize != 0) or over E (== 0) and S = sum over
+ *   picks of p_i dtopk_w_i:  dlogits[e] = p_e * (dtopk_w_j - S) for the pick j
+ *   of expert e; elsewhere 0 (renormalize != 0) or -p_e * S.
+ * Limits: 1 <= E <= 256 (route), 1 <= k <= 32, k <= E (route), T >= 1,
+ *   T*k < 2^31, H a positive multiple of 8.
+ */
+moe_status_t moe_combine_backward(const void* dout, const void* Y2, const int32_t* topk_ids,
+                                  const float* topk_w, const int32_t* row_pos, int T, int k, int H, int E,
+                                  void* dY2, float* dtopk_w, moe_stream_t stream);
+moe_status_t moe_permute_backward(const void* dxp, const int32_t* topk_ids, const int32_t* row_pos, int T, int k,
+                                  int H, int E, void* dx, moe_stream_t stream);
+moe_status_t moe_route_backward(const float* logits, const float* expert_bias, const float* dtopk_w, int T, int E,
+                                int k, int renormalize, float* dlogits, moe_stream_t stream);
+
+/*
+ * moe_layer_norm_forward, moe_layer_norm_backward -- layer norm over the last
+ * dimension, the norm in front of the block.  Per row:
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps), var the
+ *   mean of (x - mean)^2; all arithmetic and sums in fp32.
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)) with xh = (x - mean) * rstd
+ *   and g = dy * weight;  dweight = sum over rows of dy * xh;  dbias = sum over
+ *   rows of dy.
+ * dtype (MOE_BF16 or MOE_F32) is the type of x, y, dy and dx; w_dtype (the
+ * same, or MOE_F32) that of weight, bias, dweight and dbias [H].  mean and
+ * rstd fp32 [rows].  weight NULL: ones; bias NULL: zeros.  mean and rstd may be
+ * NULL in the forward call (inference).  Each of dx, dweight and dbias may be
+ * NULL and is then not computed; at least one is given.
+ * Rows may lie apart: row r of x starts at x + r * ldx elements (ldx >= H), and
+ * so on.  x, y, dy and dx need only be aligned to their element; rows that
+ * start on 16-byte boundaries and fill whole 16-byte vectors move faster.
+ * y may be x, and dx may be dy or x, with the same stride.
+ * ws: moe_layer_norm_backward_workspace_size(rows, H) bytes (dweight or dbias
+ * wanted; else it may be NULL).
+ * Limits: rows >= 1, H >= 1, eps >= 0.
+ */
+moe_status_t moe_layer_norm_forward(moe_dtype_t dtype, const void* x, int64_t ldx, int rows, int H,
+                                    moe_dtype_t w_dtype, const void* weight, const void* bias, float eps,
+                                    void* y, int64_t ldy, float* mean, float* rstd, moe_stream_t stream);
+size_t moe_layer_norm_backward_workspace_size(int rows, int H);
+moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                     int rows, int H, moe_dtype_t w_dtype, const void* weight, const float* mean,
+                                     const float* rstd, void* dx, int64_t lddx, void* dweight, void* dbias,
+                                     void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * moe_batched_matmul -- the batched expert backend ("Mixture of Experts in
