@@ -98,5 +98,5 @@ extern "C" moe_status_t moe_grouped_gemm_wgrad(const void* A, const void* dC, co
         static_cast<const uint16_t*>(dC), N, static_cast<const uint16_t*>(A), K, offsets, E, M_cap,
         static_cast<uint16_t*>(ws), err);
     MOE_CHECK_LAUNCH();
-    return moe::wgrad_gemm(dC, A, ws, offsets, E, M_cap, N, K, dB, s);
+    return moe::wgrad_gemm(dC, N, A, ws, offsets, E, M_cap, N, K, dB, s);
 }

@@ -90,8 +90,10 @@ constexpr int kStageA = BM * 128;
 constexpr int kStageB = BN * 128;
 // EPI_SWIGLU_KEEP: EPI_SWIGLU that also stores the pre-activations (swapped
 // bf16 only; an instance of its own, so that the inference kernel carries none
-// of it).
-enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_Q = 2, EPI_SWIGLU_KEEP = 3 };
+// of it).  EPI_SUM: a store whose sum over several launches is held in fp32
+// (swapped data gradient only; see Params::sum).
+enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_Q = 2, EPI_SWIGLU_KEEP = 3, EPI_SUM = 4 };
+__host__ __device__ constexpr bool plain_tiles(int epi) { return epi == EPI_STORE || epi == EPI_SUM; }
 
 // Stage ring: a single-CTA tile stages 128 A + 256 B rows (48 KB) four deep;
 // a CTA of a pair stages up to 128 + 128 rows (32 KB) seven deep: its
@@ -158,6 +160,14 @@ struct Params {
     int nfb;
     void* cout;   // out bf16 [T, out_cols]
     void* keep;   // EPI_SWIGLU_KEEP: the pre-activations, bf16 [M_cap, N]
+    // EPI_SUM: with C this launch's product, the first launch sets
+    // sum [M_cap, N] = C, the others add to it, and the last one stores
+    // out = row_scale[row] * (sum + C) instead (row_scale NULL: 1)
+    float* sum;
+    int sum_first, sum_last;
+    const float* row_scale;
+    int token_tiles;   // > 0: token tiles of every expert (else one per BT rows)
+    int no_tails;      // weight gradient: rows past the last expert's lie outside the tensor maps (zeros)
 };
 
 // Shared memory after the stage ring: barriers and the tile list (every
@@ -413,7 +423,7 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
         const int xbytes = WG ? (nh > 64 ? 2 : 1) * 8192 : nh * 128;
         const int abytes = ti.half ? kStageA / 2 : kStageA;   // M = 128: 64 weight rows per CTA
         const int nkb = WG ? ti.nkb : p.k_blocks;
-        const int nfull = WG ? (p.offsets[ti.e + 1] - ti.first) / 64 : 0;   // k-blocks read in place
+        const int nfull = WG ? (p.offsets[ti.e + 1] - ti.first + (p.no_tails ? 63 : 0)) / 64 : 0;   // k-blocks read in place
         for (int kb = 0; kb < nkb; ++kb) {
             const bool got = moe::mbar_wait(bar(S.empty[stage]), phase ^ 1u, &S.abort_flag, kWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
@@ -440,14 +450,14 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
                     moe::tma_load_2d_pair(sa + 8192, ma, fb, f0 + 64, row);
                     moe::tma_load_2d_pair(sb, mc, fb, xrow, row);
                     if (nh > 64) moe::tma_load_2d_pair(sb + 8192, mc, fb, xrow + 64, row);
-                } else if (EPI == EPI_STORE && p.mn_a) {
+                } else if (plain_tiles(EPI) && p.mn_a) {
                     // two 64-feature x 64-row swizzle atoms, 8 KB apart (one for M = 128)
                     const int f0 = ti.col0 + static_cast<int>(rank) * (ti.half ? 64 : 128);
                     moe::tma_load_3d_pair(sa, tmW, fb, f0, kc, ti.e);
                     if (!ti.half) moe::tma_load_3d_pair(sa + 8192, tmW, fb, f0 + 64, kc, ti.e);
-                } else if (EPI == EPI_STORE && ti.half) {   // 64 weight rows
+                } else if (plain_tiles(EPI) && ti.half) {   // 64 weight rows
                     moe::tma_load_3d_pair(sa, tmW64, fb, kc, ti.col0 + static_cast<int>(rank) * 64, ti.e);
-                } else if (EPI == EPI_STORE) {
+                } else if (plain_tiles(EPI)) {
                     moe::tma_load_3d_pair(sa, tmW, fb, kc, ti.col0 + static_cast<int>(rank) * 128, ti.e);
                 } else if (ti.half) {   // 4 groups: this CTA's 32 features
                     moe::tma_load_5d_pair(sa, tmW64, fb, kc, 0, 0, (ti.col0 + static_cast<int>(rank) * 32) / 8, ti.e);
@@ -589,7 +599,7 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
             const int n = swap_n(ti);
             const int m = ti.half ? BM : 2 * BM;
             idesc = WG ? moe::make_idesc_ab_mn(1u, 2 * BM, n)
-                 : EPI == EPI_STORE && p.mn_a ? moe::make_idesc_a_mn(1u, m, n) : moe::make_idesc(1u, m, n);
+                 : plain_tiles(EPI) && p.mn_a ? moe::make_idesc_a_mn(1u, m, n) : moe::make_idesc(1u, m, n);
         }
         if (!FP8) {
             // with a pair, the peer's epilogue arrives here from the other CTA
@@ -614,7 +624,7 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
             // MN-major operands (the data gradient's weights; both operands of
             // the weight gradient): a K step of 16 rows is 2 KB further on;
             // K-major: 32 bytes
-            const bool amn = WG || (SWAP && EPI == EPI_STORE && p.mn_a);
+            const bool amn = WG || (SWAP && plain_tiles(EPI) && p.mn_a);
             const uint64_t adesc = amn ? moe::smem_desc_sw128_mn(sa, 8192) : moe::smem_desc_sw128(sa);
             const uint64_t astep = amn ? 2048 >> 4 : 2;
             const uint64_t bdesc = WG ? moe::smem_desc_sw128_mn(sa + kStageA, 8192) : moe::smem_desc_sw128(sa + kStageA);
@@ -788,9 +798,34 @@ __device__ void fused_combine_empty_tokens(const Params& p) {
     }
 }
 
+// EPI_SUM: a lane's n tokens of feature f.  The sum's reads are all issued
+// before the first is used.
+__device__ __forceinline__ void sum_chunk(const Params& p, int64_t row, int f, int n, const uint32_t (&v)[32]) {
+    if (f >= p.out_cols) return;
+    float* acc = p.sum + row * p.out_cols + f;
+    float c[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        c[j] = j < n && !p.sum_first ? acc[static_cast<int64_t>(j) * p.out_cols] : 0.0f;
+    if (!p.sum_last) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n) acc[static_cast<int64_t>(j) * p.out_cols] = c[j] + __uint_as_float(v[j]);
+        return;
+    }
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row * p.out_cols + f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j < n) {
+            const float x = c[j] + __uint_as_float(v[j]);
+            o[static_cast<int64_t>(j) * p.out_cols] = __float2bfloat16_rn(p.row_scale ? p.row_scale[row + j] * x : x);
+        }
+}
+
 // Store M = 128 tile (forward and data gradient): lane l of this CTA holds
 // weight row (output feature) l % 64 for token (l / 64) * nh + column, columns
 // below nh = N/2.  Each half of the epilogue takes 64 columns.
+template <int EPI>
 __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti, uint32_t ta, int q, int hsel,
                                                 int lane, uint32_t rank) {
     const int nh = swap_n(ti) / 2, tok0 = (q >> 1) * nh, ntok = ti.rows;
@@ -804,7 +839,9 @@ __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti,
         uint32_t v[32];
         moe::tmem_ld32(ta + col, v);
         moe::tmem_ld_wait();
-        if (f < p.out_cols) {
+        if (EPI == EPI_SUM) {
+            sum_chunk(p, ti.row0 + tok0 + col, f, jmax, v);
+        } else if (f < p.out_cols) {
             __nv_bfloat16* o = out + static_cast<int64_t>(ti.row0 + tok0 + col) * p.out_cols + f;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -894,10 +931,10 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
             // weight gradient: expert e's output rows start at e * wg_rows
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
                                  (WG ? static_cast<int64_t>(ti.e) * p.wg_rows * p.out_cols : 0);
-            if (EPI != EPI_STORE && ti.half) {
+            if (!plain_tiles(EPI) && ti.half) {
                 swiglu_half_tile<EPI == EPI_SWIGLU_KEEP>(p, ti, ta, q, hsel, lane, rank);
-            } else if (EPI == EPI_STORE && ti.half) {
-                store_half_tile(p, ti, ta, q, hsel, lane, rank);
+            } else if (plain_tiles(EPI) && ti.half) {
+                store_half_tile<EPI>(p, ti, ta, q, hsel, lane, rank);
             } else {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -911,7 +948,10 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                     }
-                    if (EPI == EPI_STORE) {
+                    if (EPI == EPI_SUM) {
+                        sum_chunk(p, ti.row0 + col, ti.col0 + static_cast<int>(rank) * 128 + q * 32 + lane,
+                                  min(32, ntok - col), v);
+                    } else if (EPI == EPI_STORE) {
                         // one output feature per lane; a warp store covers 64
                         // contiguous bytes of one token row
                         const int f = ti.col0 + static_cast<int>(rank) * 128 + q * 32 + lane;
@@ -1189,7 +1229,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
                 const int lo = p.offsets[e], hi = p.offsets[e + 1];
                 if (hi < lo) bad = 1;
                 constexpr int RT = SWAP ? BT : BM;   // rows of an expert per tile
-                mt[i] = hi > lo ? (hi - lo + RT - 1) / RT : 0;
+                mt[i] = hi > lo ? (EPI == EPI_SUM && p.token_tiles ? p.token_tiles : (hi - lo + RT - 1) / RT) : 0;
                 if (WG) kbl[i] = hi > lo ? (hi - lo + 63) / 64 : 0;   // k-blocks of its rows
                 ksum += kbl[i];
                 sum += mt[i];
@@ -1265,7 +1305,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     if (warp >= 4) {
         if (FP8) moe::reg_alloc<kRegsHigh>();
         epilogue<FP8, EPI, SWAP, WG>(S, p, total, tmem, rank);
-        if (!WG) zero_sentinel_rows<EPI>(p);
+        if (!WG && EPI != EPI_SUM) zero_sentinel_rows<EPI>(p);
         if (SWAP && EPI == EPI_STORE && p.fc) fused_combine_empty_tokens(p);
     } else {
         if (FP8) moe::reg_dealloc<kRegsLow>();
@@ -1304,8 +1344,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-bool encode(CUtensorMap* map, bool fp8, const void* base, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides_bytes, const cuuint32_t* box) {
+}  // namespace
+
+bool moe::encode_tile_map(CUtensorMap* map, bool fp8, const void* base, int rank, const cuuint64_t* dims,
+                          const cuuint64_t* strides_bytes, const cuuint32_t* box) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
@@ -1315,11 +1357,15 @@ bool encode(CUtensorMap* map, bool fp8, const void* base, int rank, const cuuint
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 [rows, K] (dims/strides as for encode) with boxes of 64 x 8(j + 1) rows.
+namespace {
+
+using moe::encode_tile_map;
+
+// bf16 [rows, K] (dims/strides as for encode_tile_map) with boxes of 64 x 8(j + 1) rows.
 bool encode_token_maps(TokenMaps* t, const void* base, const cuuint64_t* dims, const cuuint64_t* strides) {
     for (int j = 0; j < kTokenMaps; ++j) {
         const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(8 * (j + 1))};
-        if (!encode(&t->m[j], false, base, 2, dims, strides, box)) return false;
+        if (!encode_tile_map(&t->m[j], false, base, 2, dims, strides, box)) return false;
     }
     return true;
 }
@@ -1430,7 +1476,7 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(gx ? T : M_cap)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * esz};
         const cuuint32_t box[2] = {bk, gx ? 1u : static_cast<cuuint32_t>(BM)};
-        if (!swap && !encode(&tmA, fp8, A, 2, dims, strides, box)) return MOE_ERR_CUDA;
+        if (!swap && !encode_tile_map(&tmA, fp8, A, 2, dims, strides, box)) return MOE_ERR_CUDA;
         if (swap && !encode_token_maps(&tmX, A, dims, strides)) return MOE_ERR_CUDA;
     }
     if (weights_mn) {
@@ -1439,17 +1485,17 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
         const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(E)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(N) * 2, static_cast<cuuint64_t>(K) * N * 2};
         const cuuint32_t box[3] = {64, 64, 1};
-        if (!encode(&tmB, false, B, 3, dims, strides, box)) return MOE_ERR_CUDA;
+        if (!encode_tile_map(&tmB, false, B, 3, dims, strides, box)) return MOE_ERR_CUDA;
         tmA = tmB;   // the M = 128 tiles load one of these boxes per CTA; tmA is only prefetched
     } else if (!swiglu) {
         const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(E)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K) * esz, static_cast<cuuint64_t>(N) * K * esz};
         const cuuint32_t box[3] = {bk, swap ? 128u : BN, 1};   // swapped: 128 weight rows per CTA
-        if (!encode(&tmB, fp8, B, 3, dims, strides, box)) return MOE_ERR_CUDA;
+        if (!encode_tile_map(&tmB, fp8, B, 3, dims, strides, box)) return MOE_ERR_CUDA;
         // swapped: tmA holds the same weights in boxes of 64 rows, for the
         // M = 128 tile at the end of an expert's features
         const cuuint32_t box64[3] = {bk, 64u, 1};
-        if (swap && !encode(&tmA, fp8, B, 3, dims, strides, box64)) return MOE_ERR_CUDA;
+        if (swap && !encode_tile_map(&tmA, fp8, B, 3, dims, strides, box64)) return MOE_ERR_CUDA;
     } else if (swap) {
         // [E, N/2/8, 2, 8, K] in memory order (expert, group of 8 features,
         // gate/up, feature in group, k): one box holds 8 groups of 8 gate rows
@@ -1459,10 +1505,10 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
         const cuuint64_t strides[4] = {static_cast<cuuint64_t>(K) * esz, static_cast<cuuint64_t>(half) * K * esz,
                                        static_cast<cuuint64_t>(8) * K * esz, static_cast<cuuint64_t>(N) * K * esz};
         const cuuint32_t box[5] = {bk, 8, 2, 8, 1};
-        if (!encode(&tmB, fp8, B, 5, dims, strides, box)) return MOE_ERR_CUDA;
+        if (!encode_tile_map(&tmB, fp8, B, 5, dims, strides, box)) return MOE_ERR_CUDA;
         // tmA: 4 groups (32 features, 64 rows) per box, for the M = 128 tile
         const cuuint32_t box4[5] = {bk, 8, 2, 4, 1};
-        if (!encode(&tmA, fp8, B, 5, dims, strides, box4)) return MOE_ERR_CUDA;
+        if (!encode_tile_map(&tmA, fp8, B, 5, dims, strides, box4)) return MOE_ERR_CUDA;
     } else {
         // [E, 2, N/2, K]: a gate box clips at N/2 instead of running into the up rows
         const cuuint64_t dims[4] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(half), 2,
@@ -1470,10 +1516,10 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
         const cuuint64_t strides[3] = {static_cast<cuuint64_t>(K) * esz, static_cast<cuuint64_t>(half) * K * esz,
                                        static_cast<cuuint64_t>(N) * K * esz};
         const cuuint32_t box[4] = {bk, BN / 2, 1u, 1};
-        if (!encode(&tmB, fp8, B, 4, dims, strides, box)) return MOE_ERR_CUDA;
+        if (!encode_tile_map(&tmB, fp8, B, 4, dims, strides, box)) return MOE_ERR_CUDA;
     }
 
-    Params p;
+    Params p{};
     p.offsets = offsets;
     p.a_scales = A_scales;
     p.b_scales = B_scales;
@@ -1537,21 +1583,74 @@ moe_status_t moe::dgrad_gemm(const void* dC, const void* B, const int32_t* offse
                             MOE_EPI_STORE, dA, nullptr, reinterpret_cast<moe_stream_t>(s), true);
 }
 
+moe_status_t moe::dgrad_sum_gemm(const void* dC, int ldc, const void* B, const int32_t* offsets, int M, int N, int K,
+                                 float* sum, bool first, bool last, const float* row_scale, void* dA,
+                                 cudaStream_t s) {
+    MOE_CHECK_ARG(dC && B && offsets && M >= 1 && N >= 1 && ldc >= N && ldc % 8 == 0 && K >= 8 && K % 8 == 0);
+    MOE_CHECK_ARG((sum || (first && last)) && (dA || !last));
+    MOE_CHECK_ARG(moe::aligned16(dC) && moe::aligned16(B) && moe::aligned16(sum) && moe::aligned16(dA));
+    int* err = moe::device_error_word();
+    const int pairs = moe::sm_count() / 2;
+    if (!err || pairs <= 0) return MOE_ERR_CUDA;
+    TokenMaps tmX{};
+    {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldc) * 2};
+        if (!encode_token_maps(&tmX, dC, dims, strides)) return MOE_ERR_CUDA;
+    }
+    CUtensorMap tmB;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N), 1};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K) * 2, static_cast<cuuint64_t>(N) * K * 2};
+    const cuuint32_t box[3] = {64, 64, 1};
+    if (!encode_tile_map(&tmB, false, B, 3, dims, strides, box)) return MOE_ERR_CUDA;
+    Params p{};
+    p.offsets = offsets;
+    p.out = dA;
+    p.err = err;
+    p.E = 1;
+    p.M_cap = M;
+    p.N = p.out_cols = K;
+    p.K = N;
+    p.n_tiles = (K + kSwapFeatStore - 1) / kSwapFeatStore;
+    p.k_blocks = (N + 63) / 64;
+    p.topk = 1;
+    p.mn_a = 1;
+    p.sum = sum;
+    p.sum_first = first;
+    p.sum_last = last;
+    p.row_scale = row_scale;
+    // Token tiles of at most BT rows, as many as make the rounds over the CTA
+    // pairs times the tile's height smallest: with one expert a tile too many
+    // costs a whole round (4096 x 2880: 16 tiles of 256 rows take 3 rounds,
+    // 19 of 216 rows as many).
+    const int least = (M + BT - 1) / BT;
+    int64_t best = INT64_MAX;
+    for (int mt = least; mt <= least + pairs && (mt - least) * 16 <= M; ++mt) {
+        const int ts = ((M + mt - 1) / mt + 15) & ~15;
+        const int used = (M + ts - 1) / ts;   // tiles that have rows
+        if (used != mt) continue;
+        const int64_t cost = static_cast<int64_t>((static_cast<int64_t>(mt) * p.n_tiles + pairs - 1) / pairs) * (ts + 32);
+        if (cost < best) { best = cost; p.token_tiles = mt; }
+    }
+    if (!p.token_tiles) p.token_tiles = least;
+    return launch<false, EPI_SUM, true>(tmB, tmB, tmX, p, s);
+}
+
 moe_status_t moe::swiglu_keep_gemm(const void* x, const void* W1, const int32_t* offsets, int E, int M_cap, int N,
                                    int K, void* Y1, void* h, cudaStream_t s) {
     return run_grouped_gemm(MOE_BF16, x, nullptr, nullptr, nullptr, 0, 0, W1, nullptr, offsets, E, M_cap, N, K,
                             MOE_EPI_SWIGLU, h, nullptr, reinterpret_cast<moe_stream_t>(s), false, nullptr, Y1);
 }
 
-moe_status_t moe::wgrad_gemm(const void* dC, const void* A, const void* tails, const int32_t* offsets, int E,
-                             int M_cap, int N, int K, void* dB, cudaStream_t s) {
+moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, const void* tails, const int32_t* offsets,
+                             int E, int M_cap, int N, int K, void* dB, cudaStream_t s) {
     // dB[e] [N, K] = dC_e^T A_e over expert e's rows.  Swapped operands on CTA
     // pairs: A supplies the MMA's M rows (the output features, 256 per pair
     // tile), dC its N columns (the output rows, in tiles of up to 256); both
     // are read MN-major, 64 features x 64 rows per box, from their own rows or,
     // for an expert's partial last k-block, from the zero-padded tails.
-    MOE_CHECK_ARG(dC && A && tails && offsets && dB && E >= 1 && E <= kMaxE && M_cap >= 1);
-    MOE_CHECK_ARG(N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0);
+    MOE_CHECK_ARG(dC && A && (tails || E == 1) && offsets && dB && E >= 1 && E <= kMaxE && M_cap >= 1);
+    MOE_CHECK_ARG(N >= 1 && ldc >= N && ldc % 8 == 0 && K >= 8 && K % 8 == 0);
     MOE_CHECK_ARG(moe::aligned16(dC) && moe::aligned16(A) && moe::aligned16(tails) && moe::aligned16(dB));
     MOE_CHECK_ARG(static_cast<int64_t>(E) * N < INT_MAX);
     const int n_tiles = (K + kSwapFeatStore - 1) / kSwapFeatStore;
@@ -1561,14 +1660,18 @@ moe_status_t moe::wgrad_gemm(const void* dC, const void* A, const void* tails, c
     TokenMaps tmX{};
     const cuuint32_t box[2] = {64, 64};
     const uint8_t* tail_c = static_cast<const uint8_t*>(tails);
-    const uint8_t* tail_a = tail_c + static_cast<size_t>(64) * E * N * 2;
-    const struct { const void* base; int cols; cuuint64_t rows; } ops[4] = {
-        {A, K, static_cast<cuuint64_t>(M_cap)}, {dC, N, static_cast<cuuint64_t>(M_cap)},
-        {tail_a, K, static_cast<cuuint64_t>(64) * E}, {tail_c, N, static_cast<cuuint64_t>(64) * E}};
+    const uint8_t* tail_a = tails ? tail_c + static_cast<size_t>(64) * E * N * 2 : nullptr;
+    const struct { const void* base; int cols, ld; cuuint64_t rows; } ops[4] = {
+        {A, K, K, static_cast<cuuint64_t>(M_cap)}, {dC, N, ldc, static_cast<cuuint64_t>(M_cap)},
+        {tail_a, K, K, static_cast<cuuint64_t>(64) * E}, {tail_c, N, N, static_cast<cuuint64_t>(64) * E}};
     for (int i = 0; i < kWgMaps; ++i) {
+        if (!tails && i >= kWgTailA) {   // never loaded
+            tmX.m[i] = tmX.m[kWgA];
+            continue;
+        }
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(ops[i].cols), ops[i].rows};
-        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ops[i].cols) * 2};
-        if (!encode(&tmX.m[i], false, ops[i].base, 2, dims, strides, box)) return MOE_ERR_CUDA;
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ops[i].ld) * 2};
+        if (!encode_tile_map(&tmX.m[i], false, ops[i].base, 2, dims, strides, box)) return MOE_ERR_CUDA;
     }
     Params p{};
     p.offsets = offsets;
@@ -1585,6 +1688,7 @@ moe_status_t moe::wgrad_gemm(const void* dC, const void* A, const void* tails, c
     p.nb_scale = 0;
     p.topk = 1;
     p.wg_rows = N;
+    p.no_tails = tails ? 0 : 1;
     return launch<false, EPI_STORE, true, true>(tmX.m[kWgA], tmX.m[kWgC], tmX, p, s);
 }
 

@@ -1,6 +1,7 @@
 // Declarations shared between translation units of libmoe.so (not exported).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "moe.h"
@@ -17,13 +18,30 @@ moe_status_t dgrad_gemm(const void* dC, const void* B, const int32_t* offsets, i
 // Launches the grouped GEMM's weight-gradient kernel on CTA pairs (grouped_gemm.cu):
 //   dB[e, n, c] = sum over expert e's rows p of dC[p, n] * A[p, c]
 // with dC bf16 [M_cap, N] and A bf16 [M_cap, K] read in place (MN-major), in
-// 64-row k-blocks from offsets[e].  An expert's last, partial k-block
+// 64-row k-blocks from offsets[e]; rows of dC start ldc elements apart.  An expert's last, partial k-block
 // (cnt_e mod 64 rows, cnt_e = offsets[e + 1] - offsets[e]) comes instead from
 // rows [64e, 64e + 64) of the tails, zero-padded copies of those rows:
 // dC's bf16 [64E, N] followed by A's bf16 [64E, K].  dB bf16 [E, N, K]; an
-// expert without rows gets zeros.
-moe_status_t wgrad_gemm(const void* dC, const void* A, const void* tails, const int32_t* offsets, int E,
+// expert without rows gets zeros.  tails NULL: a single expert of exactly M_cap
+// rows, whose last k-block reads zeros from outside the tensor maps.
+moe_status_t wgrad_gemm(const void* dC, int ldc, const void* A, const void* tails, const int32_t* offsets, int E,
                         int M_cap, int N, int K, void* dB, cudaStream_t stream);
+
+// The data gradient of one expert of M rows, its contraction split over
+// several launches (grouped_gemm.cu): with C[p, c] = sum_n dC[p, n] B[n, c]
+// over this launch's N rows of B, the first launch sets sum [M, K] fp32 = C, the
+// others add to it, and the last one stores dA[p, c] = row_scale[p] * (sum + C)
+// as bf16 instead (row_scale NULL: 1; sum may be NULL if one launch is both).
+// dC bf16 [M, N], rows ldc elements apart; B bf16 [N, K]; offsets {0, M}.
+moe_status_t dgrad_sum_gemm(const void* dC, int ldc, const void* B, const int32_t* offsets, int M, int N, int K,
+                            float* sum, bool first, bool last, const float* row_scale, void* dA,
+                            cudaStream_t stream);
+
+// A tensor map for tiles staged with the 128-byte swizzle, zeros outside
+// (grouped_gemm.cu): bytes for FP8, else bf16; dims and box innermost first,
+// strides in bytes from the second dimension on.  False on failure.
+bool encode_tile_map(CUtensorMap* map, bool fp8, const void* base, int rank, const cuuint64_t* dims,
+                     const cuuint64_t* strides_bytes, const cuuint32_t* box);
 
 // Launches the bf16 gate_up GEMM with SwiGLU that also keeps its
 // pre-activations (grouped_gemm.cu): Y1 = [gate | up] bf16 [M_cap, N] rounded

@@ -1,0 +1,590 @@
+// Softmax cross entropy of T tokens against a vocabulary matrix, without the
+// logits ever being stored: the loss behind the layer when a model with it is
+// trained or its text is scored.
+//
+//   z[t, v] = sum_c x[t, c] W[v, c],   lse[t] = log sum_v exp z[t, v],
+//   loss[t] = lse[t] - z[t, label[t]]
+//   G[t, v] = exp(z[t, v] - lse[t]) - [v = label[t]]
+//   dx[t] = dloss[t] sum_v G[t, v] W[v],   dW[v] = sum_t G[t, v] dloss[t] x[t]
+//
+// Forward: the logits kernel below computes z tile by tile in tensor memory
+// and reduces each tile to a running maximum and sum of exponentials a row;
+// a second, small kernel joins the vocabulary tiles' pairs (m, s):
+//   M = max m,  lse = M + log sum s exp(m - M).
+// 2 T H V operations, W read once: bound by the tensor pipe for many tokens
+// and by reading W for few.
+//
+// Backward, a piece of the vocabulary at a time (6 T H V operations, as the
+// logits are computed again): the logits kernel writes the piece's G in bf16,
+// the grouped GEMM's data gradient adds G W to dx in fp32, and its weight
+// gradient computes the piece's rows of dW.  G's entries are probabilities and
+// label entries near -1, each rounded by at most a relative 2^-8,
+// independently; dloss stays out of G, so that the label entries, which carry
+// most of the gradient, are not all off by the same rounding of dloss: it
+// multiplies dx in fp32 and, for dW, x (rounded to bf16 once).
+//
+// The logits kernel: CTA pairs (clusters of two), tcgen05 cta_group::2 MMAs of
+// 256 tokens (128 per CTA) x up to 256 vocabulary rows (half staged by each
+// CTA) x 64 columns a stage, seven stages, accumulators double-buffered in
+// tensor memory.  A lane of tensor memory is a token, so a row's maximum and
+// sum run along a thread's own columns.  Tiles are walked vocabulary-major
+// with the token tiles inside, so the pairs that run together read the same
+// rows of W, once from HBM, while x stays in L2.  The tile's width in
+// vocabulary rows is 256 or, where the tiles do not fill whole rounds of the
+// pairs, the smallest multiple of 16 that takes as many rounds.
+//
+// Roles in a CTA (384 threads): warp 0 loads (TMA), warp 1 of the even CTA
+// issues the MMAs, warps 4-11 are the epilogue (warp w: lanes 32 (w % 4)..,
+// half (w - 4) / 4 of the columns).  Every wait is bounded; on expiry the CTA
+// records MOE_DEVERR_TIMEOUT, waits for its loads and MMAs and leaves.
+#include <climits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace {
+
+constexpr int kStages = 7;
+constexpr int kStageA = 128 * 128;   // 128 tokens x 64 bf16
+constexpr int kStageB = 128 * 128;   // up to 128 vocabulary rows x 64 bf16
+constexpr int kStageBytes = kStageA + kStageB;
+constexpr int BT = 256, BV = 256;    // tokens and vocabulary rows of a pair's tile
+constexpr int kEpiThreads = 256;
+constexpr int kThreads = 128 + kEpiThreads;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 100000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+    const int32_t* labels;
+    int* err;
+    int T, k_blocks;
+    int v0, cols;         // the launch's vocabulary rows: [v0, v0 + cols)
+    int bv;               // vocabulary rows of a tile (multiple of 16, <= BV)
+    int tok_tiles, voc_tiles;
+    int ignore;
+    // forward
+    float2* part;         // [2 * voc_tiles, T]: maximum and sum of each half tile
+    float* at_label;      // [T]: the label's logit
+    // backward
+    const float* lse;
+    __nv_bfloat16* G;     // [T, ldg]; columns from cols on are never read
+    int ldg;
+};
+
+struct alignas(16) Shared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+
+__device__ __forceinline__ uint32_t bar(uint64_t& b) { return moe::smem_u32(&b); }
+
+__device__ __forceinline__ void fail(Shared& S, const Params& p) {
+    S.abort_flag = 1;
+    moe::raise_device_error(p.err, MOE_DEVERR_TIMEOUT);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ void producer(const CUtensorMap* tmX, const CUtensorMap* tmW, uint8_t* stages, Shared& S, const Params& p,
+                         int total, uint32_t rank) {
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_par = 0;
+    bool ok = true;
+    const int half = p.bv / 2;
+    for (int t = blockIdx.x >> 1; ok && t < total; t += gridDim.x >> 1) {
+        const int row = (t % p.tok_tiles) * BT + static_cast<int>(rank) * 128;
+        const int voc = p.v0 + (t / p.tok_tiles) * p.bv + static_cast<int>(rank) * half;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+            const bool got = moe::mbar_wait(bar(S.empty[stage]), phase ^ 1u, &S.abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            const uint32_t fb = moe::map_to_cta(bar(S.full[stage]), 0);
+            const uint32_t sa = moe::smem_u32(stages + stage * kStageBytes);
+            if (moe::elect_one()) {
+                if (rank == 0) moe::mbar_arrive_expect_tx(bar(S.full[stage]), 2 * (kStageA + half * 128));
+                moe::tma_load_2d_pair(sa, tmX, fb, kb * 64, row);
+                moe::tma_load_2d_pair(sa + kStageA, tmW, fb, kb * 64, voc);
+            }
+            __syncwarp();
+            issued |= 1u << stage;
+            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+            if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+    }
+    if (!ok && moe::elect_one()) {
+        fail(S, p);
+        int zero = 0;
+        if (rank == 0) {
+            for (int s = 0; s < kStages; ++s)
+                if ((issued >> s) & 1u) moe::mbar_wait(bar(S.full[s]), (issued_par >> s) & 1u, &zero, kDrainNs);
+        } else {
+            // the peer's loads complete on the leader's barrier: give them time to land
+            const uint64_t t0 = moe::global_timer_ns();
+            while (moe::global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+        }
+    }
+    __syncwarp();
+}
+
+__device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int total, uint32_t tmem) {
+    const uint32_t idesc = moe::make_idesc(1u, BT, p.bv);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true, issued = false;
+    for (int t = blockIdx.x >> 1; ok && t < total; t += gridDim.x >> 1) {
+        bool got = moe::mbar_wait_cluster(bar(S.acc_empty[acc]), acc_phase ^ 1u, &S.abort_flag, kWaitNs);
+        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        moe::tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * BV);
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+            got = moe::mbar_wait(bar(S.full[stage]), phase, &S.abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+            moe::tc_fence_after();
+            const uint32_t sa = moe::smem_u32(stages + stage * kStageBytes);
+            const uint64_t adesc = moe::smem_desc_sw128(sa), bdesc = moe::smem_desc_sw128(sa + kStageA);
+            if (moe::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    moe::mma_bf16_pair(d, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | k) != 0);
+                moe::tc_commit_pair(bar(S.empty[stage]), 0x3);
+            }
+            __syncwarp();
+            issued = true;
+            if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if (moe::elect_one()) moe::tc_commit_pair(bar(S.acc_full[acc]), 0x3);
+        __syncwarp();
+        acc ^= 1;
+        if (!acc) acc_phase ^= 1u;
+    }
+    if (!ok && moe::elect_one()) fail(S, p);
+    __syncwarp();
+    if (issued) {   // every MMA has finished before tensor memory is freed
+        int zero = 0;
+        if (moe::elect_one()) moe::tc_commit_pair(bar(S.mma_done), 0x1);
+        __syncwarp();
+        moe::mbar_wait(bar(S.mma_done), 0, &zero, kDrainNs);
+    }
+}
+
+template <bool BACK>
+__device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, uint32_t rank) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q = warp & 3, hsel = (warp - 4) >> 2;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    const uint32_t leader[2] = {moe::map_to_cta(bar(S.acc_empty[0]), 0), moe::map_to_cta(bar(S.acc_empty[1]), 0)};
+    const int chunks = (p.bv + 31) / 32, c_lo = hsel ? (chunks + 1) / 2 : 0, c_hi = hsel ? chunks : (chunks + 1) / 2;
+    for (int t = blockIdx.x >> 1; t < total; t += gridDim.x >> 1) {
+        const int vt = t / p.tok_tiles;
+        const int row = (t % p.tok_tiles) * BT + static_cast<int>(rank) * 128 + q * 32 + lane;
+        const int col0 = vt * p.bv;                          // first column of the tile within the launch's
+        const int ncols = min(p.bv, p.cols - col0);          // those that exist
+        const int label = row < p.T ? p.labels[row] : p.ignore;
+        const int rel = label - p.v0 - col0;                 // the label's column, in the tile if 0 <= rel < ncols
+        const bool counts = label != p.ignore && label >= 0;
+        float neg_lse = 0.0f;
+        if (BACK && row < p.T) neg_lse = -p.lse[row] * kLog2e;
+        if (!moe::mbar_wait(bar(S.acc_full[acc]), acc_phase, &S.abort_flag, kWaitNs)) { fail(S, p); return; }
+        moe::tc_fence_after();
+        const uint32_t ta = lane_base + static_cast<uint32_t>(acc * BV);
+        float m = -INFINITY, s = 0.0f;
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi; ++c) {
+            const int col = c * 32;
+            uint32_t u[32];
+            moe::tmem_ld32(ta + col, u);
+            moe::tmem_ld_wait();
+            float z[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(u[j]);
+            if (!BACK) {
+                if (counts && rel >= col && rel < min(col + 32, ncols))
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (rel == col + j) p.at_label[row] = z[j];
+                if (col + 32 > ncols)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col + j >= ncols) z[j] = -INFINITY;
+                float cm = z[0];
+#pragma unroll
+                for (int j = 1; j < 32; ++j) cm = fmaxf(cm, z[j]);
+                const float nm = fmaxf(m, cm);
+                // a piece without any column, or of -inf alone, adds nothing
+                const float base = nm == -INFINITY ? 0.0f : nm * kLog2e;
+                s *= exp2_approx(fmaf(m, kLog2e, -base));
+                m = nm;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s += exp2_approx(fmaf(z[j], kLog2e, -base));
+            } else {
+                float g[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) g[j] = exp2_approx(fmaf(z[j], kLog2e, neg_lse));
+                if (counts && rel >= col && rel < min(col + 32, ncols))
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (rel == col + j) g[j] -= 1.0f;
+                if (!counts || col + 32 > ncols)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!counts || col + j >= ncols) g[j] = 0.0f;
+                if (row < p.T) {
+                    uint4* o = reinterpret_cast<uint4*>(p.G + static_cast<int64_t>(row) * p.ldg + col0 + col);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (col + 8 * i < p.bv && col0 + col + 8 * i < p.ldg)
+                            o[i] = make_uint4(moe::pack_bf16x2(g[8 * i], g[8 * i + 1]),
+                                              moe::pack_bf16x2(g[8 * i + 2], g[8 * i + 3]),
+                                              moe::pack_bf16x2(g[8 * i + 4], g[8 * i + 5]),
+                                              moe::pack_bf16x2(g[8 * i + 6], g[8 * i + 7]));
+                }
+            }
+        }
+        moe::tc_fence_before();
+        if (rank != 0) moe::mbar_arrive_cluster(leader[acc]);
+        else moe::mbar_arrive(bar(S.acc_empty[acc]));
+        acc ^= 1;
+        if (!acc) acc_phase ^= 1u;
+        if (!BACK && row < p.T) p.part[static_cast<int64_t>(2 * vt + hsel) * p.T + row] = make_float2(m, s);
+    }
+}
+
+template <bool BACK>
+__global__ void __launch_bounds__(kThreads, 1)
+logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p) {
+    const uint32_t rank = moe::cluster_ctarank();   // 0 leads the pair
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared& S = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            moe::mbar_init(bar(S.full[s]), 1);
+            moe::mbar_init(bar(S.empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            moe::mbar_init(bar(S.acc_full[a]), 1);
+            moe::mbar_init(bar(S.acc_empty[a]), 2 * kEpiThreads);
+        }
+        moe::mbar_init(bar(S.mma_done), 1);
+        S.abort_flag = 0;
+        moe::fence_barrier_init();
+        moe::prefetch_tensormap(&tmX);
+        moe::prefetch_tensormap(&tmW);
+    }
+    __syncthreads();
+    if (warp == 1) {
+        moe::tmem_alloc_pair(moe::smem_u32(&S.tmem_base), kTmemCols);
+        moe::tmem_relinquish_pair();
+    }
+    moe::tc_fence_before();
+    moe::cluster_sync();   // the peer's barriers exist before anyone signals them
+    moe::tc_fence_after();
+    const uint32_t tmem = S.tmem_base;
+    const int total = p.tok_tiles * p.voc_tiles;
+    if (warp >= 4) epilogue<BACK>(S, p, total, tmem, rank);
+    else if (warp == 0) producer(&tmX, &tmW, stages, S, p, total, rank);
+    else if (warp == 1 && rank == 0) mma_issuer(stages, S, p, total, tmem);
+    moe::tc_fence_before();
+    moe::cluster_sync();   // no CTA of the pair leaves while its peer may still signal it
+    if (warp == 1) {
+        moe::tc_fence_after();
+        moe::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// Joins the vocabulary tiles' (m, s): eight tokens a block, 32 threads each,
+// whose shares are merged in thread order.  An ignored or invalid label gets
+// loss 0 (the latter is reported).
+constexpr int kJoinTokens = 8;
+__global__ void __launch_bounds__(256)
+join_kernel(const float2* __restrict__ part, int parts, const float* __restrict__ at_label,
+            const int32_t* __restrict__ labels, int T, int V, int ignore, float* __restrict__ loss,
+            float* __restrict__ lse, int* err) {
+    __shared__ float2 share[32][kJoinTokens];
+    const int tok = threadIdx.x % kJoinTokens, g = threadIdx.x / kJoinTokens;
+    const int t = blockIdx.x * kJoinTokens + tok;
+    float m = -INFINITY, s = 0.0f;
+    if (t < T) {
+#pragma unroll 4
+        for (int i = g; i < parts; i += 32) {
+            const float2 v = part[static_cast<int64_t>(i) * T + t];
+            const float nm = fmaxf(m, v.x), base = nm == -INFINITY ? 0.0f : nm;
+            s = s * expf(m - base) + v.y * expf(v.x - base);
+            m = nm;
+        }
+    }
+    share[g][tok] = make_float2(m, s);
+    __syncthreads();
+    if (g != 0 || t >= T) return;
+    for (int i = 1; i < 32; ++i) {
+        const float2 v = share[i][tok];
+        const float nm = fmaxf(m, v.x), base = nm == -INFINITY ? 0.0f : nm;
+        s = s * expf(m - base) + v.y * expf(v.x - base);
+        m = nm;
+    }
+    const float l = m + logf(s);
+    const int label = labels[t];
+    float out = 0.0f;
+    if (label != ignore) {
+        if (label >= 0 && label < V) out = l - at_label[t];
+        else moe::raise_device_error(err, MOE_DEVERR_LABEL);
+    }
+    loss[t] = out;
+    lse[t] = l;
+}
+
+// Backward's per-token factors: scale[t] = dloss[t] (0 where the label is
+// ignored or invalid), xs[t] = bf16(scale[t] * x[t]); offsets = {0, T}.
+__global__ void __launch_bounds__(256)
+scale_rows_kernel(const uint4* __restrict__ x, const float* __restrict__ dloss, const int32_t* __restrict__ labels,
+                  int T, int V, int row_vecs, int ignore, float* __restrict__ scale, uint4* __restrict__ xs,
+                  int32_t* __restrict__ offsets, int* err) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        offsets[0] = 0;
+        offsets[1] = T;
+    }
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const int label = labels[t];
+    const bool counts = label != ignore && label >= 0 && label < V;
+    const float d = counts ? dloss[t] : 0.0f;
+    if (lane == 0) {
+        scale[t] = d;
+        if (!counts && label != ignore) moe::raise_device_error(err, MOE_DEVERR_LABEL);
+    }
+    for (int c = lane; c < row_vecs; c += 32) {
+        const uint4 v = __ldg(x + static_cast<int64_t>(t) * row_vecs + c);
+        const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = counts ? moe::pack_bf16x2(d * moe::bf16_lo(a[i]), d * moe::bf16_hi(a[i])) : 0u;
+        xs[static_cast<int64_t>(t) * row_vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+bool valid_sizes(int T, int H, int V) {
+    return T >= 1 && V >= 1 && H >= 8 && H % 8 == 0 && V <= INT_MAX - BV && T <= INT_MAX - BT &&
+           (static_cast<int64_t>(T) / BT + 1) * (static_cast<int64_t>(V) / 16 + 1) < INT_MAX;
+}
+
+// Vocabulary rows of a tile for `cols` of them and `tok_tiles` token tiles.
+int tile_width(int cols, int tok_tiles) {
+    const int pairs = moe::sm_count() / 2 > 0 ? moe::sm_count() / 2 : 76;
+    const auto rounds = [&](int bv) {
+        return (static_cast<int64_t>((cols + bv - 1) / bv) * tok_tiles + pairs - 1) / pairs;
+    };
+    const int64_t least = rounds(BV);
+    int bv = BV;
+    while (bv > 32 && rounds(bv - 16) == least) bv -= 16;
+    return bv;
+}
+
+template <bool BACK>
+moe_status_t launch_logits(const void* x, const void* W, int H, int V, Params p, cudaStream_t s) {
+    CUtensorMap tmX, tmW;
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(H) * 2};
+    const cuuint64_t dx[2] = {static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(p.T)};
+    const cuuint64_t dw[2] = {static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(V)};
+    const cuuint32_t bx[2] = {64, 128}, bw[2] = {64, static_cast<cuuint32_t>(p.bv / 2)};
+    if (!moe::encode_tile_map(&tmX, false, x, 2, dx, stride, bx) ||
+        !moe::encode_tile_map(&tmW, false, W, 2, dw, stride, bw))
+        return MOE_ERR_CUDA;
+    auto kern = logits_kernel<BACK>;
+    static std::atomic<int> configured[moe::kMaxDevices];
+    int dev = 0;
+    MOE_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= moe::kMaxDevices) return MOE_ERR_CUDA;
+    if (!configured[dev].load(std::memory_order_relaxed)) {
+        MOE_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            static_cast<int>(kSmemBytes)));
+        configured[dev].store(1, std::memory_order_relaxed);
+    }
+    const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.voc_tiles;
+    int pairs = moe::sm_count() / 2;
+    if (pairs <= 0) return MOE_ERR_CUDA;
+    if (tiles < pairs) pairs = static_cast<int>(tiles);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tmX, tmW, p) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
+struct Carver {
+    size_t off = 0;
+    size_t take(size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) & ~static_cast<size_t>(255);
+        return at;
+    }
+};
+
+struct ForwardLayout {
+    int tok_tiles, bv, voc_tiles;
+    size_t part, at_label, total;
+};
+ForwardLayout forward_layout(int T, int V) {
+    ForwardLayout l{};
+    l.tok_tiles = (T + BT - 1) / BT;
+    l.bv = tile_width(V, l.tok_tiles);
+    l.voc_tiles = (V + l.bv - 1) / l.bv;
+    Carver c;
+    l.part = c.take(static_cast<size_t>(2) * l.voc_tiles * T * sizeof(float2));
+    l.at_label = c.take(static_cast<size_t>(T) * sizeof(float));
+    l.total = c.off;
+    return l;
+}
+
+// A piece's G takes about kPieceBytes, but a piece has at least kPieceMin
+// vocabulary rows: every piece but the last reads and writes dx's fp32 sum.
+constexpr int64_t kPieceBytes = 256ll << 20;
+constexpr int kPieceMin = 2048;
+
+struct BackwardLayout {
+    int piece, pieces, ldg;
+    size_t G, xs, scale, offsets, sum, total;
+};
+BackwardLayout backward_layout(int T, int H, int V) {
+    BackwardLayout l{};
+    int64_t piece = kPieceBytes / 2 / T / BV * BV;
+    if (piece < kPieceMin) piece = kPieceMin;
+    if (piece > V) piece = V;
+    l.pieces = static_cast<int>((V + piece - 1) / piece);
+    l.piece = l.pieces == 1 ? V : static_cast<int>(((V + l.pieces - 1) / l.pieces + BV - 1) / BV * BV);
+    l.pieces = (V + l.piece - 1) / l.piece;
+    l.ldg = (l.piece + 7) / 8 * 8;
+    Carver c;
+    l.G = c.take(static_cast<size_t>(T) * l.ldg * 2);
+    l.xs = c.take(static_cast<size_t>(T) * H * 2);
+    l.scale = c.take(static_cast<size_t>(T) * sizeof(float));
+    l.offsets = c.take(2 * sizeof(int32_t));
+    l.sum = c.take(l.pieces > 1 ? static_cast<size_t>(T) * H * sizeof(float) : 0);
+    l.total = c.off;
+    return l;
+}
+
+}  // namespace
+
+extern "C" size_t moe_cross_entropy_forward_workspace_size(int T, int H, int V) {
+    return valid_sizes(T, H, V) ? forward_layout(T, V).total : 0;
+}
+
+extern "C" moe_status_t moe_cross_entropy_forward(const void* x, const void* W, const int32_t* labels, int T, int H,
+                                                  int V, int ignore_index, float* loss, float* lse, void* ws,
+                                                  size_t ws_bytes, moe_stream_t stream) {
+    MOE_CHECK_ARG(x && W && labels && loss && lse && valid_sizes(T, H, V));
+    MOE_CHECK_ARG(moe::aligned16(x) && moe::aligned16(W) && moe::aligned16(labels) && moe::aligned16(loss) &&
+                  moe::aligned16(lse));
+    const ForwardLayout l = forward_layout(T, V);
+    if (!ws || ws_bytes < l.total) return MOE_ERR_WORKSPACE;
+    MOE_CHECK_ARG(moe::aligned16(ws));
+    int* err = moe::device_error_word();
+    if (!err) return MOE_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto* base = static_cast<uint8_t*>(ws);
+    Params p{};
+    p.labels = labels;
+    p.err = err;
+    p.T = T;
+    p.k_blocks = (H + 63) / 64;
+    p.cols = V;
+    p.bv = l.bv;
+    p.tok_tiles = l.tok_tiles;
+    p.voc_tiles = l.voc_tiles;
+    p.ignore = ignore_index;
+    p.part = reinterpret_cast<float2*>(base + l.part);
+    p.at_label = reinterpret_cast<float*>(base + l.at_label);
+    const moe_status_t st = launch_logits<false>(x, W, H, V, p, s);
+    if (st != MOE_OK) return st;
+    join_kernel<<<(T + kJoinTokens - 1) / kJoinTokens, 256, 0, s>>>(p.part, 2 * l.voc_tiles, p.at_label, labels, T, V,
+                                                                    ignore_index, loss, lse, err);
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+extern "C" size_t moe_cross_entropy_backward_workspace_size(int T, int H, int V) {
+    return valid_sizes(T, H, V) ? backward_layout(T, H, V).total : 0;
+}
+
+extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W, const int32_t* labels,
+                                                   const float* lse, const float* dloss, int T, int H, int V,
+                                                   int ignore_index, void* dx, void* dW, void* ws, size_t ws_bytes,
+                                                   moe_stream_t stream) {
+    MOE_CHECK_ARG(x && W && labels && lse && dloss && (dx || dW) && valid_sizes(T, H, V));
+    MOE_CHECK_ARG(moe::aligned16(x) && moe::aligned16(W) && moe::aligned16(labels) && moe::aligned16(lse) &&
+                  moe::aligned16(dloss) && moe::aligned16(dx) && moe::aligned16(dW));
+    const BackwardLayout l = backward_layout(T, H, V);
+    if (!ws || ws_bytes < l.total) return MOE_ERR_WORKSPACE;
+    MOE_CHECK_ARG(moe::aligned16(ws));
+    int* err = moe::device_error_word();
+    if (!err) return MOE_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto* base = static_cast<uint8_t*>(ws);
+    auto* G = reinterpret_cast<__nv_bfloat16*>(base + l.G);
+    void* xs = base + l.xs;
+    auto* scale = reinterpret_cast<float*>(base + l.scale);
+    auto* offsets = reinterpret_cast<int32_t*>(base + l.offsets);
+    auto* sum = l.pieces > 1 ? reinterpret_cast<float*>(base + l.sum) : nullptr;
+    scale_rows_kernel<<<(T + 7) / 8, 256, 0, s>>>(static_cast<const uint4*>(x), dloss, labels, T, V, H / 8,
+                                                  ignore_index, scale, static_cast<uint4*>(xs), offsets, err);
+    MOE_CHECK_LAUNCH();
+    for (int i = 0; i < l.pieces; ++i) {
+        Params p{};
+        p.labels = labels;
+        p.err = err;
+        p.T = T;
+        p.k_blocks = (H + 63) / 64;
+        p.v0 = i * l.piece;
+        p.cols = V - p.v0 < l.piece ? V - p.v0 : l.piece;
+        p.tok_tiles = (T + BT - 1) / BT;
+        p.bv = tile_width(p.cols, p.tok_tiles);
+        p.voc_tiles = (p.cols + p.bv - 1) / p.bv;
+        p.ignore = ignore_index;
+        p.lse = lse;
+        p.G = G;
+        p.ldg = l.ldg;
+        moe_status_t st = launch_logits<true>(x, W, H, V, p, s);
+        if (st != MOE_OK) return st;
+        const auto* Wp = static_cast<const __nv_bfloat16*>(W) + static_cast<int64_t>(p.v0) * H;
+        if (dx && (st = moe::dgrad_sum_gemm(G, l.ldg, Wp, offsets, T, p.cols, H, sum, i == 0, i == l.pieces - 1, scale,
+                                            dx, s)) != MOE_OK)
+            return st;
+        if (dW) {
+            auto* dWp = static_cast<__nv_bfloat16*>(dW) + static_cast<int64_t>(p.v0) * H;
+            st = moe::wgrad_gemm(G, l.ldg, xs, nullptr, offsets, 1, T, p.cols, H, dWp, s);
+            if (st != MOE_OK) return st;
+        }
+    }
+    return MOE_OK;
+}

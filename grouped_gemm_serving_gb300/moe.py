@@ -20,7 +20,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_DEVICE_CHECK, MOE_ERR_TIMEOUT = 4, 5, 6
 MOE_BF16, MOE_FP8_E4M3_B128, MOE_F32 = 0, 1, 2
 MOE_EPI_STORE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_QUANT_FP8 = 0, 1, 2
-MOE_DEVERR_NONE, MOE_DEVERR_OFFSETS, MOE_DEVERR_TIMEOUT, MOE_DEVERR_ROUTE = 0, 1, 2, 3
+MOE_DEVERR_NONE, MOE_DEVERR_OFFSETS, MOE_DEVERR_TIMEOUT, MOE_DEVERR_ROUTE, MOE_DEVERR_LABEL = 0, 1, 2, 3, 4
 MOE_FWD_HOST_IO = 1
 MOE_FWD_GATHER = 2
 MOE_FWD_FUSED_COMBINE = 4
@@ -76,6 +76,10 @@ _SIGS = {
     "moe_layer_norm_forward": (_S, [_I, _P, _L, _I, _I, _I, _P, _P, _F, _P, _L, _P, _P, _P]),
     "moe_layer_norm_backward_workspace_size": (_Z, [_I, _I]),
     "moe_layer_norm_backward": (_S, [_I, _P, _L, _P, _L, _I, _I, _I, _P, _P, _P, _P, _L, _P, _P, _P, _Z, _P]),
+    "moe_cross_entropy_forward_workspace_size": (_Z, [_I, _I, _I]),
+    "moe_cross_entropy_forward": (_S, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    "moe_cross_entropy_backward_workspace_size": (_Z, [_I, _I, _I]),
+    "moe_cross_entropy_backward": (_S, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
     "moe_swiglu": (_S, [_P, _P, _I, _I, _I, _P, _P]),
     "moe_combine": (_S, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_forward_workspace_size": (_Z, [C.POINTER(ForwardArgs)]),
@@ -286,6 +290,25 @@ def moe_layer_norm_backward(dtype, dy, lddy, x, ldx, rows, H, w_dtype, weight, m
     _check(lib().moe_layer_norm_backward(dtype, _p(dy), lddy, _p(x), ldx, rows, H, w_dtype, _p(weight), _p(mean),
                                          _p(rstd), _p(dx), lddx, _p(dweight), _p(dbias), _p(ws), ws_bytes,
                                          _stream(stream)), "moe_layer_norm_backward")
+
+
+def moe_cross_entropy_forward_workspace_size(T, H, V) -> int:
+    return lib().moe_cross_entropy_forward_workspace_size(T, H, V)
+
+
+def moe_cross_entropy_forward(x, W, labels, T, H, V, ignore_index, loss, lse, ws, ws_bytes, stream=None):
+    _check(lib().moe_cross_entropy_forward(_p(x), _p(W), _p(labels), T, H, V, ignore_index, _p(loss), _p(lse), _p(ws),
+                                           ws_bytes, _stream(stream)), "moe_cross_entropy_forward")
+
+
+def moe_cross_entropy_backward_workspace_size(T, H, V) -> int:
+    return lib().moe_cross_entropy_backward_workspace_size(T, H, V)
+
+
+def moe_cross_entropy_backward(x, W, labels, lse, dloss, T, H, V, ignore_index, dx, dW, ws, ws_bytes, stream=None):
+    _check(lib().moe_cross_entropy_backward(_p(x), _p(W), _p(labels), _p(lse), _p(dloss), T, H, V, ignore_index,
+                                            _p(dx), _p(dW), _p(ws), ws_bytes, _stream(stream)),
+           "moe_cross_entropy_backward")
 
 
 def moe_swiglu(Y1, offsets, E, M_cap, I, h, stream=None):

@@ -74,6 +74,7 @@ typedef enum {
 #define MOE_DEVERR_OFFSETS 1 /* offsets[0] != 0, decreasing, or offsets[E] > M_cap */
 #define MOE_DEVERR_TIMEOUT 2 /* an mbarrier wait inside a GEMM exceeded its time limit */
 #define MOE_DEVERR_ROUTE 3   /* an expert id outside [0, E] reached the sort */
+#define MOE_DEVERR_LABEL 4   /* a label outside [0, V) that is not ignore_index */
 
 typedef enum {
     MOE_BF16 = 0,          /* bf16 operands, fp32 accumulation */
@@ -463,6 +464,36 @@ moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, const void* dy, int64_t 
                                      int rows, int H, moe_dtype_t w_dtype, const void* weight, const float* mean,
                                      const float* rstd, void* dx, int64_t lddx, void* dweight, void* dbias,
                                      void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_cross_entropy_forward, moe_cross_entropy_backward -- softmax cross
+ * entropy of T tokens against a vocabulary matrix, without keeping the logits
+ * z[t, v] = sum_c x[t, c] * W[v, c] (bf16 operands, fp32 accumulation): the
+ * loss behind the layer.
+ * Forward:  lse[t] = log sum_v exp z[t, v];  loss[t] = lse[t] - z[t, labels[t]].
+ * Backward, from the gradient dloss[t] of loss[t] (for the mean over n tokens:
+ *   1/n each) and the forward call's lse:  with
+ *   G[t, v] = exp(z[t, v] - lse[t]) - [v == labels[t]],
+ *   dx[t] = dloss[t] * sum_v G[t, v] W[v],  dW[v] = sum_t G[t, v] dloss[t] x[t],
+ *   written (not accumulated).  Either of dx and dW may be NULL and is then
+ *   not computed.  The vocabulary is taken in pieces, so that the workspace
+ *   stays near 256 MiB plus three copies of x.
+ * A token whose label is ignore_index (any value, such as -100) has loss 0 and
+ * zero gradients, whatever its dloss; its lse is written.  A label outside
+ * [0, V) that is not ignore_index is recorded as MOE_DEVERR_LABEL and treated
+ * the same way.
+ * x, dx bf16 [T, H]; W, dW bf16 [V, H]; labels int32 [T]; loss, lse, dloss
+ * fp32 [T]; ws: the *_workspace_size bytes of the same T, H and V.
+ * Limits: T >= 1, V >= 1 (any, odd ones too), H a positive multiple of 8.
+ */
+size_t moe_cross_entropy_forward_workspace_size(int T, int H, int V);
+moe_status_t moe_cross_entropy_forward(const void* x, const void* W, const int32_t* labels, int T, int H, int V,
+                                       int ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                       moe_stream_t stream);
+size_t moe_cross_entropy_backward_workspace_size(int T, int H, int V);
+moe_status_t moe_cross_entropy_backward(const void* x, const void* W, const int32_t* labels, const float* lse,
+                                        const float* dloss, int T, int H, int V, int ignore_index, void* dx,
+                                        void* dW, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * moe_batched_matmul -- the batched expert backend ("Mixture of Experts in

@@ -23,6 +23,8 @@ FFN_BACK = (16, 16, 16, 16, 16, 16, 8, 64, 64, 64, 16, 16, 16, 16, 1 << 30, None
 COMBINE = (16, 16, 16, 16, 16, 4, 2, 64, 8, 16, 16, None)
 PERMUTE = (16, 16, 16, 4, 2, 64, 8, 16, None)
 ROUTE = (16, 16, 16, 4, 8, 2, 1, 16, None)
+XENT = (16, 16, 16, 4, 64, 500, -100, 16, 16, 16, 1 << 30, None)
+XENT_BACK = (16, 16, 16, 16, 16, 4, 64, 500, -100, 16, 16, 16, 1 << 30, None)
 
 
 def _with(args, **at):
@@ -67,6 +69,17 @@ def _with(args, **at):
     ("moe_route_backward", _with(ROUTE, _4=257)),
     ("moe_route_backward", _with(ROUTE, _5=9)),
     ("moe_route_backward", _with(ROUTE, _7=None)),
+    ("moe_cross_entropy_forward", _with(XENT, _1=None)),
+    ("moe_cross_entropy_forward", _with(XENT, _3=0)),
+    ("moe_cross_entropy_forward", _with(XENT, _4=60)),
+    ("moe_cross_entropy_forward", _with(XENT, _5=0)),
+    ("moe_cross_entropy_forward", _with(XENT, _5=2 ** 31 - 1)),
+    ("moe_cross_entropy_forward", _with(XENT, _8=24)),
+    ("moe_cross_entropy_forward", _with(XENT, _9=24)),
+    ("moe_cross_entropy_backward", _with(XENT_BACK, _3=None)),
+    ("moe_cross_entropy_backward", _with(XENT_BACK, _5=-1)),
+    ("moe_cross_entropy_backward", _with(XENT_BACK, _9=None, _10=None)),   # nothing wanted
+    ("moe_cross_entropy_backward", _with(XENT_BACK, _0=18)),
 ])
 def test_refused(moe, name, args):
     assert getattr(moe.lib(), name)(*args) == moe.MOE_ERR_INVALID_ARG
@@ -78,6 +91,10 @@ def test_refused(moe, name, args):
     ("moe_layer_norm_backward", _with(NORM_BACK, _16=64)),
     ("moe_ffn_backward", _with(FFN_BACK, _13=None)),
     ("moe_ffn_backward", _with(FFN_BACK, _14=1024)),
+    ("moe_cross_entropy_forward", _with(XENT, _9=None)),
+    ("moe_cross_entropy_forward", _with(XENT, _10=8)),
+    ("moe_cross_entropy_backward", _with(XENT_BACK, _11=None)),
+    ("moe_cross_entropy_backward", _with(XENT_BACK, _12=8)),
 ])
 def test_workspace_missing(moe, name, args):
     assert getattr(moe.lib(), name)(*args) == moe.MOE_ERR_WORKSPACE
@@ -89,3 +106,8 @@ def test_workspace_sizes(moe):
     assert moe.moe_ffn_backward_workspace_size(0, 64, 64, 64) == 0
     assert moe.moe_ffn_backward_workspace_size(8, 64, 64, 60) == 0
     assert moe.moe_ffn_backward_workspace_size(8, 64, 64, 64) >= 64 * 64 * 2 * 3   # dY1 and h
+    assert moe.moe_cross_entropy_forward_workspace_size(0, 64, 500) == 0
+    assert moe.moe_cross_entropy_backward_workspace_size(4, 60, 500) == 0
+    # one piece: the gradient of all logits in bf16; many tokens: pieces of at least 2048 vocabulary rows
+    assert moe.moe_cross_entropy_backward_workspace_size(64, 64, 512) >= 64 * 512 * 2 + 64 * 64 * 2
+    assert moe.moe_cross_entropy_backward_workspace_size(1 << 17, 64, 131072) < 1 << 30
