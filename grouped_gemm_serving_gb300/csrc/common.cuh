@@ -33,6 +33,31 @@ int sm_count();
 constexpr int kMaxDevices = 64;
 int resident_blocks(const void* kernel, int threads, size_t smem, std::atomic<int> (&cache)[kMaxDevices]);
 
+// Programmatic dependent launch of a small kernel behind the one before it:
+// launch_after() lets the kernel's blocks start once every block of the kernel
+// before it has called launch_dependents() or ended, and wait_for_primary()
+// then waits until that kernel has ended and its stores are visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+moe_status_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
 __device__ __forceinline__ void raise_device_error(int* err, int code) {
     atomicCAS(err, 0, code);
 }
@@ -105,6 +130,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
             if (global_timer_ns() - t0 > limit_ns) return false;
         }
     }
+}
+
+// Untiled bulk copy into shared memory (16-byte aligned addresses and size),
+// completion counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // TMA tile loads into shared memory, completion counted in bytes on `bar`.

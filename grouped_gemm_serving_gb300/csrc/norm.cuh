@@ -72,14 +72,45 @@ __device__ __forceinline__ void store_vec(T* p, const float* v) {
     }
 }
 
+// Pairs of fp32 values: one instruction works on both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Elements 2j and 2j + 1 of a vector.
+template <typename T, int VEC>
+__device__ __forceinline__ uint64_t get2(const Raw<T, VEC>& r, int j) {
+    return pair(get<T, VEC>(r, 2 * j), get<T, VEC>(r, 2 * j + 1));
+}
+
 // Sums of N values over a team, the same in every thread.  Teams of more than
 // a warp are whole blocks: `slots` holds 2 x N x 32 floats, and calls alternate
 // `turn` between its halves, so that one barrier a call is enough (a half is
 // written again only after every thread has passed the next call's barrier).
 template <int TEAM, int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], float* slots, int& turn) {
+    constexpr int kLanes = TEAM < 32 ? TEAM : 32;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
+    for (int off = kLanes / 2; off > 0; off >>= 1)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
     if constexpr (TEAM > 32) {
@@ -91,13 +122,47 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float* slots, int& turn)
 #pragma unroll
             for (int i = 0; i < N; ++i) s[i * 32 + warp] = v[i];
         __syncthreads();
+        // kWarps is a power of two: lanes repeat its values, so that the sum over
+        // kWarps neighbouring lanes is everybody's
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = lane < kWarps ? s[i * 32 + lane] : 0.0f;
+        for (int i = 0; i < N; ++i) v[i] = s[i * 32 + (lane & (kWarps - 1))];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
+        for (int off = kWarps / 2; off > 0; off >>= 1)
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
     }
+}
+
+// Both sums at once over a block of TEAM <= 512 threads, with half the
+// shuffles: the warp's halves trade one value each and carry on with the other.
+template <int TEAM>
+__device__ __forceinline__ void block_sum2(float& v0, float& v1, float* slots, int& turn) {
+    constexpr int kWarps = TEAM / 32;
+    static_assert(kWarps <= 16, "one slot a lane");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float a = lane < 16 ? v0 : v1;
+    a += __shfl_xor_sync(0xffffffffu, lane < 16 ? v1 : v0, 16);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+    float* s = slots + turn * 32;
+    turn ^= 1;
+    if ((lane & 15) == 0) s[lane + warp] = a;   // v0's sums at 0.., v1's at 16..
+    __syncthreads();
+    a = s[(lane & 16) + (lane & (kWarps - 1))];
+#pragma unroll
+    for (int off = kWarps / 2; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+    v0 = __shfl_sync(0xffffffffu, a, 0);
+    v1 = __shfl_sync(0xffffffffu, a, 16);
+}
+
+// A weight vector of ones, for calls without weights.
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> ones() {
+    static_assert(VEC > 1, "vectors");
+    Raw<T, VEC> r;
+#pragma unroll
+    for (int i = 0; i < Raw<T, VEC>::kWords; ++i) r.w[i] = sizeof(T) == 4 ? 0x3F800000u : 0x3F803F80u;
+    return r;
 }
 
 constexpr int kWide = 1024;        // threads of a row that no team holds in registers

@@ -8,6 +8,11 @@
 // dweight and dbias in fp32 registers as it goes.  Each block then writes one
 // partial row of each to the workspace, and a second small kernel adds the
 // partial rows in block order: no atomics, the same bits every time.
+//
+// Wide rows that start on 16-byte boundaries come through shared memory: one
+// thread keeps a ring of rows in flight with bulk copies (TMA), so that the
+// loads of the next rows run under the present row's sums and barrier without
+// taking registers.  All others are loaded straight into registers.
 #include <climits>
 
 #include "norm.cuh"
@@ -16,18 +21,34 @@ namespace {
 
 using namespace moe::norm;
 
+// Adds a thread's columns to the block's partial row of dweight and dbias.
+template <int VEC, int TEAM, int EPT>
+__device__ __forceinline__ void store_partial(float* pw, int H, int lane, const float (&dw)[EPT],
+                                              const float (&db)[EPT]) {
+#pragma unroll
+    for (int i = 0; i < EPT / VEC; ++i) {
+        const int c = (i * TEAM + lane) * VEC;
+        if (c < H)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                pw[c + j] = dw[i * VEC + j];
+                pw[H + c + j] = db[i * VEC + j];
+            }
+    }
+}
+
 template <typename T, typename W, int VEC, int TEAM, int EPT>
-__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM)
+__global__ void __launch_bounds__(TEAM <= 32 ? 256 : TEAM)
 norm_backward_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, int rows, int H,
                      const W* __restrict__ weight, const float* __restrict__ mean_in,
                      const float* __restrict__ rstd_in, T* dx, int64_t lddx,
                      float* __restrict__ partial) {
     constexpr int NV = EPT / VEC;
-    constexpr int kTeams = TEAM == 32 ? 8 : 1;
-    __shared__ float slots[TEAM == 32 ? 1 : 128];
-    const int lane = TEAM == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int team = TEAM == 32 ? threadIdx.x >> 5 : 0;
+    constexpr int kTeams = TEAM <= 32 ? 256 / TEAM : 1;
+    __shared__ float slots[TEAM <= 32 ? 1 : 128];
+    const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
     const float inv_h = 1.0f / static_cast<float>(H);
+    const int step = gridDim.x * kTeams;
     int turn = 0;
     Raw<W, VEC> w[NV];
     float dw[EPT], db[EPT];
@@ -38,21 +59,35 @@ norm_backward_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, int row
     }
 #pragma unroll
     for (int i = 0; i < EPT; ++i) dw[i] = db[i] = 0.0f;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + team; row < rows; row += gridDim.x * kTeams) {
-        Raw<T, VEC> xr[NV], gr[NV];
+    Raw<T, VEC> xn[NV], gn[NV];
+    float mean_n = 0.0f, rstd_n = 0.0f;
+    const auto fetch = [&](int64_t row) {   // the next row's loads run under the present row's sums
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TEAM + lane) * VEC;
             if (c < H) {
-                xr[i] = load_raw<T, VEC>(x + row * ldx + c);
-                gr[i] = load_raw<T, VEC>(dy + row * lddy + c);
+                xn[i] = load_raw<T, VEC>(x + row * ldx + c);
+                gn[i] = load_raw<T, VEC>(dy + row * lddy + c);
             }
         }
-        const float mean = mean_in[row], rstd = rstd_in[row];
+        mean_n = mean_in[row];
+        rstd_n = rstd_in[row];
+    };
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kTeams;   // the block's first row of a step
+    if (row0 + team < rows) fetch(row0 + team);
+    // teams of a warp or less share its shuffles: the trip count is the block's
+    for (int64_t at = row0; at < rows; at += step) {
+        const int64_t row = at + team;
+        const bool live = row < rows;
+        Raw<T, VEC> xr[NV], gr[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) { xr[i] = xn[i]; gr[i] = gn[i]; }
+        const float mean = mean_n, rstd = rstd_n;
+        if (row + step < rows) fetch(row + step);
         float s[2] = {0.0f, 0.0f};   // sum of g, sum of g * xh
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if ((i * TEAM + lane) * VEC < H)
+            if (live && (i * TEAM + lane) * VEC < H)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     const float d = get<T, VEC>(gr[i], j), xh = (get<T, VEC>(xr[i], j) - mean) * rstd;
@@ -65,7 +100,7 @@ norm_backward_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, int row
         }
         team_sum<TEAM, 2>(s, slots, turn);
         const float c0 = s[0] * inv_h, c1 = s[1] * inv_h;
-        if (dx) {
+        if (dx && live) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * TEAM + lane) * VEC;
@@ -83,10 +118,11 @@ norm_backward_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, int row
         }
     }
     if (!partial) return;
+    moe::launch_dependents();
     float* pw = partial + static_cast<int64_t>(blockIdx.x) * 2 * H;
-    if constexpr (TEAM == 32) {
-        // the block's eight warps add their columns in warp order
-        __shared__ float sum[2 * 32 * EPT];
+    if constexpr (TEAM <= 32) {
+        // the block's teams add their columns in team order
+        __shared__ float sum[2 * TEAM * EPT];
         for (int t = 0; t < kTeams; ++t) {
             if (team == t)
 #pragma unroll
@@ -95,25 +131,159 @@ norm_backward_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, int row
                     for (int j = 0; j < VEC; ++j) {
                         const int c = (i * TEAM + lane) * VEC + j;
                         sum[c] = (t ? sum[c] : 0.0f) + dw[i * VEC + j];
-                        sum[32 * EPT + c] = (t ? sum[32 * EPT + c] : 0.0f) + db[i * VEC + j];
+                        sum[TEAM * EPT + c] = (t ? sum[TEAM * EPT + c] : 0.0f) + db[i * VEC + j];
                     }
             __syncthreads();
         }
         for (int c = threadIdx.x; c < H; c += 256) {
             pw[c] = sum[c];
-            pw[H + c] = sum[32 * EPT + c];
+            pw[H + c] = sum[TEAM * EPT + c];
         }
     } else {
+        store_partial<VEC, TEAM, EPT>(pw, H, lane, dw, db);
+    }
+}
+
+// 16384 x 7168 bf16 rows with fp32 weights: 0.127 ms, 5.6 TB/s of the three
+// tensors (0.82 of the measured copy bandwidth); 0.215 ms with the loads in
+// registers, and 0.162 ms with 1024 threads of 8 elements, whose sums over the
+// row took as many instructions as the rest.
+//
+// The same for rows of 16-byte vectors, one block per row at a time, through a
+// ring of `depth` rows of x and dy in shared memory.  A stage is read into
+// registers before the row's barrier (in team_sum), so after that barrier
+// thread 0 can fill it again.  At two bytes an element the arithmetic is as
+// long as the memory traffic: it runs on pairs of elements, with xh and g held
+// from the sums to dx.
+constexpr int kMaxDepth = 8;
+constexpr size_t kRingBytes = 208 * 1024;
+
+template <typename T, typename W, int TEAM, int EPT, int BLOCKS>
+__global__ void __launch_bounds__(TEAM, BLOCKS)
+norm_backward_ring_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, int rows, int H,
+                          const W* __restrict__ weight, const float* __restrict__ mean_in,
+                          const float* __restrict__ rstd_in, T* dx, int64_t lddx, float* __restrict__ partial,
+                          int depth, int* err) {
+    constexpr int VEC = Elem<T>::kVec, NV = EPT / VEC;
+    constexpr bool kHold = EPT <= 16;   // xh and g stay in registers; else they are computed again
+    extern __shared__ __align__(128) uint8_t ring[];   // depth x (x row, dy row)
+    __shared__ uint64_t full[kMaxDepth];
+    __shared__ float slots[64];
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x;
+    const uint32_t row_bytes = static_cast<uint32_t>(H) * sizeof(T);
+    const float inv_h = 1.0f / static_cast<float>(H);
+    int turn = 0;
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int d = 0; d < depth; ++d) moe::mbar_init(moe::smem_u32(&full[d]), 1);
+        moe::fence_barrier_init();
+    }
+    __syncthreads();
+    const auto fill = [&](int stage, int64_t row) {
+        const uint32_t dst = moe::smem_u32(ring) + stage * 2 * row_bytes, b = moe::smem_u32(&full[stage]);
+        moe::mbar_arrive_expect_tx(b, 2 * row_bytes);
+        moe::bulk_load(dst, x + row * ldx, row_bytes, b);
+        moe::bulk_load(dst + row_bytes, dy + row * lddy, row_bytes, b);
+    };
+    if (tid == 0)
+        for (int d = 0; d < depth; ++d) {
+            const int64_t row = blockIdx.x + static_cast<int64_t>(d) * gridDim.x;
+            if (row < rows) fill(d, row);
+        }
+    Raw<W, VEC> w[NV];
+    uint64_t dw[EPT / 2], db[EPT / 2];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TEAM + tid) * VEC;
+        w[i] = c < H && weight ? load_raw<W, VEC>(weight + c) : ones<W, VEC>();
+    }
+#pragma unroll
+    for (int i = 0; i < EPT / 2; ++i) dw[i] = db[i] = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    // a row's mean and rstd are fetched a row ahead
+    float mean_n = mean_in[blockIdx.x], rstd_n = rstd_in[blockIdx.x];
+    const int step = gridDim.x;
+    for (int row = blockIdx.x; row < rows; row += step) {
+        const float rstd = rstd_n;
+        const uint64_t neg_mean = pair(-mean_n, -mean_n), rstd2 = pair(rstd, rstd);
+        if (rows - row > step) {
+            mean_n = mean_in[row + step];
+            rstd_n = rstd_in[row + step];
+        }
+        if (!moe::mbar_wait(moe::smem_u32(&full[stage]), phase, &abort_flag, 2000000000ull)) {
+            abort_flag = 1;   // the rows that follow are not waited for as long
+            moe::raise_device_error(err, MOE_DEVERR_TIMEOUT);
+        }
+        const T* xs = reinterpret_cast<const T*>(ring + static_cast<size_t>(stage) * 2 * row_bytes);
+        const T* gs = xs + H;
+        Raw<T, VEC> xr[NV], gr[NV];
+        uint64_t xh[kHold ? EPT / 2 : 1], g[kHold ? EPT / 2 : 1];
+        uint64_t s0 = 0, s1 = 0;   // sum of g, sum of g * xh
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TEAM + lane) * VEC;
-            if (c < H)
+            const int c = (i * TEAM + tid) * VEC;
+            if (c < H) {
+                xr[i] = load_raw<T, VEC>(xs + c);
+                gr[i] = load_raw<T, VEC>(gs + c);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    pw[c + j] = dw[i * VEC + j];
-                    pw[H + c + j] = db[i * VEC + j];
+                for (int j = 0; j < VEC / 2; ++j) {
+                    const int e = i * (VEC / 2) + j;
+                    const uint64_t d = get2<T, VEC>(gr[i], j);
+                    const uint64_t xe = mul2(add2(get2<T, VEC>(xr[i], j), neg_mean), rstd2);
+                    const uint64_t ge = mul2(d, get2<W, VEC>(w[i], j));
+                    s0 = add2(s0, ge);
+                    s1 = fma2(ge, xe, s1);
+                    dw[e] = fma2(d, xe, dw[e]);
+                    db[e] = add2(db[e], d);
+                    if (kHold) {
+                        xh[kHold ? e : 0] = xe;
+                        g[kHold ? e : 0] = ge;
+                    }
                 }
+            }
         }
+        float s[2], hi;
+        split(s0, s[0], hi);
+        s[0] += hi;
+        split(s1, s[1], hi);
+        s[1] += hi;
+        block_sum2<TEAM>(s[0], s[1], slots, turn);
+        if (tid == 0 && row + static_cast<int64_t>(depth) * step < rows)
+            fill(stage, row + static_cast<int64_t>(depth) * step);
+        if (++stage == depth) { stage = 0; phase ^= 1u; }
+        if (dx) {
+            const float c0 = -s[0] * inv_h, c1 = -s[1] * inv_h;
+            T* dx_row = dx + static_cast<int64_t>(row) * lddx;
+            const uint64_t c02 = pair(c0, c0), c12 = pair(c1, c1);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TEAM + tid) * VEC;
+                if (c < H) {
+                    float o[VEC];
+#pragma unroll
+                    for (int j = 0; j < VEC / 2; ++j) {
+                        const int e = kHold ? i * (VEC / 2) + j : 0;
+                        const uint64_t d = get2<T, VEC>(gr[i], j);
+                        const uint64_t xe = kHold ? xh[e] : mul2(add2(get2<T, VEC>(xr[i], j), neg_mean), rstd2);
+                        const uint64_t ge = kHold ? g[e] : mul2(d, get2<W, VEC>(w[i], j));
+                        split(mul2(fma2(xe, c12, add2(ge, c02)), rstd2), o[2 * j], o[2 * j + 1]);
+                    }
+                    store_vec<T, VEC>(dx_row + c, o);
+                }
+            }
+        }
+    }
+    moe::launch_dependents();
+    if (partial) {
+        float a[EPT], b[EPT];
+#pragma unroll
+        for (int i = 0; i < EPT / 2; ++i) {
+            split(dw[i], a[2 * i], a[2 * i + 1]);
+            split(db[i], b[2 * i], b[2 * i + 1]);
+        }
+        store_partial<VEC, TEAM, EPT>(partial + static_cast<int64_t>(blockIdx.x) * 2 * H, H, tid, a, b);
     }
 }
 
@@ -153,14 +323,16 @@ norm_backward_wide_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, in
     }
 }
 
-// out[c] = sum of the blocks' partial rows, block order within each of eight
-// interleaved shares, then the shares in order.  blockIdx.y: 0 dweight, 1 dbias.
+// out[c] = sum of the blocks' partial rows, in order within each of 32
+// interleaved shares, then over the shares.  blockIdx.y: 0 dweight, 1 dbias.
+constexpr int kShares = 32;
 template <typename W>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kShares)
 norm_reduce_kernel(const float* __restrict__ partial, int blocks, int H, W* __restrict__ dweight,
                    W* __restrict__ dbias) {
-    __shared__ float share[8][32];
+    __shared__ float share[kShares][33];
     W* out = blockIdx.y == 0 ? dweight : dbias;
+    moe::wait_for_primary();   // this grid may start while the blocks' last stores are under way
     if (!out) return;
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
@@ -168,24 +340,26 @@ norm_reduce_kernel(const float* __restrict__ partial, int blocks, int H, W* __re
     if (c < H) {
         const float* p = partial + static_cast<int64_t>(blockIdx.y) * H + c;
 #pragma unroll 8
-        for (int b = part; b < blocks; b += 8) s += p[static_cast<int64_t>(b) * 2 * H];
+        for (int b = part; b < blocks; b += kShares) s += p[static_cast<int64_t>(b) * 2 * H];
     }
     share[part][lane] = s;
     __syncthreads();
-    if (part == 0 && c < H) {
-        float v = share[0][lane];
+    // warp i: column i of the block, one share a lane
+    float v = share[lane][part];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) v += share[i][lane];
-        store_vec<W, 1>(out + c, &v);
-    }
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == 0 && blockIdx.x * 32 + part < H) store_vec<W, 1>(out + blockIdx.x * 32 + part, &v);
 }
 
-// Blocks whose partial rows the workspace has room for.
+// Blocks of a launch, each of which writes a partial row: as many as the GPU
+// holds, but (past one an SM) with at least four rows each.
 int partial_rows(int rows, int H) {
     const int sm = moe::sm_count() > 0 ? moe::sm_count() : 152;
-    const int64_t teams = H <= 1024 ? (static_cast<int64_t>(rows) + 7) / 8 : rows;
-    const int64_t cap = static_cast<int64_t>(sm) * (H <= 1024 ? 4 : 2);
-    return static_cast<int>(teams < cap ? teams : cap);
+    const int per_sm = H <= 1024 ? 8 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1;
+    const int64_t most = static_cast<int64_t>(sm) * per_sm;
+    int64_t n = rows / 4 > sm ? rows / 4 : sm;
+    if (n > most) n = most;
+    return static_cast<int>(n < rows ? n : rows);
 }
 
 struct Args {
@@ -195,32 +369,70 @@ struct Args {
     const float *mean, *rstd;
     void* dx;
     float* partial;   // NULL: neither dweight nor dbias is wanted
+    int* err;
     cudaStream_t stream;
 };
 
 template <typename T, typename W, int VEC, int TEAM, int EPT>
 int launch(const Args& a) {   // the blocks launched, 0 on failure
     auto kern = norm_backward_kernel<T, W, VEC, TEAM, EPT>;
-    constexpr int kThreads = TEAM == 32 ? 256 : TEAM;
+    constexpr int kThreads = TEAM <= 32 ? 256 : TEAM, kTeams = TEAM <= 32 ? 256 / TEAM : 1;
     static std::atomic<int> resident[moe::kMaxDevices];
     int grid = moe::resident_blocks(reinterpret_cast<const void*>(kern), kThreads, 0, resident);
     if (grid <= 0) return 0;
-    const int room = partial_rows(a.rows, a.H);
+    const int room = partial_rows(a.rows, a.H), need = (a.rows + kTeams - 1) / kTeams;
     if (room < grid) grid = room;
+    if (need < grid) grid = need;
     kern<<<grid, kThreads, 0, a.stream>>>(
         static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x), a.ldx, a.rows, a.H,
         static_cast<const W*>(a.weight), a.mean, a.rstd, static_cast<T*>(a.dx), a.lddx, a.partial);
     return grid;
 }
 
+template <typename T, typename W, int TEAM, int EPT, int BLOCKS>
+int launch_ring(const Args& a) {
+    auto kern = norm_backward_ring_kernel<T, W, TEAM, EPT, BLOCKS>;
+    constexpr size_t kBytes = kRingBytes / BLOCKS;
+    static std::atomic<int> configured[moe::kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= moe::kMaxDevices) return 0;
+    if (!configured[dev].load(std::memory_order_relaxed)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBytes)) != cudaSuccess) return 0;
+        configured[dev].store(1, std::memory_order_relaxed);
+    }
+    const size_t stage = static_cast<size_t>(a.H) * sizeof(T) * 2;
+    int depth = static_cast<int>(kBytes / stage);
+    if (depth > kMaxDepth) depth = kMaxDepth;
+    const int grid = partial_rows(a.rows, a.H);
+    kern<<<grid, TEAM, depth * stage, a.stream>>>(
+        static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x), a.ldx, a.rows, a.H,
+        static_cast<const W*>(a.weight), a.mean, a.rstd, static_cast<T*>(a.dx), a.lddx, a.partial, depth, a.err);
+    return grid;
+}
+
+// Rows of vectors go through the ring from 257 elements on: 16 a thread, 512
+// threads an SM.  Narrower ones, and rows that are no vectors, do not.
+template <typename T, typename W>
+int pick_ring(const Args& a) {
+    if (a.H <= 64 * 16) return launch_ring<T, W, 64, 16, 8>(a);
+    if (a.H <= 128 * 16) return launch_ring<T, W, 128, 16, 4>(a);
+    if (a.H <= 256 * 16) return launch_ring<T, W, 256, 16, 2>(a);
+    if (a.H <= 512 * 16) return launch_ring<T, W, 512, 16, 1>(a);
+    return launch_ring<T, W, 512, 32, 1>(a);
+}
 template <typename T, typename W, int VEC>
 int pick(const Args& a) {
+    if (a.H <= 8 * 8) return launch<T, W, VEC, 8, 8>(a);
     if (a.H <= 32 * 8) return launch<T, W, VEC, 32, 8>(a);
-    if (a.H <= 32 * 32) return launch<T, W, VEC, 32, 32>(a);
-    if (a.H <= 128 * 16) return launch<T, W, VEC, 128, 16>(a);
-    if (a.H <= 256 * 16) return launch<T, W, VEC, 256, 16>(a);
-    if (a.H <= 512 * 16) return launch<T, W, VEC, 512, 16>(a);
-    return launch<T, W, VEC, 512, 32>(a);
+    if constexpr (VEC == 1) {
+        if (a.H <= 128 * 8) return launch<T, W, VEC, 128, 8>(a);
+        if (a.H <= 256 * 8) return launch<T, W, VEC, 256, 8>(a);
+        if (a.H <= 512 * 8) return launch<T, W, VEC, 512, 8>(a);
+        if (a.H <= 512 * 16) return launch<T, W, VEC, 512, 16>(a);   // 4099 bf16: 0.29 ms, 0.38 as 1024 x 8
+        return launch<T, W, VEC, 1024, 16>(a);                       // 12289 bf16: 0.6 ms, 1.2 as 512 x 32
+    } else {
+        return pick_ring<T, W>(a);
+    }
 }
 
 template <typename T, typename W>
@@ -240,9 +452,9 @@ moe_status_t run(const Args& a, void* dweight, void* dbias) {
     }
     MOE_CHECK_LAUNCH();
     if (a.partial) {
-        norm_reduce_kernel<W><<<dim3((a.H + 31) / 32, 2), 256, 0, a.stream>>>(
-            a.partial, blocks, a.H, static_cast<W*>(dweight), static_cast<W*>(dbias));
-        MOE_CHECK_LAUNCH();
+        return moe::launch_after(norm_reduce_kernel<W>, dim3((a.H + 31) / 32, 2), 32 * kShares, a.stream,
+                                 static_cast<const float*>(a.partial), blocks, a.H, static_cast<W*>(dweight),
+                                 static_cast<W*>(dbias));
     }
     return MOE_OK;
 }
@@ -271,8 +483,10 @@ extern "C" moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, const void* d
         if (!ws || ws_bytes < moe_layer_norm_backward_workspace_size(rows, H)) return MOE_ERR_WORKSPACE;
         MOE_CHECK_ARG(moe::aligned16(ws));
     }
-    const Args a{dy, x, weight, lddy, ldx, lddx, rows, H, mean, rstd, dx, sums ? static_cast<float*>(ws) : nullptr,
-                 reinterpret_cast<cudaStream_t>(stream)};
+    int* err = moe::device_error_word();
+    if (!err) return MOE_ERR_CUDA;
+    const Args a{dy, x, weight, lddy, ldx, dx ? lddx : 0, rows, H, mean, rstd, dx,
+                 sums ? static_cast<float*>(ws) : nullptr, err, reinterpret_cast<cudaStream_t>(stream)};
     if (dtype == MOE_F32) return run<float, float>(a, dweight, dbias);
     if (w_dtype == MOE_F32) return run<__nv_bfloat16, float>(a, dweight, dbias);
     return run<__nv_bfloat16, __nv_bfloat16>(a, dweight, dbias);

@@ -15,15 +15,14 @@ namespace {
 using namespace moe::norm;
 
 template <typename T, typename W, int VEC, int TEAM, int EPT>
-__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM)
+__global__ void __launch_bounds__(TEAM <= 32 ? 256 : TEAM)
 norm_forward_kernel(const T* x, int64_t ldx, int rows, int H, const W* __restrict__ weight,
                     const W* __restrict__ bias, float eps, T* y, int64_t ldy,
                     float* __restrict__ mean_out, float* __restrict__ rstd_out) {
     constexpr int NV = EPT / VEC;
-    constexpr int kTeams = TEAM == 32 ? 8 : 1;   // rows in flight in a block
-    __shared__ float slots[TEAM == 32 ? 1 : 64];
-    const int lane = TEAM == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int team = TEAM == 32 ? threadIdx.x >> 5 : 0;
+    constexpr int kTeams = TEAM <= 32 ? 256 / TEAM : 1;   // rows in flight in a block
+    __shared__ float slots[TEAM <= 32 ? 1 : 64];
+    const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
     const int step = gridDim.x * kTeams;
     const float inv_h = 1.0f / static_cast<float>(H);
     int turn = 0;
@@ -35,16 +34,18 @@ norm_forward_kernel(const T* x, int64_t ldx, int rows, int H, const W* __restric
         if (c < H && bias) b[i] = load_raw<W, VEC>(bias + c);
     }
     Raw<T, VEC> cur[NV], next[NV];
-    int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + team;
-    if (row < rows) {
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kTeams;   // the block's first row of a step
+    if (row0 + team < rows) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TEAM + lane) * VEC;
-            if (c < H) next[i] = load_raw<T, VEC>(x + row * ldx + c);
+            if (c < H) next[i] = load_raw<T, VEC>(x + (row0 + team) * ldx + c);
         }
     }
-    // a team's threads leave together: the trip count is the same for all of them
-    for (; row < rows; row += step) {
+    // teams of a warp or less share its shuffles: the trip count is the block's
+    for (int64_t at = row0; at < rows; at += step) {
+        const int64_t row = at + team;
+        const bool live = row < rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) cur[i] = next[i];
         if (row + step < rows) {
@@ -57,7 +58,7 @@ norm_forward_kernel(const T* x, int64_t ldx, int rows, int H, const W* __restric
         float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if ((i * TEAM + lane) * VEC < H)
+            if (live && (i * TEAM + lane) * VEC < H)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) s[0] += get<T, VEC>(cur[i], j);
         team_sum<TEAM, 1>(s, slots, turn);
@@ -65,7 +66,7 @@ norm_forward_kernel(const T* x, int64_t ldx, int rows, int H, const W* __restric
         float q[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if ((i * TEAM + lane) * VEC < H)
+            if (live && (i * TEAM + lane) * VEC < H)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     const float d = get<T, VEC>(cur[i], j) - mean;
@@ -76,7 +77,7 @@ norm_forward_kernel(const T* x, int64_t ldx, int rows, int H, const W* __restric
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TEAM + lane) * VEC;
-            if (c < H) {
+            if (live && c < H) {
                 float o[VEC];
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
@@ -86,7 +87,7 @@ norm_forward_kernel(const T* x, int64_t ldx, int rows, int H, const W* __restric
                 store_vec<T, VEC>(y + row * ldy + c, o);
             }
         }
-        if (lane == 0) {
+        if (live && lane == 0) {
             if (mean_out) mean_out[row] = mean;
             if (rstd_out) rstd_out[row] = rstd;
         }
@@ -140,7 +141,7 @@ struct Args {
 template <typename T, typename W, int VEC, int TEAM, int EPT>
 moe_status_t launch(const Args& a) {
     auto kern = norm_forward_kernel<T, W, VEC, TEAM, EPT>;
-    constexpr int kThreads = TEAM == 32 ? 256 : TEAM, kTeams = TEAM == 32 ? 8 : 1;
+    constexpr int kThreads = TEAM <= 32 ? 256 : TEAM, kTeams = TEAM <= 32 ? 256 / TEAM : 1;
     static std::atomic<int> resident[moe::kMaxDevices];
     const int grid = moe::resident_blocks(reinterpret_cast<const void*>(kern), kThreads, 0, resident);
     if (grid <= 0) return MOE_ERR_CUDA;
@@ -154,6 +155,7 @@ moe_status_t launch(const Args& a) {
 
 template <typename T, typename W, int VEC>
 moe_status_t pick(const Args& a) {
+    if (a.H <= 8 * 8) return launch<T, W, VEC, 8, 8>(a);
     if (a.H <= 32 * 8) return launch<T, W, VEC, 32, 8>(a);
     if (a.H <= 32 * 32) return launch<T, W, VEC, 32, 32>(a);
     if (a.H <= 128 * 16) return launch<T, W, VEC, 128, 16>(a);

@@ -130,8 +130,15 @@ def _p(t):
     return t.data_ptr()
 
 
+# The current stream's handle without the Stream object that
+# torch.cuda.current_stream() builds around it (0.1 us instead of 2.9 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
