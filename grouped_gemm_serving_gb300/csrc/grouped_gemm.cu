@@ -160,12 +160,15 @@ struct Params {
     int nfb;
     void* cout;   // out bf16 [T, out_cols]
     void* keep;   // EPI_SWIGLU_KEEP: the pre-activations, bf16 [M_cap, N]
-    // EPI_SUM: with C this launch's product, the first launch sets
-    // sum [M_cap, N] = C, the others add to it, and the last one stores
-    // out = row_scale[row] * (sum + C) instead (row_scale NULL: 1)
+    // EPI_SUM: the contraction is cut into `splits` ranges of k-blocks, each a
+    // tile of its own.  With C a range's product, the first launch sets
+    // sum[range] [M_cap, N] = C and the others add to it; with a single range
+    // the last launch stores out = row_scale[row] * (sum + C) instead.
+    // Weight gradient with EPI_SUM: out = row_scale[0] * C.
     float* sum;
     int sum_first, sum_last;
     const float* row_scale;
+    int splits;
     int token_tiles;   // > 0: token tiles of every expert (else one per BT rows)
     int no_tails;      // weight gradient: rows past the last expert's lie outside the tensor maps (zeros)
 };
@@ -224,16 +227,23 @@ struct Tile {
     // store), runs as an M = 128 pair MMA (64 weight rows per CTA)
     bool half;
     int nkb;    // the tile's k-blocks
+    int kb0;    // EPI_SUM: its first k-block
+    int split;  // EPI_SUM: its range of the contraction
     int first;  // weight gradient: the expert's first row
 };
 
 // Weight gradient: every expert has the same wg_pair_mt(p) token tiles.
 __device__ __forceinline__ int wg_pair_mt(const Params& p) { return (p.wg_rows + BT - 1) / BT; }
 
-template <bool SWAP, bool WG = false>
+template <bool SWAP, bool WG = false, bool SUM = false>
 __device__ __forceinline__ Tile decode_tile(int t, const Shared& S, const Params& p) {
     static_assert(!WG || SWAP, "the weight gradient runs on CTA pairs");
-    int lo = 0, mt, local;
+    int lo = 0, mt, local, split = 0;
+    if (SUM) {   // range-major: the tiles of a range run together
+        const int per = S.prefix[p.E] * p.n_tiles;
+        split = t / per;
+        t -= split * per;
+    }
     if (WG) {
         // every expert has mt x n_tiles tiles; S.prefix is its k-block prefix
         mt = wg_pair_mt(p);
@@ -253,6 +263,12 @@ __device__ __forceinline__ Tile decode_tile(int t, const Shared& S, const Params
     ti.row_end = p.offsets[lo + 1];
     ti.first = 0;
     ti.nkb = p.k_blocks;
+    ti.kb0 = 0;
+    ti.split = split;
+    if (SUM) {
+        ti.kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * split / p.splits);
+        ti.nkb = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (split + 1) / p.splits) - ti.kb0;
+    }
     ti.half = false;
     if (WG) {
         // weight gradient on a pair: the tokens are the wg_rows output rows
@@ -415,14 +431,14 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
     uint32_t phase = 0, issued = 0, issued_par = 0;
     bool ok = true;
     for (int t = tile_first<true>(); ok && t < total; t += tile_step<true>()) {
-        const Tile ti = decode_tile<true, WG>(t, S, p);
+        const Tile ti = decode_tile<true, WG, EPI == EPI_SUM && !WG>(t, S, p);
         const int nh = swap_n(ti) / 2;                 // token rows in each CTA: 8 .. 128
         const CUtensorMap* tmXh = &tmX->m[nh / 8 - 1];
         const int xrow = ti.row0 + static_cast<int>(rank) * nh;
         // weight gradient: this CTA's nh columns of dC in one or two 64-wide boxes
         const int xbytes = WG ? (nh > 64 ? 2 : 1) * 8192 : nh * 128;
         const int abytes = ti.half ? kStageA / 2 : kStageA;   // M = 128: 64 weight rows per CTA
-        const int nkb = WG ? ti.nkb : p.k_blocks;
+        const int nkb = WG || EPI == EPI_SUM ? ti.nkb : p.k_blocks;
         const int nfull = WG ? (p.offsets[ti.e + 1] - ti.first + (p.no_tails ? 63 : 0)) / 64 : 0;   // k-blocks read in place
         for (int kb = 0; kb < nkb; ++kb) {
             const bool got = moe::mbar_wait(bar(S.empty[stage]), phase ^ 1u, &S.abort_flag, kWaitNs);
@@ -433,7 +449,7 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
             const uint32_t fb = moe::map_to_cta(bar(S.full[stage]), 0);
             const uint32_t sa = moe::smem_u32(stages + stage * Geo<true, EPI>::kStageBytes);
             const uint32_t sb = sa + kStageA;
-            const int kc = kb * 64;
+            const int kc = (EPI == EPI_SUM && !WG ? ti.kb0 + kb : kb) * 64;
             if (moe::elect_one()) {
                 if (rank == 0) moe::mbar_arrive_expect_tx(bar(S.full[stage]), 2 * (abytes + xbytes));
                 if (WG) {
@@ -595,7 +611,7 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
     bool ok = true, issued = false;
     for (int t = tile_first<SWAP>(); ok && t < total; t += tile_step<SWAP>()) {
         if (SWAP) {
-            const Tile ti = decode_tile<true, WG>(t, S, p);
+            const Tile ti = decode_tile<true, WG, EPI == EPI_SUM && !WG>(t, S, p);
             const int n = swap_n(ti);
             const int m = ti.half ? BM : 2 * BM;
             idesc = WG ? moe::make_idesc_ab_mn(1u, 2 * BM, n)
@@ -610,7 +626,8 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
         }
         // weight-gradient tiles of an expert without rows have no k-blocks:
         // the accumulator is committed untouched and the epilogue writes zeros
-        const int nkb = WG ? decode_tile<SWAP, WG>(t, S, p).nkb : p.k_blocks;
+        constexpr bool kSum = EPI == EPI_SUM && !WG;
+        const int nkb = WG || kSum ? decode_tile<SWAP, WG, kSum>(t, S, p).nkb : p.k_blocks;
         for (int kb = 0; kb < nkb; ++kb) {
             if (FP8) {
                 const bool got = moe::mbar_wait(bar(S.acc_empty[acc]), acc_phase ^ 1u, &S.abort_flag, kWaitNs);
@@ -800,9 +817,10 @@ __device__ void fused_combine_empty_tokens(const Params& p) {
 
 // EPI_SUM: a lane's n tokens of feature f.  The sum's reads are all issued
 // before the first is used.
-__device__ __forceinline__ void sum_chunk(const Params& p, int64_t row, int f, int n, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void sum_chunk(const Params& p, int split, int64_t row, int f, int n,
+                                          const uint32_t (&v)[32]) {
     if (f >= p.out_cols) return;
-    float* acc = p.sum + row * p.out_cols + f;
+    float* acc = p.sum + (static_cast<int64_t>(split) * p.M_cap + row) * p.out_cols + f;
     float c[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -840,7 +858,7 @@ __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti,
         moe::tmem_ld32(ta + col, v);
         moe::tmem_ld_wait();
         if (EPI == EPI_SUM) {
-            sum_chunk(p, ti.row0 + tok0 + col, f, jmax, v);
+            sum_chunk(p, ti.split, ti.row0 + tok0 + col, f, jmax, v);
         } else if (f < p.out_cols) {
             __nv_bfloat16* o = out + static_cast<int64_t>(ti.row0 + tok0 + col) * p.out_cols + f;
 #pragma unroll
@@ -919,7 +937,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
         acc_empty_leader[1] = moe::map_to_cta(bar(S.acc_empty[1]), 0);
     }
     for (int t = tile_first<SWAP>(); t < total; t += tile_step<SWAP>()) {
-        const Tile ti = decode_tile<SWAP, WG>(t, S, p);
+        const Tile ti = decode_tile<SWAP, WG, EPI == EPI_SUM && !WG>(t, S, p);
         const int row = ti.row0 + r;
         const bool live = row < ti.row_end;
         if (SWAP) {
@@ -948,10 +966,15 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                     }
-                    if (EPI == EPI_SUM) {
-                        sum_chunk(p, ti.row0 + col, ti.col0 + static_cast<int>(rank) * 128 + q * 32 + lane,
+                    if (EPI == EPI_SUM && WG) {
+                        const float scale = p.row_scale[0];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(scale * __uint_as_float(v[i]));
+                    }
+                    if (EPI == EPI_SUM && !WG) {
+                        sum_chunk(p, ti.split, ti.row0 + col, ti.col0 + static_cast<int>(rank) * 128 + q * 32 + lane,
                                   min(32, ntok - col), v);
-                    } else if (EPI == EPI_STORE) {
+                    } else if (plain_tiles(EPI)) {
                         // one output feature per lane; a warp store covers 64
                         // contiguous bytes of one token row
                         const int f = ti.col0 + static_cast<int>(rank) * 128 + q * 32 + lane;
@@ -1297,7 +1320,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     moe::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     // tiles (pair tiles when SWAP)
-    const int total = WG ? p.E * wg_pair_mt(p) * p.n_tiles : S.prefix[p.E] * p.n_tiles;
+    const int total = WG ? p.E * wg_pair_mt(p) * p.n_tiles
+                         : S.prefix[p.E] * p.n_tiles * (EPI == EPI_SUM ? p.splits : 1);
 
     // FP8 promotion keeps 128 fp32 accumulators per epilogue thread: move
     // registers from warpgroup 0 (TMA, MMA) to the two epilogue warpgroups.
@@ -1583,11 +1607,44 @@ moe_status_t moe::dgrad_gemm(const void* dC, const void* B, const int32_t* offse
                             MOE_EPI_STORE, dA, nullptr, reinterpret_cast<moe_stream_t>(s), true);
 }
 
+// How dgrad_sum_gemm cuts M rows x K features over a contraction of N: token
+// tiles of equal height (at most BT) and ranges of the contraction.  The cost
+// is the rounds over the CTA pairs times a tile's time (340 ns a k-block of 256
+// rows, measured, with 32 rows' worth that does not shrink with the height, and
+// about 6 k-blocks for the epilogue), and for several ranges their sums'
+// traffic.  4096 x 2880 over 32768: 19 tiles of 216 rows fill 3 rounds that 16
+// of 256 leave half empty; 1021 x 1000 over 50257: 16 tiles alone would leave
+// 60 of 76 pairs idle.
+struct SumPlan {
+    int token_tiles, splits;
+};
+static SumPlan sum_plan(int M, int N, int K, int pairs) {
+    const int n_tiles = (K + kSwapFeatStore - 1) / kSwapFeatStore, kb = (N + 63) / 64;
+    const int least = (M + BT - 1) / BT;
+    SumPlan best{least, 1};
+    double best_ns = 1e30;
+    for (int splits = 1; splits <= 16 && (splits == 1 || kb / splits >= 16); ++splits)
+        for (int mt = least; mt <= least + pairs && (mt == least || (mt - 1) * 16 < M); ++mt) {
+            const int ts = ((M + mt - 1) / mt + 15) & ~15;
+            if ((M + ts - 1) / ts != mt) continue;   // a tile without rows
+            const double rounds = static_cast<double>((static_cast<int64_t>(mt) * n_tiles * splits + pairs - 1) / pairs);
+            const double ns = rounds * (ts + 32) / 288.0 * 340.0 * ((kb + splits - 1) / splits + 6) +
+                              (splits > 1 ? static_cast<double>(splits) * M * K * 8 / 6800.0 : 0.0);
+            if (ns < best_ns) { best_ns = ns; best = SumPlan{mt, splits}; }
+        }
+    return best;
+}
+
+int moe::dgrad_sum_splits(int M, int N, int K) {
+    const int pairs = moe::sm_count() / 2;
+    return sum_plan(M, N, K, pairs > 0 ? pairs : 76).splits;
+}
+
 moe_status_t moe::dgrad_sum_gemm(const void* dC, int ldc, const void* B, const int32_t* offsets, int M, int N, int K,
-                                 float* sum, bool first, bool last, const float* row_scale, void* dA,
+                                 float* sum, int splits, bool first, bool last, const float* row_scale, void* dA,
                                  cudaStream_t s) {
     MOE_CHECK_ARG(dC && B && offsets && M >= 1 && N >= 1 && ldc >= N && ldc % 8 == 0 && K >= 8 && K % 8 == 0);
-    MOE_CHECK_ARG((sum || (first && last)) && (dA || !last));
+    MOE_CHECK_ARG(splits >= 1 && (splits == 1 || !last) && (sum || (first && last)) && (dA || !last));
     MOE_CHECK_ARG(moe::aligned16(dC) && moe::aligned16(B) && moe::aligned16(sum) && moe::aligned16(dA));
     int* err = moe::device_error_word();
     const int pairs = moe::sm_count() / 2;
@@ -1619,20 +1676,8 @@ moe_status_t moe::dgrad_sum_gemm(const void* dC, int ldc, const void* B, const i
     p.sum_first = first;
     p.sum_last = last;
     p.row_scale = row_scale;
-    // Token tiles of at most BT rows, as many as make the rounds over the CTA
-    // pairs times the tile's height smallest: with one expert a tile too many
-    // costs a whole round (4096 x 2880: 16 tiles of 256 rows take 3 rounds,
-    // 19 of 216 rows as many).
-    const int least = (M + BT - 1) / BT;
-    int64_t best = INT64_MAX;
-    for (int mt = least; mt <= least + pairs && (mt - least) * 16 <= M; ++mt) {
-        const int ts = ((M + mt - 1) / mt + 15) & ~15;
-        const int used = (M + ts - 1) / ts;   // tiles that have rows
-        if (used != mt) continue;
-        const int64_t cost = static_cast<int64_t>((static_cast<int64_t>(mt) * p.n_tiles + pairs - 1) / pairs) * (ts + 32);
-        if (cost < best) { best = cost; p.token_tiles = mt; }
-    }
-    if (!p.token_tiles) p.token_tiles = least;
+    p.splits = splits;
+    p.token_tiles = sum_plan(M, N, K, pairs).token_tiles;
     return launch<false, EPI_SUM, true>(tmB, tmB, tmX, p, s);
 }
 
@@ -1643,7 +1688,7 @@ moe_status_t moe::swiglu_keep_gemm(const void* x, const void* W1, const int32_t*
 }
 
 moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, const void* tails, const int32_t* offsets,
-                             int E, int M_cap, int N, int K, void* dB, cudaStream_t s) {
+                             int E, int M_cap, int N, int K, void* dB, cudaStream_t s, const float* scale) {
     // dB[e] [N, K] = dC_e^T A_e over expert e's rows.  Swapped operands on CTA
     // pairs: A supplies the MMA's M rows (the output features, 256 per pair
     // tile), dC its N columns (the output rows, in tiles of up to 256); both
@@ -1689,6 +1734,8 @@ moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, const void*
     p.topk = 1;
     p.wg_rows = N;
     p.no_tails = tails ? 0 : 1;
+    p.row_scale = scale;
+    if (scale) return launch<false, EPI_SUM, true, true>(tmX.m[kWgA], tmX.m[kWgC], tmX, p, s);
     return launch<false, EPI_STORE, true, true>(tmX.m[kWgA], tmX.m[kWgC], tmX, p, s);
 }
 

@@ -23,18 +23,23 @@ moe_status_t dgrad_gemm(const void* dC, const void* B, const int32_t* offsets, i
 // rows [64e, 64e + 64) of the tails, zero-padded copies of those rows:
 // dC's bf16 [64E, N] followed by A's bf16 [64E, K].  dB bf16 [E, N, K]; an
 // expert without rows gets zeros.  tails NULL: a single expert of exactly M_cap
-// rows, whose last k-block reads zeros from outside the tensor maps.
+// rows, whose last k-block reads zeros from outside the tensor maps.  scale (one
+// float on the device) multiplies dB in fp32 before it is rounded.
 moe_status_t wgrad_gemm(const void* dC, int ldc, const void* A, const void* tails, const int32_t* offsets, int E,
-                        int M_cap, int N, int K, void* dB, cudaStream_t stream);
+                        int M_cap, int N, int K, void* dB, cudaStream_t stream, const float* scale = nullptr);
 
 // The data gradient of one expert of M rows, its contraction split over
-// several launches (grouped_gemm.cu): with C[p, c] = sum_n dC[p, n] B[n, c]
-// over this launch's N rows of B, the first launch sets sum [M, K] fp32 = C, the
-// others add to it, and the last one stores dA[p, c] = row_scale[p] * (sum + C)
-// as bf16 instead (row_scale NULL: 1; sum may be NULL if one launch is both).
+// several launches and, within one, over `splits` ranges (grouped_gemm.cu): with
+// C[p, c] = sum_n dC[p, n] B[n, c] over this launch's N rows of B, cut into
+// ranges, the first launch sets sum [splits, M, K] fp32 to the ranges' products
+// and the others add theirs; the caller adds the ranges up.  With one range
+// the last launch stores dA[p, c] = row_scale[p] * (sum + C) as bf16 instead
+// (sum may be NULL if it is also the first).  dgrad_sum_splits: the number of
+// ranges that fills the GPU, for the longest N of the launches.
 // dC bf16 [M, N], rows ldc elements apart; B bf16 [N, K]; offsets {0, M}.
+int dgrad_sum_splits(int M, int N, int K);
 moe_status_t dgrad_sum_gemm(const void* dC, int ldc, const void* B, const int32_t* offsets, int M, int N, int K,
-                            float* sum, bool first, bool last, const float* row_scale, void* dA,
+                            float* sum, int splits, bool first, bool last, const float* row_scale, void* dA,
                             cudaStream_t stream);
 
 // A tensor map for tiles staged with the 128-byte swizzle, zeros outside

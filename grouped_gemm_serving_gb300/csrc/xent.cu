@@ -8,9 +8,15 @@
 //   dx[t] = dloss[t] sum_v G[t, v] W[v],   dW[v] = sum_t G[t, v] dloss[t] x[t]
 //
 // Forward: the logits kernel below computes z tile by tile in tensor memory
-// and reduces each tile to a running maximum and sum of exponentials a row;
-// a second, small kernel joins the vocabulary tiles' pairs (m, s):
-//   M = max m,  lse = M + log sum s exp(m - M).
+// and reduces each tile to a running maximum and sum of exponentials a row,
+// without the label's column.  The label's logit z_l comes from a dot product
+// of its own, in fp32 arithmetic that rounds to nearest, by warps that have
+// nothing else to do: the tensor cores' sums, which cut off, are off by some
+// 2e-6 of z_l, which the difference lse - z_l would keep.  A second, small
+// kernel joins the vocabulary tiles' pairs (m, s) and the label:
+//   M = max m,  S = sum s exp(m - M),  lse = log(S exp M + exp z_l),
+//   loss = log(1 + S exp(M - z_l)),
+// which keeps its precision where the label is all but certain.
 // 2 T H V operations, W read once: bound by the tensor pipe for many tokens
 // and by reading W for few.
 //
@@ -20,8 +26,10 @@
 // gradient computes the piece's rows of dW.  G's entries are probabilities and
 // label entries near -1, each rounded by at most a relative 2^-8,
 // independently; dloss stays out of G, so that the label entries, which carry
-// most of the gradient, are not all off by the same rounding of dloss: it
-// multiplies dx in fp32 and, for dW, x (rounded to bf16 once).
+// most of the gradient, are not all off by the same rounding of dloss.  It
+// multiplies dx in fp32; for dW its largest magnitude d does, and x is scaled by
+// dloss / d, which changes nothing where all tokens weigh the same (a mean) and
+// rounds x to bf16 once more elsewhere.
 //
 // The logits kernel: CTA pairs (clusters of two), tcgen05 cta_group::2 MMAs of
 // 256 tokens (128 per CTA) x up to 256 vocabulary rows (half staged by each
@@ -35,7 +43,8 @@
 //
 // Roles in a CTA (384 threads): warp 0 loads (TMA), warp 1 of the even CTA
 // issues the MMAs, warps 4-11 are the epilogue (warp w: lanes 32 (w % 4)..,
-// half (w - 4) / 4 of the columns).  Every wait is bounded; on expiry the CTA
+// half (w - 4) / 4 of the columns), and in the forward pass warps 2 and 3 take
+// the labels' logits.  Every wait is bounded; on expiry the CTA
 // records MOE_DEVERR_TIMEOUT, waits for its loads and MMAs and leaves.
 #include <climits>
 
@@ -66,6 +75,8 @@ struct Params {
     // forward
     float2* part;         // [2 * voc_tiles, T]: maximum and sum of each half tile
     float* at_label;      // [T]: the label's logit
+    const uint4 *x, *W;
+    int V, row_vecs;
     // backward
     const float* lse;
     __nv_bfloat16* G;     // [T, ldg]; columns from cols on are never read
@@ -213,10 +224,10 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(u[j]);
             if (!BACK) {
-                if (counts && rel >= col && rel < min(col + 32, ncols))
+                if (counts && rel >= col && rel < min(col + 32, ncols))   // the join adds it
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (rel == col + j) p.at_label[row] = z[j];
+                        if (rel == col + j) z[j] = -INFINITY;
                 if (col + 32 > ncols)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -264,6 +275,31 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
     }
 }
 
+// The labels' logits, a warp a token: x[t] and W[label] in fp32.
+__device__ void label_logits(const Params& p, int warp) {
+    const int lane = threadIdx.x & 31;
+    for (int t = blockIdx.x * 2 + warp; t < p.T; t += gridDim.x * 2) {
+        const int label = p.labels[t];
+        if (label == p.ignore || label < 0 || label >= p.V) continue;
+        const uint4* x = p.x + static_cast<int64_t>(t) * p.row_vecs;
+        const uint4* w = p.W + static_cast<int64_t>(label) * p.row_vecs;
+        float dot = 0.0f;
+#pragma unroll 4
+        for (int c = lane; c < p.row_vecs; c += 32) {
+            const uint4 a = __ldg(x + c), b = __ldg(w + c);
+            const uint32_t a4[4] = {a.x, a.y, a.z, a.w}, b4[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dot = fmaf(moe::bf16_lo(a4[i]), moe::bf16_lo(b4[i]), dot);
+                dot = fmaf(moe::bf16_hi(a4[i]), moe::bf16_hi(b4[i]), dot);
+            }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        if (lane == 0) p.at_label[t] = dot;
+    }
+}
+
 template <bool BACK>
 __global__ void __launch_bounds__(kThreads, 1)
 logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p) {
@@ -300,6 +336,7 @@ logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     if (warp >= 4) epilogue<BACK>(S, p, total, tmem, rank);
     else if (warp == 0) producer(&tmX, &tmW, stages, S, p, total, rank);
     else if (warp == 1 && rank == 0) mma_issuer(stages, S, p, total, tmem);
+    else if (!BACK && warp >= 2) label_logits(p, warp - 2);
     moe::tc_fence_before();
     moe::cluster_sync();   // no CTA of the pair leaves while its peer may still signal it
     if (warp == 1) {
@@ -338,46 +375,91 @@ join_kernel(const float2* __restrict__ part, int parts, const float* __restrict_
         s = s * expf(m - base) + v.y * expf(v.x - base);
         m = nm;
     }
-    const float l = m + logf(s);
     const int label = labels[t];
-    float out = 0.0f;
-    if (label != ignore) {
-        if (label >= 0 && label < V) out = l - at_label[t];
-        else moe::raise_device_error(err, MOE_DEVERR_LABEL);
+    float out = 0.0f, l;
+    if (label != ignore && label >= 0 && label < V) {
+        const float z = at_label[t], top = fmaxf(m, z);
+        const float rest = s * expf(m - top), sum = rest + expf(z - top);
+        l = top + logf(sum);
+        out = z >= m ? log1pf(rest) : (m - z) + logf(sum);
+    } else {
+        l = m + logf(s);
+        if (label != ignore) moe::raise_device_error(err, MOE_DEVERR_LABEL);
     }
     loss[t] = out;
     lse[t] = l;
 }
 
-// Backward's per-token factors: scale[t] = dloss[t] (0 where the label is
-// ignored or invalid), xs[t] = bf16(scale[t] * x[t]); offsets = {0, T}.
-__global__ void __launch_bounds__(256)
-scale_rows_kernel(const uint4* __restrict__ x, const float* __restrict__ dloss, const int32_t* __restrict__ labels,
-                  int T, int V, int row_vecs, int ignore, float* __restrict__ scale, uint4* __restrict__ xs,
-                  int32_t* __restrict__ offsets, int* err) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        offsets[0] = 0;
-        offsets[1] = T;
+// Backward's per-token factors: scale[t] = dloss[t], 0 where the label is
+// ignored or invalid (the latter is reported), scale[T] = the largest
+// magnitude among them; offsets = {0, T}.  One block.
+__global__ void __launch_bounds__(1024)
+scale_kernel(const float* __restrict__ dloss, const int32_t* __restrict__ labels, int T, int V, int ignore,
+             float* __restrict__ scale, int32_t* __restrict__ offsets, int* err) {
+    __shared__ float part[32];
+    float top = 0.0f;
+    bool bad = false;
+    for (int t = threadIdx.x; t < T; t += 1024) {
+        const int label = labels[t];
+        const bool counts = label != ignore && label >= 0 && label < V;
+        const float d = counts ? dloss[t] : 0.0f;
+        bad |= !counts && label != ignore;
+        scale[t] = d;
+        top = fmaxf(top, fabsf(d));
     }
+    if (bad) moe::raise_device_error(err, MOE_DEVERR_LABEL);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        top = part[threadIdx.x];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        if (threadIdx.x == 0) {
+            scale[T] = top;
+            offsets[0] = 0;
+            offsets[1] = T;
+        }
+    }
+}
+
+// xs[t] = bf16(scale[t] / scale[T] * x[t]), zeros where scale[t] is 0.
+__global__ void __launch_bounds__(256)
+scale_rows_kernel(const uint4* __restrict__ x, const float* scale, int T, int row_vecs, uint4* __restrict__ xs) {
+    moe::wait_for_primary();
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (t >= T) return;
-    const int label = labels[t];
-    const bool counts = label != ignore && label >= 0 && label < V;
-    const float d = counts ? dloss[t] : 0.0f;
-    if (lane == 0) {
-        scale[t] = d;
-        if (!counts && label != ignore) moe::raise_device_error(err, MOE_DEVERR_LABEL);
-    }
+    const float d = scale[t], r = d == 0.0f ? 0.0f : __fdiv_rn(d, scale[T]);
     for (int c = lane; c < row_vecs; c += 32) {
         const uint4 v = __ldg(x + static_cast<int64_t>(t) * row_vecs + c);
         const uint32_t a[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            o[i] = counts ? moe::pack_bf16x2(d * moe::bf16_lo(a[i]), d * moe::bf16_hi(a[i])) : 0u;
+            o[i] = d == 0.0f ? 0u : moe::pack_bf16x2(r * moe::bf16_lo(a[i]), r * moe::bf16_hi(a[i]));
         xs[static_cast<int64_t>(t) * row_vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
+}
+
+// dx[t] = scale[t] * (the ranges' sums, in range order), four columns a thread.
+__global__ void __launch_bounds__(256)
+finish_kernel(const float4* __restrict__ sum, int splits, int64_t n, int row_quads, const float* __restrict__ scale,
+              uint2* __restrict__ dx) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    float4 a = sum[i];
+#pragma unroll 4
+    for (int r = 1; r < splits; ++r) {
+        const float4 b = sum[r * n + i];
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+    }
+    const float d = scale[i / row_quads];
+    dx[i] = make_uint2(moe::pack_bf16x2(d * a.x, d * a.y), moe::pack_bf16x2(d * a.z, d * a.w));
 }
 
 // ---------------------------------------------------------------- host side
@@ -472,7 +554,7 @@ constexpr int64_t kPieceBytes = 256ll << 20;
 constexpr int kPieceMin = 2048;
 
 struct BackwardLayout {
-    int piece, pieces, ldg;
+    int piece, pieces, ldg, splits;
     size_t G, xs, scale, offsets, sum, total;
 };
 BackwardLayout backward_layout(int T, int H, int V) {
@@ -487,9 +569,10 @@ BackwardLayout backward_layout(int T, int H, int V) {
     Carver c;
     l.G = c.take(static_cast<size_t>(T) * l.ldg * 2);
     l.xs = c.take(static_cast<size_t>(T) * H * 2);
-    l.scale = c.take(static_cast<size_t>(T) * sizeof(float));
+    l.scale = c.take((static_cast<size_t>(T) + 1) * sizeof(float));
     l.offsets = c.take(2 * sizeof(int32_t));
-    l.sum = c.take(l.pieces > 1 ? static_cast<size_t>(T) * H * sizeof(float) : 0);
+    l.splits = moe::dgrad_sum_splits(T, l.piece, H);
+    l.sum = c.take(l.pieces > 1 || l.splits > 1 ? static_cast<size_t>(l.splits) * T * H * sizeof(float) : 0);
     l.total = c.off;
     return l;
 }
@@ -525,6 +608,10 @@ extern "C" moe_status_t moe_cross_entropy_forward(const void* x, const void* W, 
     p.ignore = ignore_index;
     p.part = reinterpret_cast<float2*>(base + l.part);
     p.at_label = reinterpret_cast<float*>(base + l.at_label);
+    p.x = static_cast<const uint4*>(x);
+    p.W = static_cast<const uint4*>(W);
+    p.V = V;
+    p.row_vecs = H / 8;
     const moe_status_t st = launch_logits<false>(x, W, H, V, p, s);
     if (st != MOE_OK) return st;
     join_kernel<<<(T + kJoinTokens - 1) / kJoinTokens, 256, 0, s>>>(p.part, 2 * l.voc_tiles, p.at_label, labels, T, V,
@@ -555,10 +642,13 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
     void* xs = base + l.xs;
     auto* scale = reinterpret_cast<float*>(base + l.scale);
     auto* offsets = reinterpret_cast<int32_t*>(base + l.offsets);
-    auto* sum = l.pieces > 1 ? reinterpret_cast<float*>(base + l.sum) : nullptr;
-    scale_rows_kernel<<<(T + 7) / 8, 256, 0, s>>>(static_cast<const uint4*>(x), dloss, labels, T, V, H / 8,
-                                                  ignore_index, scale, static_cast<uint4*>(xs), offsets, err);
+    auto* sum = l.pieces > 1 || l.splits > 1 ? reinterpret_cast<float*>(base + l.sum) : nullptr;
+    scale_kernel<<<1, 1024, 0, s>>>(dloss, labels, T, V, ignore_index, scale, offsets, err);
     MOE_CHECK_LAUNCH();
+    moe_status_t st = MOE_OK;
+    if (dW && (st = moe::launch_after(scale_rows_kernel, dim3((T + 7) / 8), 256, s, static_cast<const uint4*>(x),
+                                      static_cast<const float*>(scale), T, H / 8, static_cast<uint4*>(xs))) != MOE_OK)
+        return st;
     for (int i = 0; i < l.pieces; ++i) {
         Params p{};
         p.labels = labels;
@@ -574,17 +664,23 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
         p.lse = lse;
         p.G = G;
         p.ldg = l.ldg;
-        moe_status_t st = launch_logits<true>(x, W, H, V, p, s);
+        st = launch_logits<true>(x, W, H, V, p, s);
         if (st != MOE_OK) return st;
         const auto* Wp = static_cast<const __nv_bfloat16*>(W) + static_cast<int64_t>(p.v0) * H;
-        if (dx && (st = moe::dgrad_sum_gemm(G, l.ldg, Wp, offsets, T, p.cols, H, sum, i == 0, i == l.pieces - 1, scale,
-                                            dx, s)) != MOE_OK)
+        if (dx && (st = moe::dgrad_sum_gemm(G, l.ldg, Wp, offsets, T, p.cols, H, sum, l.splits, i == 0,
+                                            l.splits == 1 && i == l.pieces - 1, scale, dx, s)) != MOE_OK)
             return st;
         if (dW) {
             auto* dWp = static_cast<__nv_bfloat16*>(dW) + static_cast<int64_t>(p.v0) * H;
-            st = moe::wgrad_gemm(G, l.ldg, xs, nullptr, offsets, 1, T, p.cols, H, dWp, s);
+            st = moe::wgrad_gemm(G, l.ldg, xs, nullptr, offsets, 1, T, p.cols, H, dWp, s, scale + T);
             if (st != MOE_OK) return st;
         }
+    }
+    if (dx && l.splits > 1) {
+        const int64_t n = static_cast<int64_t>(T) * (H / 4);
+        finish_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(
+            reinterpret_cast<const float4*>(sum), l.splits, n, H / 4, scale, static_cast<uint2*>(dx));
+        MOE_CHECK_LAUNCH();
     }
     return MOE_OK;
 }

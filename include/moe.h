@@ -477,7 +477,7 @@ moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, const void* dy, int64_t 
  *   dx[t] = dloss[t] * sum_v G[t, v] W[v],  dW[v] = sum_t G[t, v] dloss[t] x[t],
  *   written (not accumulated).  Either of dx and dW may be NULL and is then
  *   not computed.  The vocabulary is taken in pieces, so that the workspace
- *   stays near 256 MiB plus three copies of x.
+ *   stays near 256 MiB plus some copies of x (in bf16 and, summed, in fp32).
  * A token whose label is ignore_index (any value, such as -100) has loss 0 and
  * zero gradients, whatever its dloss; its lse is written.  A label outside
  * [0, V) that is not ignore_index is recorded as MOE_DEVERR_LABEL and treated
