@@ -239,7 +239,7 @@ template <bool SWAP, bool WG = false, bool SUM = false>
 __device__ __forceinline__ Tile decode_tile(int t, const Shared& S, const Params& p) {
     static_assert(!WG || SWAP, "the weight gradient runs on CTA pairs");
     int lo = 0, mt, local, split = 0;
-    if (SUM) {   // range-major: the tiles of a range run together
+    if (SUM && !WG) {   // range-major: the tiles of a range run together
         const int per = S.prefix[p.E] * p.n_tiles;
         split = t / per;
         t -= split * per;
@@ -265,7 +265,7 @@ __device__ __forceinline__ Tile decode_tile(int t, const Shared& S, const Params
     ti.nkb = p.k_blocks;
     ti.kb0 = 0;
     ti.split = split;
-    if (SUM) {
+    if (SUM && !WG) {
         ti.kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * split / p.splits);
         ti.nkb = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (split + 1) / p.splits) - ti.kb0;
     }
@@ -274,7 +274,10 @@ __device__ __forceinline__ Tile decode_tile(int t, const Shared& S, const Params
         // weight gradient on a pair: the tokens are the wg_rows output rows
         // in tiles of BT; the contraction runs over the expert's own rows in
         // k-blocks of 64 (S.prefix is the k-block prefix)
-        ti.row0 = (local % mt) * BT;
+        // (with EPI_SUM the column tiles are walked first: the pairs that run
+        // together share dC's columns, which would otherwise come from HBM
+        // once for every column tile)
+        ti.row0 = (SUM ? local / p.n_tiles : local % mt) * BT;
         ti.rows = min(BT, p.wg_rows - ti.row0);
         ti.row_end = p.wg_rows;
         ti.first = p.offsets[lo];
@@ -291,7 +294,7 @@ __device__ __forceinline__ Tile decode_tile(int t, const Shared& S, const Params
         ti.row0 = p.offsets[lo] + (local % mt) * BM;
         ti.rows = 0;
     }
-    ti.col0 = (local / mt) * (SWAP ? (p.half ? kSwapFeatSwiglu : kSwapFeatStore) : (p.half ? BN / 2 : BN));
+    ti.col0 = (SUM && WG ? local % p.n_tiles : local / mt) * (SWAP ? (p.half ? kSwapFeatSwiglu : kSwapFeatStore) : (p.half ? BN / 2 : BN));
     if (SWAP && p.half && !WG) ti.half = p.half - ti.col0 <= kSwapFeatSwiglu / 2;
     else if (SWAP && !p.half && !p.fc && !WG) ti.half = p.N - ti.col0 <= kSwapFeatStore / 2;
     return ti;
@@ -431,7 +434,7 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
     uint32_t phase = 0, issued = 0, issued_par = 0;
     bool ok = true;
     for (int t = tile_first<true>(); ok && t < total; t += tile_step<true>()) {
-        const Tile ti = decode_tile<true, WG, EPI == EPI_SUM && !WG>(t, S, p);
+        const Tile ti = decode_tile<true, WG, EPI == EPI_SUM>(t, S, p);
         const int nh = swap_n(ti) / 2;                 // token rows in each CTA: 8 .. 128
         const CUtensorMap* tmXh = &tmX->m[nh / 8 - 1];
         const int xrow = ti.row0 + static_cast<int>(rank) * nh;
@@ -611,7 +614,7 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
     bool ok = true, issued = false;
     for (int t = tile_first<SWAP>(); ok && t < total; t += tile_step<SWAP>()) {
         if (SWAP) {
-            const Tile ti = decode_tile<true, WG, EPI == EPI_SUM && !WG>(t, S, p);
+            const Tile ti = decode_tile<true, WG, EPI == EPI_SUM>(t, S, p);
             const int n = swap_n(ti);
             const int m = ti.half ? BM : 2 * BM;
             idesc = WG ? moe::make_idesc_ab_mn(1u, 2 * BM, n)
@@ -626,8 +629,7 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
         }
         // weight-gradient tiles of an expert without rows have no k-blocks:
         // the accumulator is committed untouched and the epilogue writes zeros
-        constexpr bool kSum = EPI == EPI_SUM && !WG;
-        const int nkb = WG || kSum ? decode_tile<SWAP, WG, kSum>(t, S, p).nkb : p.k_blocks;
+        const int nkb = WG || EPI == EPI_SUM ? decode_tile<SWAP, WG, EPI == EPI_SUM>(t, S, p).nkb : p.k_blocks;
         for (int kb = 0; kb < nkb; ++kb) {
             if (FP8) {
                 const bool got = moe::mbar_wait(bar(S.acc_empty[acc]), acc_phase ^ 1u, &S.abort_flag, kWaitNs);
@@ -937,7 +939,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
         acc_empty_leader[1] = moe::map_to_cta(bar(S.acc_empty[1]), 0);
     }
     for (int t = tile_first<SWAP>(); t < total; t += tile_step<SWAP>()) {
-        const Tile ti = decode_tile<SWAP, WG, EPI == EPI_SUM && !WG>(t, S, p);
+        const Tile ti = decode_tile<SWAP, WG, EPI == EPI_SUM>(t, S, p);
         const int row = ti.row0 + r;
         const bool live = row < ti.row_end;
         if (SWAP) {

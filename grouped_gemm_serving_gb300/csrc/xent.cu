@@ -37,7 +37,9 @@
 // tensor memory.  A lane of tensor memory is a token, so a row's maximum and
 // sum run along a thread's own columns.  Tiles are walked vocabulary-major
 // with the token tiles inside, so the pairs that run together read the same
-// rows of W, once from HBM, while x stays in L2.  The tile's width in
+// rows of W, once from HBM, while x stays in L2.  At most 128 tokens take
+// M = 128 MMAs (64 tokens staged per CTA, half the tensor time), whose
+// accumulator holds token l % 64 in lane l, columns (l / 64) N/2 .. + N/2.  The tile's width in
 // vocabulary rows is 256 or, where the tiles do not fill whole rounds of the
 // pairs, the smallest multiple of 16 that takes as many rounds.
 //
@@ -53,7 +55,10 @@
 
 namespace {
 
-constexpr int kStages = 7;
+constexpr int kMaxStages = 7;
+// Backward gives one stage to the warps' transposes of G.
+template <bool BACK>
+constexpr int kStagesOf = BACK ? 6 : kMaxStages;
 constexpr int kStageA = 128 * 128;   // 128 tokens x 64 bf16
 constexpr int kStageB = 128 * 128;   // up to 128 vocabulary rows x 64 bf16
 constexpr int kStageBytes = kStageA + kStageB;
@@ -68,12 +73,14 @@ struct Params {
     const int32_t* labels;
     int* err;
     int T, k_blocks;
+    int bt;               // tokens of a tile: BT, or 128 for at most 128 tokens
     int v0, cols;         // the launch's vocabulary rows: [v0, v0 + cols)
     int bv;               // vocabulary rows of a tile (multiple of 16, <= BV)
     int tok_tiles, voc_tiles;
     int ignore;
     // forward
-    float2* part;         // [2 * voc_tiles, T]: maximum and sum of each half tile
+    float2* part;         // [shares * voc_tiles, T]: maximum and sum of each share of a tile's columns
+    int shares;           // 2, or 4 for tiles of 128 tokens
     float* at_label;      // [T]: the label's logit
     const uint4 *x, *W;
     int V, row_vecs;
@@ -84,13 +91,15 @@ struct Params {
 };
 
 struct alignas(16) Shared {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
 };
-constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared);
+constexpr int kTransposeBytes = 32 * 128;   // a warp's 32 tokens x 64 columns of G
+static_assert(8 * kTransposeBytes <= kStageBytes, "the transposes take the stage they were given");
+constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(kMaxStages) * kStageBytes + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
 __device__ __forceinline__ uint32_t bar(uint64_t& b) { return moe::smem_u32(&b); }
@@ -106,6 +115,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+template <int kStages>
 __device__ void producer(const CUtensorMap* tmX, const CUtensorMap* tmW, uint8_t* stages, Shared& S, const Params& p,
                          int total, uint32_t rank) {
     int stage = 0;
@@ -113,7 +123,7 @@ __device__ void producer(const CUtensorMap* tmX, const CUtensorMap* tmW, uint8_t
     bool ok = true;
     const int half = p.bv / 2;
     for (int t = blockIdx.x >> 1; ok && t < total; t += gridDim.x >> 1) {
-        const int row = (t % p.tok_tiles) * BT + static_cast<int>(rank) * 128;
+        const int row = (t % p.tok_tiles) * BT + static_cast<int>(rank) * (p.bt / 2);
         const int voc = p.v0 + (t / p.tok_tiles) * p.bv + static_cast<int>(rank) * half;
         for (int kb = 0; kb < p.k_blocks; ++kb) {
             const bool got = moe::mbar_wait(bar(S.empty[stage]), phase ^ 1u, &S.abort_flag, kWaitNs);
@@ -124,7 +134,7 @@ __device__ void producer(const CUtensorMap* tmX, const CUtensorMap* tmW, uint8_t
             const uint32_t fb = moe::map_to_cta(bar(S.full[stage]), 0);
             const uint32_t sa = moe::smem_u32(stages + stage * kStageBytes);
             if (moe::elect_one()) {
-                if (rank == 0) moe::mbar_arrive_expect_tx(bar(S.full[stage]), 2 * (kStageA + half * 128));
+                if (rank == 0) moe::mbar_arrive_expect_tx(bar(S.full[stage]), (p.bt + p.bv) * 128);   // both CTAs' rows
                 moe::tma_load_2d_pair(sa, tmX, fb, kb * 64, row);
                 moe::tma_load_2d_pair(sa + kStageA, tmW, fb, kb * 64, voc);
             }
@@ -149,8 +159,9 @@ __device__ void producer(const CUtensorMap* tmX, const CUtensorMap* tmW, uint8_t
     __syncwarp();
 }
 
+template <int kStages>
 __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int total, uint32_t tmem) {
-    const uint32_t idesc = moe::make_idesc(1u, BT, p.bv);
+    const uint32_t idesc = moe::make_idesc(1u, p.bt, p.bv);
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true, issued = false;
@@ -192,19 +203,28 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
 }
 
 template <bool BACK>
-__device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, uint32_t rank) {
+__device__ void epilogue(uint8_t* stages, Shared& S, const Params& p, int total, uint32_t tmem, uint32_t rank) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q = warp & 3, hsel = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    // backward: the warp's transpose buffer, rows of 128 bytes whose 16-byte
+    // pieces are permuted by the row, so that neither side conflicts on banks
+    uint4* buf = reinterpret_cast<uint4*>(stages + kStagesOf<BACK> * kStageBytes + (warp - 4) * kTransposeBytes);
     int acc = 0;
     uint32_t acc_phase = 0;
     const uint32_t leader[2] = {moe::map_to_cta(bar(S.acc_empty[0]), 0), moe::map_to_cta(bar(S.acc_empty[1]), 0)};
-    const int chunks = (p.bv + 31) / 32, c_lo = hsel ? (chunks + 1) / 2 : 0, c_hi = hsel ? chunks : (chunks + 1) / 2;
+    // this thread's token within the CTA's, and its accumulator columns: the
+    // tile's, or for M = 128 the half of them that its lanes hold
+    const bool small = p.bt == 128;
+    const int trow = small ? (q & 1) * 32 + lane : q * 32 + lane;
+    const int shift = small ? (q >> 1) * (p.bv / 2) : 0, width = small ? p.bv / 2 : p.bv;
+    const int chunks = (width + 31) / 32, c_lo = hsel ? (chunks + 1) / 2 : 0, c_hi = hsel ? chunks : (chunks + 1) / 2;
+    const int share = small ? 2 * (q >> 1) + hsel : hsel;   // which part of a row's tile this thread reduces
     for (int t = blockIdx.x >> 1; t < total; t += gridDim.x >> 1) {
         const int vt = t / p.tok_tiles;
-        const int row = (t % p.tok_tiles) * BT + static_cast<int>(rank) * 128 + q * 32 + lane;
-        const int col0 = vt * p.bv;                          // first column of the tile within the launch's
-        const int ncols = min(p.bv, p.cols - col0);          // those that exist
+        const int row = (t % p.tok_tiles) * BT + static_cast<int>(rank) * (p.bt / 2) + trow;
+        const int col0 = vt * p.bv + shift;                  // first of its columns within the launch's
+        const int ncols = min(width, p.cols - col0);         // those that exist
         const int label = row < p.T ? p.labels[row] : p.ignore;
         const int rel = label - p.v0 - col0;                 // the label's column, in the tile if 0 <= rel < ncols
         const bool counts = label != p.ignore && label >= 0;
@@ -254,16 +274,26 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (!counts || col + j >= ncols) g[j] = 0.0f;
-                if (row < p.T) {
-                    uint4* o = reinterpret_cast<uint4*>(p.G + static_cast<int64_t>(row) * p.ldg + col0 + col);
+                const int half = (c - c_lo) & 1;   // two chunks fill the buffer
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (col + 8 * i < p.bv && col0 + col + 8 * i < p.ldg)
-                            o[i] = make_uint4(moe::pack_bf16x2(g[8 * i], g[8 * i + 1]),
-                                              moe::pack_bf16x2(g[8 * i + 2], g[8 * i + 3]),
-                                              moe::pack_bf16x2(g[8 * i + 4], g[8 * i + 5]),
-                                              moe::pack_bf16x2(g[8 * i + 6], g[8 * i + 7]));
+                for (int i = 0; i < 4; ++i)
+                    buf[lane * 8 + ((4 * half + i) ^ (lane & 7))] =
+                        make_uint4(moe::pack_bf16x2(g[8 * i], g[8 * i + 1]), moe::pack_bf16x2(g[8 * i + 2], g[8 * i + 3]),
+                                   moe::pack_bf16x2(g[8 * i + 4], g[8 * i + 5]),
+                                   moe::pack_bf16x2(g[8 * i + 6], g[8 * i + 7]));
+                if (half == 0 && c + 1 < c_hi) continue;
+                // eight lanes a token: 128 contiguous bytes of its row of G
+                __syncwarp();
+                const int first = col - 32 * half, piece = lane & 7;
+                const bool in = piece < 4 * (half + 1) && first + 8 * piece < width && col0 + first + 8 * piece < p.ldg;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3), token = row - lane + r;
+                    const uint4 v = buf[r * 8 + (piece ^ (r & 7))];
+                    if (in && token < p.T)
+                        *reinterpret_cast<uint4*>(p.G + static_cast<int64_t>(token) * p.ldg + col0 + first + 8 * piece) = v;
                 }
+                __syncwarp();
             }
         }
         moe::tc_fence_before();
@@ -271,7 +301,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
         else moe::mbar_arrive(bar(S.acc_empty[acc]));
         acc ^= 1;
         if (!acc) acc_phase ^= 1u;
-        if (!BACK && row < p.T) p.part[static_cast<int64_t>(2 * vt + hsel) * p.T + row] = make_float2(m, s);
+        if (!BACK && row < p.T) p.part[static_cast<int64_t>(p.shares * vt + share) * p.T + row] = make_float2(m, s);
     }
 }
 
@@ -306,10 +336,10 @@ logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     const uint32_t rank = moe::cluster_ctarank();   // 0 leads the pair
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Shared& S = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
+    Shared& S = *reinterpret_cast<Shared*>(stages + kMaxStages * kStageBytes);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             moe::mbar_init(bar(S.full[s]), 1);
             moe::mbar_init(bar(S.empty[s]), 1);
         }
@@ -333,10 +363,11 @@ logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     moe::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     const int total = p.tok_tiles * p.voc_tiles;
-    if (warp >= 4) epilogue<BACK>(S, p, total, tmem, rank);
-    else if (warp == 0) producer(&tmX, &tmW, stages, S, p, total, rank);
-    else if (warp == 1 && rank == 0) mma_issuer(stages, S, p, total, tmem);
+    if (warp >= 4) epilogue<BACK>(stages, S, p, total, tmem, rank);
+    else if (warp == 0) producer<kStagesOf<BACK>>(&tmX, &tmW, stages, S, p, total, rank);
+    else if (warp == 1 && rank == 0) mma_issuer<kStagesOf<BACK>>(stages, S, p, total, tmem);
     else if (!BACK && warp >= 2) label_logits(p, warp - 2);
+    moe::launch_dependents();
     moe::tc_fence_before();
     moe::cluster_sync();   // no CTA of the pair leaves while its peer may still signal it
     if (warp == 1) {
@@ -350,10 +381,11 @@ logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
 // loss 0 (the latter is reported).
 constexpr int kJoinTokens = 8;
 __global__ void __launch_bounds__(256)
-join_kernel(const float2* __restrict__ part, int parts, const float* __restrict__ at_label,
+join_kernel(const float2* part, int parts, const float* at_label,
             const int32_t* __restrict__ labels, int T, int V, int ignore, float* __restrict__ loss,
             float* __restrict__ lse, int* err) {
     __shared__ float2 share[32][kJoinTokens];
+    moe::wait_for_primary();
     const int tok = threadIdx.x % kJoinTokens, g = threadIdx.x / kJoinTokens;
     const int t = blockIdx.x * kJoinTokens + tok;
     float m = -INFINITY, s = 0.0f;
@@ -468,15 +500,17 @@ bool valid_sizes(int T, int H, int V) {
            (static_cast<int64_t>(T) / BT + 1) * (static_cast<int64_t>(V) / 16 + 1) < INT_MAX;
 }
 
-// Vocabulary rows of a tile for `cols` of them and `tok_tiles` token tiles.
-int tile_width(int cols, int tok_tiles) {
+// Vocabulary rows of a tile for `cols` of them and T tokens: a multiple of 16,
+// or of 32 for M = 128 MMAs.
+int tile_width(int cols, int T) {
+    const int tok_tiles = (T + BT - 1) / BT, step = T <= 128 ? 32 : 16;
     const int pairs = moe::sm_count() / 2 > 0 ? moe::sm_count() / 2 : 76;
     const auto rounds = [&](int bv) {
         return (static_cast<int64_t>((cols + bv - 1) / bv) * tok_tiles + pairs - 1) / pairs;
     };
     const int64_t least = rounds(BV);
     int bv = BV;
-    while (bv > 32 && rounds(bv - 16) == least) bv -= 16;
+    while (bv > 32 && rounds(bv - step) == least) bv -= step;
     return bv;
 }
 
@@ -486,7 +520,7 @@ moe_status_t launch_logits(const void* x, const void* W, int H, int V, Params p,
     const cuuint64_t stride[1] = {static_cast<cuuint64_t>(H) * 2};
     const cuuint64_t dx[2] = {static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(p.T)};
     const cuuint64_t dw[2] = {static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(V)};
-    const cuuint32_t bx[2] = {64, 128}, bw[2] = {64, static_cast<cuuint32_t>(p.bv / 2)};
+    const cuuint32_t bx[2] = {64, static_cast<cuuint32_t>(p.bt / 2)}, bw[2] = {64, static_cast<cuuint32_t>(p.bv / 2)};
     if (!moe::encode_tile_map(&tmX, false, x, 2, dx, stride, bx) ||
         !moe::encode_tile_map(&tmW, false, W, 2, dw, stride, bw))
         return MOE_ERR_CUDA;
@@ -539,10 +573,10 @@ struct ForwardLayout {
 ForwardLayout forward_layout(int T, int V) {
     ForwardLayout l{};
     l.tok_tiles = (T + BT - 1) / BT;
-    l.bv = tile_width(V, l.tok_tiles);
+    l.bv = tile_width(V, T);
     l.voc_tiles = (V + l.bv - 1) / l.bv;
     Carver c;
-    l.part = c.take(static_cast<size_t>(2) * l.voc_tiles * T * sizeof(float2));
+    l.part = c.take(static_cast<size_t>(T <= 128 ? 4 : 2) * l.voc_tiles * T * sizeof(float2));
     l.at_label = c.take(static_cast<size_t>(T) * sizeof(float));
     l.total = c.off;
     return l;
@@ -565,7 +599,7 @@ BackwardLayout backward_layout(int T, int H, int V) {
     l.pieces = static_cast<int>((V + piece - 1) / piece);
     l.piece = l.pieces == 1 ? V : static_cast<int>(((V + l.pieces - 1) / l.pieces + BV - 1) / BV * BV);
     l.pieces = (V + l.piece - 1) / l.piece;
-    l.ldg = (l.piece + 7) / 8 * 8;
+    l.ldg = (l.piece + 63) / 64 * 64;   // rows of whole 128-byte lines
     Carver c;
     l.G = c.take(static_cast<size_t>(T) * l.ldg * 2);
     l.xs = c.take(static_cast<size_t>(T) * H * 2);
@@ -602,6 +636,8 @@ extern "C" moe_status_t moe_cross_entropy_forward(const void* x, const void* W, 
     p.T = T;
     p.k_blocks = (H + 63) / 64;
     p.cols = V;
+    p.bt = T <= 128 ? 128 : BT;
+    p.shares = T <= 128 ? 4 : 2;
     p.bv = l.bv;
     p.tok_tiles = l.tok_tiles;
     p.voc_tiles = l.voc_tiles;
@@ -614,10 +650,9 @@ extern "C" moe_status_t moe_cross_entropy_forward(const void* x, const void* W, 
     p.row_vecs = H / 8;
     const moe_status_t st = launch_logits<false>(x, W, H, V, p, s);
     if (st != MOE_OK) return st;
-    join_kernel<<<(T + kJoinTokens - 1) / kJoinTokens, 256, 0, s>>>(p.part, 2 * l.voc_tiles, p.at_label, labels, T, V,
-                                                                    ignore_index, loss, lse, err);
-    MOE_CHECK_LAUNCH();
-    return MOE_OK;
+    return moe::launch_after(join_kernel, dim3((T + kJoinTokens - 1) / kJoinTokens), 256, s,
+                             static_cast<const float2*>(p.part), p.shares * l.voc_tiles,
+                             static_cast<const float*>(p.at_label), labels, T, V, ignore_index, loss, lse, err);
 }
 
 extern "C" size_t moe_cross_entropy_backward_workspace_size(int T, int H, int V) {
@@ -658,7 +693,8 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
         p.v0 = i * l.piece;
         p.cols = V - p.v0 < l.piece ? V - p.v0 : l.piece;
         p.tok_tiles = (T + BT - 1) / BT;
-        p.bv = tile_width(p.cols, p.tok_tiles);
+        p.bt = T <= 128 ? 128 : BT;
+        p.bv = tile_width(p.cols, T);
         p.voc_tiles = (p.cols + p.bv - 1) / p.bv;
         p.ignore = ignore_index;
         p.lse = lse;
