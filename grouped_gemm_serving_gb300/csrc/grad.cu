@@ -6,13 +6,10 @@
 //   dgrad  dA[p, c] = sum_n dC[p, n] B[e, n, c]: the grouped GEMM kernel with
 //          B read in place as an MN-major operand (the c features contiguous);
 //          it writes zeros for the sentinel rows and never reads them.
-//   wgrad  dB[e, n, c] = sum over expert e's rows of dC[p, n] A[p, c]: the
-//          grouped GEMM's weight-gradient kernel reads dC and A in place as
-//          MN-major operands (tcgen05 cta_group::2, A's features as the MMA's
-//          256 rows and dC's as its columns, TMEM accumulators, TMA), 64 rows
-//          of the expert per k-block; the expert's last, partial k-block comes
-//          from a zero-padded copy of its cnt mod 64 last rows (the tails), so
-//          no k-block reaches into the next expert's rows.
+//   wgrad  dB[e, n, c] = sum over expert e's rows of dC[p, n] A[p, c]: wgrad.cu's
+//          kernel reads dC and A in place, 64 rows of the expert per k-block;
+//          the expert's last, partial k-block comes from a zero-padded copy of
+//          its cnt mod 64 last rows (the tails), made here.
 // Both run on the device from offsets: no host synchronisation.
 #include <climits>
 
@@ -26,7 +23,7 @@ constexpr int kTailCols = 512;   // columns per CTA of the tail copy
 
 // The tails of the weight gradient: for expert e with r = cnt_e mod 64 > 0,
 // rows [offsets[e + 1] - r, offsets[e + 1]) of X [M_cap, C] go to rows
-// [64e, 64e + r) of tail [64E, C] and rows [64e + r, 64e + 64) are zeroed.
+// [64e, 64e + r) of tail [64E, C], zeros after them up to a multiple of 16.
 // blockIdx.z picks the operand (0: dC, 1: A); a CTA copies kTailCols columns
 // of one expert with 16-byte loads and stores.  Offsets that are not a
 // monotone prefix within M_cap are reported and no row is read.
@@ -50,7 +47,7 @@ wgrad_tail_kernel(const uint16_t* __restrict__ dC, int N, const uint16_t* __rest
     const int r = (hi - lo) % 64;
     if (r == 0) return;   // every k-block of this expert is read in place
     constexpr int kVecs = kTailCols / 8;   // 16-byte vectors per row
-    for (int i = threadIdx.x; i < 64 * kVecs; i += blockDim.x) {
+    for (int i = threadIdx.x; i < (r + 15) / 16 * 16 * kVecs; i += blockDim.x) {
         const int j = i / kVecs, c = c0 + 8 * (i % kVecs);
         if (c >= C) continue;
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -98,5 +95,6 @@ extern "C" moe_status_t moe_grouped_gemm_wgrad(const void* A, const void* dC, co
         static_cast<const uint16_t*>(dC), N, static_cast<const uint16_t*>(A), K, offsets, E, M_cap,
         static_cast<uint16_t*>(ws), err);
     MOE_CHECK_LAUNCH();
-    return moe::wgrad_gemm(dC, N, A, ws, offsets, E, M_cap, N, K, dB, s);
+    const auto* tails = static_cast<const uint16_t*>(ws);
+    return moe::wgrad_gemm(dC, N, A, tails, tails + static_cast<size_t>(64) * E * N, offsets, E, M_cap, N, K, dB, s);
 }

@@ -31,7 +31,7 @@
 // features) and its accumulator holds weight row l % 64 for tokens
 // (l / 64) * N/2 + column in lane l, columns below N/2.  So is an expert's
 // last store tile with at most 128 of its 256 features (forward and data
-// gradient; the weight gradient keeps M = 256 there, which measured faster).
+// gradient).
 //
 // FP8 (and gathered A): single CTAs, 128 rows (tokens) x 256 columns
 // (weights), 48 KB per k-block, four deep.  Each 128-wide k-block is an exact
@@ -138,12 +138,6 @@ struct Params {
     const uint8_t* gx;
     const int32_t* sorted_rows;
     int T, topk;
-    // weight-gradient kernel (WG: pair, bf16 store): the "weights" are A
-    // [M_cap, out_cols] and the "tokens" dC [M_cap, wg_rows], both read
-    // MN-major over the expert's own rows; every expert has all
-    // wg_rows x out_cols output tiles over its own k-blocks; the output is
-    // [E, wg_rows, out_cols].
-    int wg_rows;
     // swapped store tiles only: the weights are MN-major, B [E, K, N] with
     // the N output features contiguous (the data gradient reads the forward
     // weights [E, N_fwd, K_fwd] in place this way)
@@ -164,13 +158,11 @@ struct Params {
     // tile of its own.  With C a range's product, the first launch sets
     // sum[range] [M_cap, N] = C and the others add to it; with a single range
     // the last launch stores out = row_scale[row] * (sum + C) instead.
-    // Weight gradient with EPI_SUM: out = row_scale[0] * C.
     float* sum;
     int sum_first, sum_last;
     const float* row_scale;
     int splits;
     int token_tiles;   // > 0: token tiles of every expert (else one per BT rows)
-    int no_tails;      // weight gradient: rows past the last expert's lie outside the tensor maps (zeros)
 };
 
 // Shared memory after the stage ring: barriers and the tile list (every
@@ -210,14 +202,10 @@ static_assert(smem_bytes<false, EPI_STORE>() <= 227 * 1024 && smem_bytes<false, 
 // Tensor maps over the token operand of the swapped kernels with boxes of
 // 8, 16, .., 128 rows: a CTA's half of a token tile is one box of exactly
 // its height.
-// The weight gradient puts its four operand maps in the first slots instead:
-// A and dC in place, then their zero-padded tails (64 features x 64 rows
-// boxes, MN-major).
 constexpr int kTokenMaps = 16;
 struct TokenMaps {
     CUtensorMap m[kTokenMaps];
 };
-constexpr int kWgA = 0, kWgC = 1, kWgTailA = 2, kWgTailC = 3, kWgMaps = 4;
 
 struct Tile {
     int e, row0, row_end, col0;
@@ -229,60 +217,35 @@ struct Tile {
     int nkb;    // the tile's k-blocks
     int kb0;    // EPI_SUM: its first k-block
     int split;  // EPI_SUM: its range of the contraction
-    int first;  // weight gradient: the expert's first row
 };
 
-// Weight gradient: every expert has the same wg_pair_mt(p) token tiles.
-__device__ __forceinline__ int wg_pair_mt(const Params& p) { return (p.wg_rows + BT - 1) / BT; }
-
-template <bool SWAP, bool WG = false, bool SUM = false>
+template <bool SWAP, bool SUM = false>
 __device__ __forceinline__ Tile decode_tile(int t, const Shared& S, const Params& p) {
-    static_assert(!WG || SWAP, "the weight gradient runs on CTA pairs");
-    int lo = 0, mt, local, split = 0;
-    if (SUM && !WG) {   // range-major: the tiles of a range run together
+    int split = 0;
+    if (SUM) {   // range-major: the tiles of a range run together
         const int per = S.prefix[p.E] * p.n_tiles;
         split = t / per;
         t -= split * per;
     }
-    if (WG) {
-        // every expert has mt x n_tiles tiles; S.prefix is its k-block prefix
-        mt = wg_pair_mt(p);
-        lo = t / (mt * p.n_tiles);
-        local = t - lo * mt * p.n_tiles;
-    } else {
-        int hi = p.E;  // largest e < E with prefix[e] * n_tiles <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (S.prefix[mid] * p.n_tiles <= t) lo = mid; else hi = mid;
-        }
-        mt = S.prefix[lo + 1] - S.prefix[lo];
-        local = t - S.prefix[lo] * p.n_tiles;
+    int lo = 0, hi = p.E;  // largest e < E with prefix[e] * n_tiles <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (S.prefix[mid] * p.n_tiles <= t) lo = mid; else hi = mid;
     }
+    const int mt = S.prefix[lo + 1] - S.prefix[lo];
+    const int local = t - S.prefix[lo] * p.n_tiles;
     Tile ti;
     ti.e = lo;
     ti.row_end = p.offsets[lo + 1];
-    ti.first = 0;
     ti.nkb = p.k_blocks;
     ti.kb0 = 0;
     ti.split = split;
-    if (SUM && !WG) {
+    if (SUM) {
         ti.kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * split / p.splits);
         ti.nkb = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (split + 1) / p.splits) - ti.kb0;
     }
     ti.half = false;
-    if (WG) {
-        // weight gradient on a pair: the tokens are the wg_rows output rows
-        // in tiles of BT; the contraction runs over the expert's own rows in
-        // k-blocks of 64 (S.prefix is the k-block prefix)
-        // (with EPI_SUM the column tiles are walked first: the pairs that run
-        // together share dC's columns, which would otherwise come from HBM
-        // once for every column tile)
-        ti.row0 = (SUM ? local / p.n_tiles : local % mt) * BT;
-        ti.rows = min(BT, p.wg_rows - ti.row0);
-        ti.row_end = p.wg_rows;
-        ti.first = p.offsets[lo];
-        ti.nkb = S.prefix[lo + 1] - S.prefix[lo];
-    } else if (SWAP) {
+    if (SWAP) {
         // an expert's tokens in mt tiles of equal size (a multiple of 16),
         // rather than full tiles and a small remainder that would still
         // stream the whole weight tile
@@ -294,9 +257,9 @@ __device__ __forceinline__ Tile decode_tile(int t, const Shared& S, const Params
         ti.row0 = p.offsets[lo] + (local % mt) * BM;
         ti.rows = 0;
     }
-    ti.col0 = (SUM && WG ? local % p.n_tiles : local / mt) * (SWAP ? (p.half ? kSwapFeatSwiglu : kSwapFeatStore) : (p.half ? BN / 2 : BN));
-    if (SWAP && p.half && !WG) ti.half = p.half - ti.col0 <= kSwapFeatSwiglu / 2;
-    else if (SWAP && !p.half && !p.fc && !WG) ti.half = p.N - ti.col0 <= kSwapFeatStore / 2;
+    ti.col0 = (local / mt) * (SWAP ? (p.half ? kSwapFeatSwiglu : kSwapFeatStore) : (p.half ? BN / 2 : BN));
+    if (SWAP && p.half) ti.half = p.half - ti.col0 <= kSwapFeatSwiglu / 2;
+    else if (SWAP && !p.fc) ti.half = p.N - ti.col0 <= kSwapFeatStore / 2;
     return ti;
 }
 
@@ -427,22 +390,20 @@ __device__ __forceinline__ int tile_step() { return PAIR ? gridDim.x >> 1 : grid
 // Tokens: one box of exactly the tile's N/2 rows (a multiple of 8, one
 // tensor map per height).  A TMA instruction costs the issuing thread many
 // cycles, so a k-block takes as few as possible.
-template <int EPI, bool WG>
+template <int EPI>
 __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, const CUtensorMap* tmW64,
                               uint8_t* stages, Shared& S, const Params& p, int total, uint32_t rank) {
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_par = 0;
     bool ok = true;
     for (int t = tile_first<true>(); ok && t < total; t += tile_step<true>()) {
-        const Tile ti = decode_tile<true, WG, EPI == EPI_SUM>(t, S, p);
+        const Tile ti = decode_tile<true, EPI == EPI_SUM>(t, S, p);
         const int nh = swap_n(ti) / 2;                 // token rows in each CTA: 8 .. 128
         const CUtensorMap* tmXh = &tmX->m[nh / 8 - 1];
         const int xrow = ti.row0 + static_cast<int>(rank) * nh;
-        // weight gradient: this CTA's nh columns of dC in one or two 64-wide boxes
-        const int xbytes = WG ? (nh > 64 ? 2 : 1) * 8192 : nh * 128;
+        const int xbytes = nh * 128;
         const int abytes = ti.half ? kStageA / 2 : kStageA;   // M = 128: 64 weight rows per CTA
-        const int nkb = WG || EPI == EPI_SUM ? ti.nkb : p.k_blocks;
-        const int nfull = WG ? (p.offsets[ti.e + 1] - ti.first + (p.no_tails ? 63 : 0)) / 64 : 0;   // k-blocks read in place
+        const int nkb = EPI == EPI_SUM ? ti.nkb : p.k_blocks;
         for (int kb = 0; kb < nkb; ++kb) {
             const bool got = moe::mbar_wait(bar(S.empty[stage]), phase ^ 1u, &S.abort_flag, kWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
@@ -452,24 +413,10 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
             const uint32_t fb = moe::map_to_cta(bar(S.full[stage]), 0);
             const uint32_t sa = moe::smem_u32(stages + stage * Geo<true, EPI>::kStageBytes);
             const uint32_t sb = sa + kStageA;
-            const int kc = (EPI == EPI_SUM && !WG ? ti.kb0 + kb : kb) * 64;
+            const int kc = (EPI == EPI_SUM ? ti.kb0 + kb : kb) * 64;
             if (moe::elect_one()) {
                 if (rank == 0) moe::mbar_arrive_expect_tx(bar(S.full[stage]), 2 * (abytes + xbytes));
-                if (WG) {
-                    // weight gradient: A's 128 features and dC's nh columns of
-                    // this CTA over 64 rows, as 64 x 64 MN-major swizzle atoms
-                    // 8 KB apart, from the expert's own rows or, for its
-                    // partial last k-block, from the zero-padded tails
-                    const bool in_place = kb < nfull;
-                    const CUtensorMap* ma = &tmX->m[in_place ? kWgA : kWgTailA];
-                    const CUtensorMap* mc = &tmX->m[in_place ? kWgC : kWgTailC];
-                    const int row = in_place ? ti.first + kc : ti.e * 64;
-                    const int f0 = ti.col0 + static_cast<int>(rank) * 128;
-                    moe::tma_load_2d_pair(sa, ma, fb, f0, row);
-                    moe::tma_load_2d_pair(sa + 8192, ma, fb, f0 + 64, row);
-                    moe::tma_load_2d_pair(sb, mc, fb, xrow, row);
-                    if (nh > 64) moe::tma_load_2d_pair(sb + 8192, mc, fb, xrow + 64, row);
-                } else if (plain_tiles(EPI) && p.mn_a) {
+                if (plain_tiles(EPI) && p.mn_a) {
                     // two 64-feature x 64-row swizzle atoms, 8 KB apart (one for M = 128)
                     const int f0 = ti.col0 + static_cast<int>(rank) * (ti.half ? 64 : 128);
                     moe::tma_load_3d_pair(sa, tmW, fb, f0, kc, ti.e);
@@ -483,7 +430,7 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
                 } else {   // 8 groups of (8 gate rows, 8 up rows) of this CTA's 64 features
                     moe::tma_load_5d_pair(sa, tmW, fb, kc, 0, 0, (ti.col0 + static_cast<int>(rank) * 64) / 8, ti.e);
                 }
-                if (!WG) moe::tma_load_2d_pair(sb, tmXh, fb, kc, xrow);
+                moe::tma_load_2d_pair(sb, tmXh, fb, kc, xrow);
             }
             __syncwarp();
             issued |= 1u << stage;
@@ -606,7 +553,7 @@ __device__ void producer_gather(const CUtensorMap* tmA, const CUtensorMap* tmB, 
     }
 }
 
-template <bool FP8, int EPI, bool SWAP, bool WG>
+template <bool FP8, int EPI, bool SWAP>
 __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int total, uint32_t tmem) {
     uint32_t idesc = moe::make_idesc(FP8 ? 0u : 1u, BM, BN);
     int stage = 0, acc = 0;
@@ -614,11 +561,10 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
     bool ok = true, issued = false;
     for (int t = tile_first<SWAP>(); ok && t < total; t += tile_step<SWAP>()) {
         if (SWAP) {
-            const Tile ti = decode_tile<true, WG, EPI == EPI_SUM>(t, S, p);
+            const Tile ti = decode_tile<true, EPI == EPI_SUM>(t, S, p);
             const int n = swap_n(ti);
             const int m = ti.half ? BM : 2 * BM;
-            idesc = WG ? moe::make_idesc_ab_mn(1u, 2 * BM, n)
-                 : plain_tiles(EPI) && p.mn_a ? moe::make_idesc_a_mn(1u, m, n) : moe::make_idesc(1u, m, n);
+            idesc = plain_tiles(EPI) && p.mn_a ? moe::make_idesc_a_mn(1u, m, n) : moe::make_idesc(1u, m, n);
         }
         if (!FP8) {
             // with a pair, the peer's epilogue arrives here from the other CTA
@@ -627,9 +573,7 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
             if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
             moe::tc_fence_after();
         }
-        // weight-gradient tiles of an expert without rows have no k-blocks:
-        // the accumulator is committed untouched and the epilogue writes zeros
-        const int nkb = WG || EPI == EPI_SUM ? decode_tile<SWAP, WG, EPI == EPI_SUM>(t, S, p).nkb : p.k_blocks;
+        const int nkb = EPI == EPI_SUM ? decode_tile<SWAP, EPI == EPI_SUM>(t, S, p).nkb : p.k_blocks;
         for (int kb = 0; kb < nkb; ++kb) {
             if (FP8) {
                 const bool got = moe::mbar_wait(bar(S.acc_empty[acc]), acc_phase ^ 1u, &S.abort_flag, kWaitNs);
@@ -640,14 +584,12 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
             if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
             moe::tc_fence_after();
             const uint32_t sa = moe::smem_u32(stages + stage * Geo<SWAP, EPI>::kStageBytes);
-            // MN-major operands (the data gradient's weights; both operands of
-            // the weight gradient): a K step of 16 rows is 2 KB further on;
-            // K-major: 32 bytes
-            const bool amn = WG || (SWAP && plain_tiles(EPI) && p.mn_a);
+            // MN-major weights (the data gradient's): a K step of 16 rows is 2 KB
+            // further on; K-major: 32 bytes
+            const bool amn = SWAP && plain_tiles(EPI) && p.mn_a;
             const uint64_t adesc = amn ? moe::smem_desc_sw128_mn(sa, 8192) : moe::smem_desc_sw128(sa);
             const uint64_t astep = amn ? 2048 >> 4 : 2;
-            const uint64_t bdesc = WG ? moe::smem_desc_sw128_mn(sa + kStageA, 8192) : moe::smem_desc_sw128(sa + kStageA);
-            const uint64_t bstep = WG ? 2048 >> 4 : 2;
+            const uint64_t bdesc = moe::smem_desc_sw128(sa + kStageA);
             const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
             // the same (lowest) lane is elected every time, so its commits
             // track all the MMAs it issued
@@ -657,7 +599,7 @@ __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int tota
                     if (FP8)
                         moe::mma_fp8(d, adesc + 2 * k, bdesc + 2 * k, idesc, k > 0);
                     else if (SWAP)
-                        moe::mma_bf16_pair(d, adesc + astep * k, bdesc + bstep * k, idesc, (kb | k) != 0);
+                        moe::mma_bf16_pair(d, adesc + astep * k, bdesc + 2 * k, idesc, (kb | k) != 0);
                     else
                         moe::mma_bf16(d, adesc + 2 * k, bdesc + 2 * k, idesc, (kb | k) != 0);
                 if (SWAP) moe::tc_commit_pair(bar(S.empty[stage]), 0x3);   // frees the stage in both CTAs
@@ -920,7 +862,7 @@ __device__ __forceinline__ void swiglu_half_tile(const Params& p, const Tile& ti
     }
 }
 
-template <bool FP8, int EPI, bool SWAP, bool WG>
+template <bool FP8, int EPI, bool SWAP>
 __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, uint32_t rank) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q = warp & 3;               // TMEM lane quarter this warp may access
@@ -939,7 +881,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
         acc_empty_leader[1] = moe::map_to_cta(bar(S.acc_empty[1]), 0);
     }
     for (int t = tile_first<SWAP>(); t < total; t += tile_step<SWAP>()) {
-        const Tile ti = decode_tile<SWAP, WG, EPI == EPI_SUM>(t, S, p);
+        const Tile ti = decode_tile<SWAP, EPI == EPI_SUM>(t, S, p);
         const int row = ti.row0 + r;
         const bool live = row < ti.row_end;
         if (SWAP) {
@@ -948,9 +890,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
             moe::tc_fence_after();
             const uint32_t ta = lane_base + static_cast<uint32_t>(acc * BN);
             const int ntok = swap_rows(ti);
-            // weight gradient: expert e's output rows start at e * wg_rows
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
-                                 (WG ? static_cast<int64_t>(ti.e) * p.wg_rows * p.out_cols : 0);
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
             if (!plain_tiles(EPI) && ti.half) {
                 swiglu_half_tile<EPI == EPI_SWIGLU_KEEP>(p, ti, ta, q, hsel, lane, rank);
             } else if (plain_tiles(EPI) && ti.half) {
@@ -961,19 +901,9 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
                     const int col = hsel * 128 + c * 32;
                     if (col >= ntok) break;                       // the same for the whole warp
                     uint32_t v[32];
-                    if (!WG || ti.nkb > 0) {
-                        moe::tmem_ld32(ta + col, v);
-                        moe::tmem_ld_wait();
-                    } else {   // an expert without rows: its weight gradient is zero
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
-                    }
-                    if (EPI == EPI_SUM && WG) {
-                        const float scale = p.row_scale[0];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(scale * __uint_as_float(v[i]));
-                    }
-                    if (EPI == EPI_SUM && !WG) {
+                    moe::tmem_ld32(ta + col, v);
+                    moe::tmem_ld_wait();
+                    if (EPI == EPI_SUM) {
                         sum_chunk(p, ti.split, ti.row0 + col, ti.col0 + static_cast<int>(rank) * 128 + q * 32 + lane,
                                   min(32, ntok - col), v);
                     } else if (plain_tiles(EPI)) {
@@ -1215,7 +1145,7 @@ __device__ void zero_sentinel_rows(const Params& p) {
     }
 }
 
-template <bool FP8, int EPI, bool SWAP, bool WG = false>
+template <bool FP8, int EPI, bool SWAP>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ TokenMaps tmX,
@@ -1244,19 +1174,16 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     }
     if (warp == 0) {
         // validate offsets and build the row-tile prefix (8 experts per lane)
-        int mt[8], kbl[8], sum = 0, ksum = 0, bad = 0;
+        int mt[8], sum = 0, bad = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = lane * 8 + i;
             mt[i] = 0;
-            kbl[i] = 0;
             if (e < p.E) {
                 const int lo = p.offsets[e], hi = p.offsets[e + 1];
                 if (hi < lo) bad = 1;
                 constexpr int RT = SWAP ? BT : BM;   // rows of an expert per tile
                 mt[i] = hi > lo ? (EPI == EPI_SUM && p.token_tiles ? p.token_tiles : (hi - lo + RT - 1) / RT) : 0;
-                if (WG) kbl[i] = hi > lo ? (hi - lo + 63) / 64 : 0;   // k-blocks of its rows
-                ksum += kbl[i];
                 sum += mt[i];
             }
         }
@@ -1271,29 +1198,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             if (lane >= off) incl += o;
         }
         int run = incl - sum;
-        if (!WG) {   // the weight gradient keeps its k-block prefix here instead
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int e = lane * 8 + i;
-                if (e < p.E) { S.prefix[e] = run; run += mt[i]; }
-            }
-            if (lane == 31) S.prefix[p.E] = incl;
+        for (int i = 0; i < 8; ++i) {
+            const int e = lane * 8 + i;
+            if (e < p.E) { S.prefix[e] = run; run += mt[i]; }
         }
-        if (WG) {
-            int kincl = ksum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, kincl, off);
-                if (lane >= off) kincl += o;
-            }
-            int krun = kincl - ksum;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int e = lane * 8 + i;
-                if (e < p.E) { S.prefix[e] = krun; krun += kbl[i]; }
-            }
-            if (lane == 31) S.prefix[p.E] = kincl;
-        }
+        if (lane == 31) S.prefix[p.E] = incl;
         if (lane == 0) {
             S.valid = !bad;
             if (bad && blockIdx.x == 0) moe::raise_device_error(p.err, MOE_DEVERR_OFFSETS);
@@ -1302,7 +1212,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         moe::prefetch_tensormap(&tmA);
         moe::prefetch_tensormap(&tmB);
         if (SWAP) {
-            for (int j = 0; j < (WG ? kWgMaps : kTokenMaps); ++j) moe::prefetch_tensormap(&tmX.m[j]);
+            for (int j = 0; j < kTokenMaps; ++j) moe::prefetch_tensormap(&tmX.m[j]);
         }
     }
     __syncthreads();
@@ -1322,16 +1232,15 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     moe::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     // tiles (pair tiles when SWAP)
-    const int total = WG ? p.E * wg_pair_mt(p) * p.n_tiles
-                         : S.prefix[p.E] * p.n_tiles * (EPI == EPI_SUM ? p.splits : 1);
+    const int total = S.prefix[p.E] * p.n_tiles * (EPI == EPI_SUM ? p.splits : 1);
 
     // FP8 promotion keeps 128 fp32 accumulators per epilogue thread: move
     // registers from warpgroup 0 (TMA, MMA) to the two epilogue warpgroups.
     // 128 * kRegsLow + 256 * kRegsHigh = 384 * 168, the launch allocation.
     if (warp >= 4) {
         if (FP8) moe::reg_alloc<kRegsHigh>();
-        epilogue<FP8, EPI, SWAP, WG>(S, p, total, tmem, rank);
-        if (!WG && EPI != EPI_SUM) zero_sentinel_rows<EPI>(p);
+        epilogue<FP8, EPI, SWAP>(S, p, total, tmem, rank);
+        if (EPI != EPI_SUM) zero_sentinel_rows<EPI>(p);
         if (SWAP && EPI == EPI_STORE && p.fc) fused_combine_empty_tokens(p);
     } else {
         if (FP8) moe::reg_dealloc<kRegsLow>();
@@ -1339,10 +1248,10 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             producer_gather<FP8, EPI>(&tmA, &tmB, stages, S, p, total, warp == 0 ? 0 : warp - 1);
             __syncwarp();
         } else if (warp == 0) {
-            if (SWAP) producer_swap<EPI, WG>(&tmX, &tmB, &tmA, stages, S, p, total, rank);
+            if (SWAP) producer_swap<EPI>(&tmX, &tmB, &tmA, stages, S, p, total, rank);
             else producer<FP8, EPI>(&tmA, &tmB, stages, S, p, total);
         } else if (warp == 1) {
-            if (rank == 0) mma_issuer<FP8, EPI, SWAP, WG>(stages, S, p, total, tmem);
+            if (rank == 0) mma_issuer<FP8, EPI, SWAP>(stages, S, p, total, tmem);
         }
     }
     moe::tc_fence_before();
@@ -1396,10 +1305,10 @@ bool encode_token_maps(TokenMaps* t, const void* base, const cuuint64_t* dims, c
     return true;
 }
 
-template <bool FP8, int EPI, bool SWAP = false, bool WG = false>
+template <bool FP8, int EPI, bool SWAP = false>
 moe_status_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const TokenMaps& tmX, const Params& p,
                     cudaStream_t s) {
-    auto kern = grouped_gemm_kernel<FP8, EPI, SWAP, WG>;
+    auto kern = grouped_gemm_kernel<FP8, EPI, SWAP>;
     constexpr size_t kSmemBytes = smem_bytes<SWAP, EPI>();
     static int configured[64] = {0};
     int dev = 0;
@@ -1565,7 +1474,6 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
     p.sorted_rows = sorted_rows;
     p.T = gx ? T : 0;
     p.topk = gx ? topk : 1;
-    p.wg_rows = 0;
     p.mn_a = weights_mn ? 1 : 0;
     p.fc = 0;
     p.keep = keep;
@@ -1687,58 +1595,6 @@ moe_status_t moe::swiglu_keep_gemm(const void* x, const void* W1, const int32_t*
                                    int K, void* Y1, void* h, cudaStream_t s) {
     return run_grouped_gemm(MOE_BF16, x, nullptr, nullptr, nullptr, 0, 0, W1, nullptr, offsets, E, M_cap, N, K,
                             MOE_EPI_SWIGLU, h, nullptr, reinterpret_cast<moe_stream_t>(s), false, nullptr, Y1);
-}
-
-moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, const void* tails, const int32_t* offsets,
-                             int E, int M_cap, int N, int K, void* dB, cudaStream_t s, const float* scale) {
-    // dB[e] [N, K] = dC_e^T A_e over expert e's rows.  Swapped operands on CTA
-    // pairs: A supplies the MMA's M rows (the output features, 256 per pair
-    // tile), dC its N columns (the output rows, in tiles of up to 256); both
-    // are read MN-major, 64 features x 64 rows per box, from their own rows or,
-    // for an expert's partial last k-block, from the zero-padded tails.
-    MOE_CHECK_ARG(dC && A && (tails || E == 1) && offsets && dB && E >= 1 && E <= kMaxE && M_cap >= 1);
-    MOE_CHECK_ARG(N >= 1 && ldc >= N && ldc % 8 == 0 && K >= 8 && K % 8 == 0);
-    MOE_CHECK_ARG(moe::aligned16(dC) && moe::aligned16(A) && moe::aligned16(tails) && moe::aligned16(dB));
-    MOE_CHECK_ARG(static_cast<int64_t>(E) * N < INT_MAX);
-    const int n_tiles = (K + kSwapFeatStore - 1) / kSwapFeatStore;
-    MOE_CHECK_ARG(static_cast<int64_t>(E) * ((N + BT - 1) / BT) * n_tiles < INT_MAX);
-    int* err = moe::device_error_word();
-    if (!err) return MOE_ERR_CUDA;
-    TokenMaps tmX{};
-    const cuuint32_t box[2] = {64, 64};
-    const uint8_t* tail_c = static_cast<const uint8_t*>(tails);
-    const uint8_t* tail_a = tails ? tail_c + static_cast<size_t>(64) * E * N * 2 : nullptr;
-    const struct { const void* base; int cols, ld; cuuint64_t rows; } ops[4] = {
-        {A, K, K, static_cast<cuuint64_t>(M_cap)}, {dC, N, ldc, static_cast<cuuint64_t>(M_cap)},
-        {tail_a, K, K, static_cast<cuuint64_t>(64) * E}, {tail_c, N, N, static_cast<cuuint64_t>(64) * E}};
-    for (int i = 0; i < kWgMaps; ++i) {
-        if (!tails && i >= kWgTailA) {   // never loaded
-            tmX.m[i] = tmX.m[kWgA];
-            continue;
-        }
-        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(ops[i].cols), ops[i].rows};
-        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ops[i].ld) * 2};
-        if (!encode_tile_map(&tmX.m[i], false, ops[i].base, 2, dims, strides, box)) return MOE_ERR_CUDA;
-    }
-    Params p{};
-    p.offsets = offsets;
-    p.out = dB;
-    p.err = err;
-    p.E = E;
-    p.M_cap = M_cap;
-    p.N = K;
-    p.K = 64;
-    p.half = 0;
-    p.out_cols = K;
-    p.n_tiles = n_tiles;
-    p.k_blocks = 0;
-    p.nb_scale = 0;
-    p.topk = 1;
-    p.wg_rows = N;
-    p.no_tails = tails ? 0 : 1;
-    p.row_scale = scale;
-    if (scale) return launch<false, EPI_SUM, true, true>(tmX.m[kWgA], tmX.m[kWgC], tmX, p, s);
-    return launch<false, EPI_STORE, true, true>(tmX.m[kWgA], tmX.m[kWgC], tmX, p, s);
 }
 
 extern "C" moe_status_t moe_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_scales,

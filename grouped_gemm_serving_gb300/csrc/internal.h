@@ -15,18 +15,19 @@ namespace moe {
 moe_status_t dgrad_gemm(const void* dC, const void* B, const int32_t* offsets, int E, int M_cap, int N, int K,
                         void* dA, cudaStream_t stream);
 
-// Launches the grouped GEMM's weight-gradient kernel on CTA pairs (grouped_gemm.cu):
+// Launches the weight-gradient GEMM (wgrad.cu):
 //   dB[e, n, c] = sum over expert e's rows p of dC[p, n] * A[p, c]
-// with dC bf16 [M_cap, N] and A bf16 [M_cap, K] read in place (MN-major), in
-// 64-row k-blocks from offsets[e]; rows of dC start ldc elements apart.  An expert's last, partial k-block
-// (cnt_e mod 64 rows, cnt_e = offsets[e + 1] - offsets[e]) comes instead from
-// rows [64e, 64e + 64) of the tails, zero-padded copies of those rows:
-// dC's bf16 [64E, N] followed by A's bf16 [64E, K].  dB bf16 [E, N, K]; an
-// expert without rows gets zeros.  tails NULL: a single expert of exactly M_cap
-// rows, whose last k-block reads zeros from outside the tensor maps.  scale (one
-// float on the device) multiplies dB in fp32 before it is rounded.
-moe_status_t wgrad_gemm(const void* dC, int ldc, const void* A, const void* tails, const int32_t* offsets, int E,
-                        int M_cap, int N, int K, void* dB, cudaStream_t stream, const float* scale = nullptr);
+// with dC bf16 [M_cap, N] (rows ldc elements apart) and A bf16 [M_cap, K] read
+// in place in 64-row k-blocks from offsets[e].  An expert's last, partial
+// k-block (r = cnt_e mod 64 rows) comes instead from rows [64e, 64e + r) of the
+// tails, copies of those rows of dC and A (bf16 [64E, N] and [64E, K]) with zeros
+// up to the next multiple of 16.  Tails NULL: a single expert of exactly M_cap
+// rows, whose last k-block reads zeros from outside the tensor maps.  dB bf16
+// [E, N, K]; an expert without rows gets zeros.  scale (one float on the
+// device, or NULL) multiplies dB in fp32 before it is rounded.
+moe_status_t wgrad_gemm(const void* dC, int ldc, const void* A, const void* tail_c, const void* tail_a,
+                        const int32_t* offsets, int E, int M_cap, int N, int K, void* dB, cudaStream_t stream,
+                        const float* scale = nullptr);
 
 // The data gradient of one expert of M rows, its contraction split over
 // several launches and, within one, over `splits` ranges (grouped_gemm.cu): with

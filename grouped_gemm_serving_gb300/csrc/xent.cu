@@ -708,7 +708,7 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
             return st;
         if (dW) {
             auto* dWp = static_cast<__nv_bfloat16*>(dW) + static_cast<int64_t>(p.v0) * H;
-            st = moe::wgrad_gemm(G, l.ldg, xs, nullptr, offsets, 1, T, p.cols, H, dWp, s, scale + T);
+            st = moe::wgrad_gemm(G, l.ldg, xs, nullptr, nullptr, offsets, 1, T, p.cols, H, dWp, s, scale + T);
             if (st != MOE_OK) return st;
         }
     }
