@@ -443,10 +443,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // The gated block's activation and its gradient, from the pre-activations g and
 // u and the gradient d of h = silu(g) * u:  with s = 1 / (1 + exp(-g)),
 //   du = d g s,   dg = d u s (1 + g (1 - s)).
-// For g far below zero exp(-g) overflows to infinity and s is 0, so all three
-// are 0 (times a finite factor), their limits.
+// The results are rounded to bf16, so a reciprocal and an exponential of a few
+// units in 2^-23 will do.  For g far below zero exp(-g) overflows to infinity and
+// s is 0, so all three are 0 (times a finite factor), their limits.
 __device__ __forceinline__ void swiglu_grad(float d, float g, float u, float& dg, float& du, float& h) {
-    const float s = 1.0f / (1.0f + __expf(-g));
+    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
     const float a = g * s;
     h = a * u;
     du = d * a;

@@ -91,18 +91,27 @@ constexpr int kStageB = BN * 128;
 // EPI_SWIGLU_KEEP: EPI_SWIGLU that also stores the pre-activations (swapped
 // bf16 only; an instance of its own, so that the inference kernel carries none
 // of it).  EPI_SUM: a store whose sum over several launches is held in fp32
-// (swapped data gradient only; see Params::sum).
-enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_Q = 2, EPI_SWIGLU_KEEP = 3, EPI_SUM = 4 };
-__host__ __device__ constexpr bool plain_tiles(int epi) { return epi == EPI_STORE || epi == EPI_SUM; }
+// (swapped data gradient only; see Params::sum).  EPI_SWIGLU_BACK: the data
+// gradient of fc2 with the gradient of silu(gate) * up applied to it (see
+// Params::Y1).
+enum Epi {
+    EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_Q = 2, EPI_SWIGLU_KEEP = 3, EPI_SUM = 4, EPI_SWIGLU_BACK = 5
+};
+// One output feature per weight row (not gate and up rows interleaved).
+__host__ __device__ constexpr bool plain_tiles(int epi) {
+    return epi == EPI_STORE || epi == EPI_SUM || epi == EPI_SWIGLU_BACK;
+}
 
 // Stage ring: a single-CTA tile stages 128 A + 256 B rows (48 KB) four deep;
 // a CTA of a pair stages up to 128 + 128 rows (32 KB) seven deep: its
 // epilogues need no shared memory beyond the ring and the barriers (pair
 // kernels allocate no Aux block, see smem_bytes).
 constexpr int kMaxStages = 7;
+// EPI_SWIGLU_BACK gives one stage to its warps' transposes.
+constexpr int kTransposeBytes = 32 * 128;   // a warp's 32 tokens x 32 fp32 features
 template <bool PAIR, int EPI>
 struct Geo {
-    static constexpr int kStages = PAIR ? 7 : 4;
+    static constexpr int kStages = EPI == EPI_SWIGLU_BACK ? 6 : PAIR ? 7 : 4;
     static constexpr int kStageBytes = PAIR ? kStageA + kStageB / 2 : kStageA + kStageB;
 };
 constexpr int kMaxE = 256;
@@ -162,6 +171,17 @@ struct Params {
     int sum_first, sum_last;
     const float* row_scale;
     int splits;
+    // EPI_SWIGLU_BACK: out is unused.  With d the tile's gradient of h, feature
+    // f < out_cols of row p:  dY1[p, f] = dg, dY1[p, out_cols + f] = du and
+    // h[p, f] = silu(g) u from Y1[p] = [g | u] [M_cap, 2 out_cols].  Rows of an
+    // expert's last, partial 64 rows go to the tails too, and the idle warps
+    // copy those rows of x and dy [M_cap, dy_cols] there (weight gradients).
+    const __nv_bfloat16* Y1;
+    __nv_bfloat16 *dY1, *h;
+    const uint4 *x, *dy;
+    int dy_cols;
+    __nv_bfloat16 *tail_dY1, *tail_h;
+    uint4 *tail_x, *tail_dy;
     int token_tiles;   // > 0: token tiles of every expert (else one per BT rows)
 };
 
@@ -193,10 +213,12 @@ template <bool PAIR, int EPI>
 constexpr size_t smem_bytes() {
     using G = Geo<PAIR, EPI>;
     constexpr bool with_aux = !PAIR;
-    return 1024 + static_cast<size_t>(G::kStages) * G::kStageBytes + sizeof(Shared) + (with_aux ? sizeof(Aux) : 0);
+    return 1024 + static_cast<size_t>(G::kStages) * G::kStageBytes + sizeof(Shared) + (with_aux ? sizeof(Aux) : 0) +
+           (EPI == EPI_SWIGLU_BACK ? 8 * kTransposeBytes : 0);
 }
 static_assert(smem_bytes<false, EPI_STORE>() <= 227 * 1024 && smem_bytes<false, EPI_SWIGLU_Q>() <= 227 * 1024 &&
-                  smem_bytes<true, EPI_STORE>() <= 227 * 1024 && smem_bytes<true, EPI_SWIGLU>() <= 227 * 1024,
+                  smem_bytes<true, EPI_STORE>() <= 227 * 1024 && smem_bytes<true, EPI_SWIGLU>() <= 227 * 1024 &&
+                  smem_bytes<true, EPI_SWIGLU_BACK>() <= 227 * 1024,
               "shared memory per CTA");
 
 // Tensor maps over the token operand of the swapped kernels with boxes of
@@ -784,12 +806,98 @@ __device__ __forceinline__ void sum_chunk(const Params& p, int split, int64_t ro
         }
 }
 
+// EPI_SWIGLU_BACK: the gradient of the activation on 32 features x n tokens
+// whose gradients of h are in v (a feature a lane, a token a register), rows
+// row.. of expert e and features f0...  Through the warp's transpose buffer,
+// rows of 32 features whose 16-byte pieces are permuted by the token, a lane
+// gets 8 features of 4 tokens, so that Y1, dY1 and h move in 16-byte vectors.
+struct GateUp {
+    uint4 g[4], u[4];
+};
+__device__ __forceinline__ void load_gate_up(const Params& p, int64_t row, int f0, int n, GateUp& gu) {
+    const int lane = threadIdx.x & 31, f = f0 + 8 * (lane & 3), I = p.out_cols;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        gu.g[i] = gu.u[i] = make_uint4(0, 0, 0, 0);
+        if (f < I && r < n) {
+            const __nv_bfloat16* y = p.Y1 + (row + r) * 2 * I + f;
+            gu.g[i] = __ldg(reinterpret_cast<const uint4*>(y));
+            gu.u[i] = __ldg(reinterpret_cast<const uint4*>(y + I));
+        }
+    }
+}
+__device__ __forceinline__ void swiglu_back_chunk(const Params& p, const Tile& ti, float* buf, int64_t row, int f0,
+                                                  int n, const uint32_t (&v)[32], const GateUp& gu) {
+    const int lane = threadIdx.x & 31;
+    const int f = f0 + 8 * (lane & 3), I = p.out_cols;
+    const bool in = f < I;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        buf[j * 32 + (((lane >> 2) ^ (j & 7)) << 2) + (lane & 3)] = __uint_as_float(v[j]);
+    __syncwarp();
+    const int cnt = p.offsets[ti.e + 1] - p.offsets[ti.e];
+    const int tail0 = ti.row_end - cnt % 64;   // the expert's first row that is in its tails
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        const float4* d4 = reinterpret_cast<const float4*>(buf + r * 32);
+        const float4 da = d4[(2 * (lane & 3)) ^ (r & 7)], db = d4[(2 * (lane & 3) + 1) ^ (r & 7)];
+        const float d[8] = {da.x, da.y, da.z, da.w, db.x, db.y, db.z, db.w};
+        const uint32_t gw[4] = {gu.g[i].x, gu.g[i].y, gu.g[i].z, gu.g[i].w};
+        const uint32_t uw[4] = {gu.u[i].x, gu.u[i].y, gu.u[i].z, gu.u[i].w};
+        uint32_t dg[4], du[4], h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float dgl, dul, hl, dgh, duh, hh;
+            moe::swiglu_grad(d[2 * j], moe::bf16_lo(gw[j]), moe::bf16_lo(uw[j]), dgl, dul, hl);
+            moe::swiglu_grad(d[2 * j + 1], moe::bf16_hi(gw[j]), moe::bf16_hi(uw[j]), dgh, duh, hh);
+            dg[j] = moe::pack_bf16x2(dgl, dgh);
+            du[j] = moe::pack_bf16x2(dul, duh);
+            h[j] = moe::pack_bf16x2(hl, hh);
+        }
+        if (!in || r >= n) continue;
+        const auto put = [&](__nv_bfloat16* dY1, __nv_bfloat16* hout, int64_t at) {
+            *reinterpret_cast<uint4*>(dY1 + at * 2 * I + f) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+            *reinterpret_cast<uint4*>(dY1 + at * 2 * I + I + f) = make_uint4(du[0], du[1], du[2], du[3]);
+            *reinterpret_cast<uint4*>(hout + at * I + f) = make_uint4(h[0], h[1], h[2], h[3]);
+        };
+        put(p.dY1, p.h, row + r);
+        if (row + r >= tail0) put(p.tail_dY1, p.tail_h, 64ll * ti.e + (row + r - tail0));
+    }
+    __syncwarp();
+}
+
+// EPI_SWIGLU_BACK, two idle warps of every CTA: the tails of x and dy, and the
+// zeros that fill each of the four tails up to a multiple of 16 rows.
+__device__ void make_tails(const Params& p, int warp) {
+    const int lane = threadIdx.x & 31;
+    const int nwarps = gridDim.x * 2;
+    const int vd = p.dy_cols / 8, vi = p.out_cols / 8;   // 16-byte vectors of a row of x and dy, and of h
+    for (int w = blockIdx.x * 2 + warp; w < p.E * 64; w += nwarps) {
+        const int e = w >> 6, j = w & 63;
+        const int hi = p.offsets[e + 1], r = (hi - p.offsets[e]) % 64;
+        if (j >= (r + 15) / 16 * 16) continue;
+        const int64_t src = hi - r + j;
+        for (int c = lane; c < vd; c += 32) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            if (p.x) p.tail_x[static_cast<int64_t>(w) * vd + c] = j < r ? __ldg(p.x + src * vd + c) : zero;
+            p.tail_dy[static_cast<int64_t>(w) * vd + c] = j < r ? __ldg(p.dy + src * vd + c) : zero;
+        }
+        if (j < r) continue;
+        for (int c = lane; c < 2 * vi; c += 32) {
+            reinterpret_cast<uint4*>(p.tail_dY1)[static_cast<int64_t>(w) * 2 * vi + c] = make_uint4(0, 0, 0, 0);
+            if (c < vi) reinterpret_cast<uint4*>(p.tail_h)[static_cast<int64_t>(w) * vi + c] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 // Store M = 128 tile (forward and data gradient): lane l of this CTA holds
 // weight row (output feature) l % 64 for token (l / 64) * nh + column, columns
 // below nh = N/2.  Each half of the epilogue takes 64 columns.
 template <int EPI>
 __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti, uint32_t ta, int q, int hsel,
-                                                int lane, uint32_t rank) {
+                                                int lane, uint32_t rank, float* buf) {
     const int nh = swap_n(ti) / 2, tok0 = (q >> 1) * nh, ntok = ti.rows;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
     const int f = ti.col0 + static_cast<int>(rank) * 64 + (q & 1) * 32 + lane;
@@ -803,6 +911,10 @@ __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti,
         moe::tmem_ld_wait();
         if (EPI == EPI_SUM) {
             sum_chunk(p, ti.split, ti.row0 + tok0 + col, f, jmax, v);
+        } else if (EPI == EPI_SWIGLU_BACK) {
+            GateUp gu;
+            load_gate_up(p, ti.row0 + tok0 + col, f - lane, jmax, gu);
+            swiglu_back_chunk(p, ti, buf, ti.row0 + tok0 + col, f - lane, jmax, v, gu);
         } else if (f < p.out_cols) {
             __nv_bfloat16* o = out + static_cast<int64_t>(ti.row0 + tok0 + col) * p.out_cols + f;
 #pragma unroll
@@ -874,6 +986,8 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
     uint32_t cph = 0;                    // fused combine barrier phase
     const int KB = p.k_blocks;
 
+    // the warp's transpose buffer (EPI_SWIGLU_BACK)
+    float* buf = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&S) + sizeof(Shared) + (warp - 4) * kTransposeBytes);
     // the pair's MMA waits for both CTAs' epilogues on the leader's barrier
     uint32_t acc_empty_leader[2] = {0, 0};
     if (SWAP) {
@@ -886,6 +1000,10 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
         const bool live = row < ti.row_end;
         if (SWAP) {
             // accumulator lane = weight row, column = token of the tile
+            const int back_f0 = ti.col0 + static_cast<int>(rank) * 128 + q * 32;
+            GateUp gu;   // the pre-activations of a chunk are fetched a chunk ahead
+            if (EPI == EPI_SWIGLU_BACK && !ti.half)
+                load_gate_up(p, ti.row0 + hsel * 128, back_f0, min(32, ti.rows - hsel * 128), gu);
             if (!moe::mbar_wait(bar(S.acc_full[acc]), acc_phase, &S.abort_flag, kWaitNs)) { fail(S, p); return; }
             moe::tc_fence_after();
             const uint32_t ta = lane_base + static_cast<uint32_t>(acc * BN);
@@ -894,7 +1012,19 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
             if (!plain_tiles(EPI) && ti.half) {
                 swiglu_half_tile<EPI == EPI_SWIGLU_KEEP>(p, ti, ta, q, hsel, lane, rank);
             } else if (plain_tiles(EPI) && ti.half) {
-                store_half_tile<EPI>(p, ti, ta, q, hsel, lane, rank);
+                store_half_tile<EPI>(p, ti, ta, q, hsel, lane, rank, buf);
+            } else if (EPI == EPI_SWIGLU_BACK) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const int col = hsel * 128 + c * 32;
+                    if (col >= ntok) break;                       // the same for the whole warp
+                    uint32_t v[32];
+                    moe::tmem_ld32(ta + col, v);
+                    const GateUp now = gu;
+                    if (c < 3) load_gate_up(p, ti.row0 + col + 32, back_f0, min(32, ntok - col - 32), gu);
+                    moe::tmem_ld_wait();
+                    swiglu_back_chunk(p, ti, buf, ti.row0 + col, back_f0, min(32, ntok - col), v, now);
+                }
             } else {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -1240,7 +1370,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     if (warp >= 4) {
         if (FP8) moe::reg_alloc<kRegsHigh>();
         epilogue<FP8, EPI, SWAP>(S, p, total, tmem, rank);
-        if (EPI != EPI_SUM) zero_sentinel_rows<EPI>(p);
+        if (EPI != EPI_SUM && EPI != EPI_SWIGLU_BACK) zero_sentinel_rows<EPI>(p);
         if (SWAP && EPI == EPI_STORE && p.fc) fused_combine_empty_tokens(p);
     } else {
         if (FP8) moe::reg_dealloc<kRegsLow>();
@@ -1252,6 +1382,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             else producer<FP8, EPI>(&tmA, &tmB, stages, S, p, total);
         } else if (warp == 1) {
             if (rank == 0) mma_issuer<FP8, EPI, SWAP>(stages, S, p, total, tmem);
+        } else if (EPI == EPI_SWIGLU_BACK) {
+            make_tails(p, warp - 2);
         }
     }
     moe::tc_fence_before();
@@ -1361,13 +1493,16 @@ struct FusedCombine {
 
 // With weights_mn (bf16 store only) B is [E, K, N], read MN-major.  With fc
 // (bf16 store only) the weighted combine is fused into the epilogue.  With keep
-// (bf16 SwiGLU only) the pre-activations are stored too, bf16 [M_cap, N].
+// (bf16 SwiGLU only) the pre-activations are stored too, bf16 [M_cap, N].  With
+// back (weights_mn only) the gradient of the activation is applied to the
+// product and C is not written.
 moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_scales, const void* gx,
                               const int32_t* sorted_rows, int T, int topk, const void* B,
                               const float* B_scales, const int32_t* offsets, int E, int M_cap, int N, int K,
                               moe_epilogue_t epilogue, void* C, float* C_scales, moe_stream_t stream,
-                              bool weights_mn = false, const FusedCombine* fc = nullptr, void* keep = nullptr) {
-    MOE_CHECK_ARG(A && B && offsets && C && E >= 1 && E <= kMaxE && M_cap >= 1 && N >= 8 && K >= 8);
+                              bool weights_mn = false, const FusedCombine* fc = nullptr, void* keep = nullptr,
+                              const moe::SwigluBack* back = nullptr) {
+    MOE_CHECK_ARG(A && B && offsets && (C || back) && E >= 1 && E <= kMaxE && M_cap >= 1 && N >= 8 && K >= 8);
     MOE_CHECK_ARG(moe::aligned16(A) && moe::aligned16(B) && moe::aligned16(C));
     const bool fp8 = dtype == MOE_FP8_E4M3_B128;
     if (!fp8 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
@@ -1478,6 +1613,20 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
     p.fc = 0;
     p.keep = keep;
     if (keep && (fp8 || !swiglu || gx)) return MOE_ERR_UNSUPPORTED;
+    if (back) {
+        if (!weights_mn) return MOE_ERR_UNSUPPORTED;
+        p.Y1 = static_cast<const __nv_bfloat16*>(back->Y1);
+        p.dY1 = static_cast<__nv_bfloat16*>(back->dY1);
+        p.h = static_cast<__nv_bfloat16*>(back->h);
+        p.x = static_cast<const uint4*>(back->x);
+        p.dy = static_cast<const uint4*>(A);
+        p.dy_cols = K;
+        p.tail_dY1 = static_cast<__nv_bfloat16*>(back->tail_dY1);
+        p.tail_h = static_cast<__nv_bfloat16*>(back->tail_h);
+        p.tail_x = static_cast<uint4*>(back->tail_x);
+        p.tail_dy = static_cast<uint4*>(back->tail_dy);
+        return launch<false, EPI_SWIGLU_BACK, true>(tmA, tmB, tmX, p, reinterpret_cast<cudaStream_t>(stream));
+    }
     if (fc) {
         if (fp8 || swiglu || gx || weights_mn) return MOE_ERR_UNSUPPORTED;
         p.fc = 1;
@@ -1515,6 +1664,13 @@ moe_status_t moe::dgrad_gemm(const void* dC, const void* B, const int32_t* offse
     // MN-major in place
     return run_grouped_gemm(MOE_BF16, dC, nullptr, nullptr, nullptr, 0, 0, B, nullptr, offsets, E, M_cap, K, N,
                             MOE_EPI_STORE, dA, nullptr, reinterpret_cast<moe_stream_t>(s), true);
+}
+
+moe_status_t moe::swiglu_back_gemm(const void* dy, const void* W2, const int32_t* offsets, int E, int M_cap, int H,
+                                   int I, const SwigluBack& back, cudaStream_t s) {
+    return run_grouped_gemm(MOE_BF16, dy, nullptr, nullptr, nullptr, 0, 0, W2, nullptr, offsets, E, M_cap, I, H,
+                            MOE_EPI_STORE, nullptr, nullptr, reinterpret_cast<moe_stream_t>(s), true, nullptr, nullptr,
+                            &back);
 }
 
 // How dgrad_sum_gemm cuts M rows x K features over a contraction of N: token

@@ -15,6 +15,21 @@ namespace moe {
 moe_status_t dgrad_gemm(const void* dC, const void* B, const int32_t* offsets, int E, int M_cap, int N, int K,
                         void* dA, cudaStream_t stream);
 
+// The data gradient of fc2 with the gradient of silu(gate) * up applied to it
+// in the epilogue (grouped_gemm.cu): with dh[p] = dy[p] W2[e] in fp32 and
+// Y1[p] = [g | u],  dY1[p] = [dg | du] and h[p] = silu(g) u, all bf16 (M_cap rows
+// of 2I, 2I and I; dy M_cap rows of H, W2 [E, H, I]).  Rows p >= offsets[E] are
+// neither read nor written.  The kernel also makes the tails (see wgrad_gemm)
+// of dY1, h, x (M_cap rows of H; NULL: none) and dy, 64E rows of the same widths.
+struct SwigluBack {
+    const void* Y1;
+    void *dY1, *h;
+    const void* x;
+    void *tail_dY1, *tail_h, *tail_x, *tail_dy;
+};
+moe_status_t swiglu_back_gemm(const void* dy, const void* W2, const int32_t* offsets, int E, int M_cap, int H, int I,
+                              const SwigluBack& back, cudaStream_t stream);
+
 // Launches the weight-gradient GEMM (wgrad.cu):
 //   dB[e, n, c] = sum over expert e's rows p of dC[p, n] * A[p, c]
 // with dC bf16 [M_cap, N] (rows ldc elements apart) and A bf16 [M_cap, K] read
