@@ -107,11 +107,12 @@ __host__ __device__ constexpr bool plain_tiles(int epi) {
 // epilogues need no shared memory beyond the ring and the barriers (pair
 // kernels allocate no Aux block, see smem_bytes).
 constexpr int kMaxStages = 7;
-// EPI_SWIGLU_BACK gives one stage to its warps' transposes.
+// EPI_SWIGLU_BACK and EPI_SWIGLU_KEEP give one stage to their warps' transposes.
+__host__ __device__ constexpr bool transposes(int epi) { return epi == EPI_SWIGLU_BACK || epi == EPI_SWIGLU_KEEP; }
 constexpr int kTransposeBytes = 32 * 128;   // a warp's 32 tokens x 32 fp32 features
 template <bool PAIR, int EPI>
 struct Geo {
-    static constexpr int kStages = EPI == EPI_SWIGLU_BACK ? 6 : PAIR ? 7 : 4;
+    static constexpr int kStages = transposes(EPI) ? 6 : PAIR ? 7 : 4;
     static constexpr int kStageBytes = PAIR ? kStageA + kStageB / 2 : kStageA + kStageB;
 };
 constexpr int kMaxE = 256;
@@ -214,7 +215,7 @@ constexpr size_t smem_bytes() {
     using G = Geo<PAIR, EPI>;
     constexpr bool with_aux = !PAIR;
     return 1024 + static_cast<size_t>(G::kStages) * G::kStageBytes + sizeof(Shared) + (with_aux ? sizeof(Aux) : 0) +
-           (EPI == EPI_SWIGLU_BACK ? 8 * kTransposeBytes : 0);
+           (transposes(EPI) ? 8 * kTransposeBytes : 0);
 }
 static_assert(smem_bytes<false, EPI_STORE>() <= 227 * 1024 && smem_bytes<false, EPI_SWIGLU_Q>() <= 227 * 1024 &&
                   smem_bytes<true, EPI_STORE>() <= 227 * 1024 && smem_bytes<true, EPI_SWIGLU>() <= 227 * 1024 &&
@@ -924,16 +925,35 @@ __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti,
     }
 }
 
-// Pre-activations kept for the backward pass: a lane's 32 tokens of its own
-// gate (r = 0) or up (r = 1) row of feature f.  Eight neighbouring lanes hold
-// eight neighbouring features of one, so a warp store fills two 32-byte
-// sectors, one of the gate half and one of the up half.
-__device__ __forceinline__ void keep_chunk(const Params& p, int64_t row, int f, int r, int n, const uint32_t (&v)[32]) {
-    if (f >= p.out_cols) return;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.keep) + row * p.N + r * p.half + f;
+// EPI_SWIGLU_KEEP: 32 accumulator lanes (the gate and up rows of 16 features
+// from f0 on, interleaved in groups of 8) x n tokens from row on.  Through the
+// warp's transpose buffer, rows of 32 fp32 values whose 16-byte pieces are
+// permuted by the token, a lane gets 4 features of 4 tokens: h as the inference
+// epilogue computes it, and the pre-activations beside it, in 8-byte stores that
+// fill 32-byte sectors four lanes at a time.
+__device__ __forceinline__ void keep_chunk(const Params& p, float* buf, int64_t row, int f0, int n,
+                                           const uint32_t (&v)[32]) {
+    const int lane = threadIdx.x & 31, s = lane & 3;
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-        if (j < n) o[static_cast<int64_t>(j) * p.N] = __float2bfloat16_rn(__uint_as_float(v[j]));
+        buf[j * 32 + (((lane >> 2) ^ (j & 7)) << 2) + (lane & 3)] = __uint_as_float(v[j]);
+    __syncwarp();
+    const int f = f0 + 4 * s, piece = 4 * (s >> 1) + (s & 1);   // the gate values' 16 bytes; up: two further on
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        const float4* d4 = reinterpret_cast<const float4*>(buf + r * 32);
+        const float4 g = d4[piece ^ (r & 7)], u = d4[(piece + 2) ^ (r & 7)];
+        if (r >= n || f >= p.out_cols) continue;
+        const int64_t at = row + r;
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.keep) + at * p.N + f;
+        *reinterpret_cast<uint2*>(y) = make_uint2(moe::pack_bf16x2(g.x, g.y), moe::pack_bf16x2(g.z, g.w));
+        *reinterpret_cast<uint2*>(y + p.half) = make_uint2(moe::pack_bf16x2(u.x, u.y), moe::pack_bf16x2(u.z, u.w));
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * p.out_cols + f) =
+            make_uint2(moe::pack_bf16x2(silu_mul(g.x, u.x), silu_mul(g.y, u.y)),
+                       moe::pack_bf16x2(silu_mul(g.z, u.z), silu_mul(g.w, u.w)));
+    }
+    __syncwarp();
 }
 
 // SwiGLU M = 128 tile: lane l of this CTA holds weight row l % 64 (its 32
@@ -943,7 +963,7 @@ __device__ __forceinline__ void keep_chunk(const Params& p, int64_t row, int f, 
 // chunk as in a full tile.
 template <bool KEEP>
 __device__ __forceinline__ void swiglu_half_tile(const Params& p, const Tile& ti, uint32_t ta, int q, int hsel,
-                                                 int lane, uint32_t rank) {
+                                                 int lane, uint32_t rank, float* buf) {
     const int nh = swap_n(ti) / 2, tok0 = (q >> 1) * nh, ntok = ti.rows;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
 #pragma unroll 1
@@ -954,6 +974,10 @@ __device__ __forceinline__ void swiglu_half_tile(const Params& p, const Tile& ti
         uint32_t v[32];
         moe::tmem_ld32(ta + col, v);
         moe::tmem_ld_wait();
+        if (KEEP) {
+            keep_chunk(p, buf, ti.row0 + tok0 + col, ti.col0 + static_cast<int>(rank) * 32 + 16 * (q & 1), jmax, v);
+            continue;
+        }
         const int r = (lane >> 3) & 1;   // 0: gate lane, 1: up lane
         float h[16];
 #pragma unroll
@@ -963,7 +987,6 @@ __device__ __forceinline__ void swiglu_half_tile(const Params& p, const Tile& ti
             h[j] = r ? silu_mul(o, hi) : silu_mul(lo, o);
         }
         const int f = ti.col0 + static_cast<int>(rank) * 32 + 16 * (q & 1) + 8 * (lane >> 4) + (lane & 7);
-        if (KEEP) keep_chunk(p, ti.row0 + tok0 + col, f, r, jmax, v);
         const int t0 = 16 * r;   // within the chunk
         if (f < p.out_cols) {
             __nv_bfloat16* o = out + static_cast<int64_t>(ti.row0 + tok0 + col + t0) * p.out_cols + f;
@@ -986,7 +1009,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
     uint32_t cph = 0;                    // fused combine barrier phase
     const int KB = p.k_blocks;
 
-    // the warp's transpose buffer (EPI_SWIGLU_BACK)
+    // the warp's transpose buffer (transposes(EPI) only)
     float* buf = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&S) + sizeof(Shared) + (warp - 4) * kTransposeBytes);
     // the pair's MMA waits for both CTAs' epilogues on the leader's barrier
     uint32_t acc_empty_leader[2] = {0, 0};
@@ -1010,7 +1033,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
             const int ntok = swap_rows(ti);
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
             if (!plain_tiles(EPI) && ti.half) {
-                swiglu_half_tile<EPI == EPI_SWIGLU_KEEP>(p, ti, ta, q, hsel, lane, rank);
+                swiglu_half_tile<EPI == EPI_SWIGLU_KEEP>(p, ti, ta, q, hsel, lane, rank, buf);
             } else if (plain_tiles(EPI) && ti.half) {
                 store_half_tile<EPI>(p, ti, ta, q, hsel, lane, rank, buf);
             } else if (EPI == EPI_SWIGLU_BACK) {
@@ -1046,6 +1069,9 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
                             for (int j = 0; j < 32; ++j)
                                 if (col + j < ntok) o[static_cast<int64_t>(j) * p.out_cols] = __float2bfloat16_rn(__uint_as_float(v[j]));
                         }
+                    } else if (EPI == EPI_SWIGLU_KEEP) {
+                        keep_chunk(p, buf, ti.row0 + col, ti.col0 + static_cast<int>(rank) * 64 + 16 * q,
+                                   min(32, ntok - col), v);
                     } else {
                         // lane l holds the gate (up, if bit 3 of l is set) row of
                         // feature 16q + 8(l / 16) + l % 8; lanes l and l ^ 8 share
@@ -1061,7 +1087,6 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
                             h[j] = r ? silu_mul(o, hi) : silu_mul(lo, o);
                         }
                         const int f = ti.col0 + static_cast<int>(rank) * 64 + 16 * q + 8 * (lane >> 4) + (lane & 7);
-                        if (EPI == EPI_SWIGLU_KEEP) keep_chunk(p, ti.row0 + col, f, r, min(32, ntok - col), v);
                         const int t0 = col + 16 * r;
                         if (f < p.out_cols) {
                             __nv_bfloat16* o = out + static_cast<int64_t>(ti.row0 + t0) * p.out_cols + f;

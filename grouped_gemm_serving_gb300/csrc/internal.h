@@ -71,6 +71,10 @@ bool encode_tile_map(CUtensorMap* map, bool fp8, const void* base, int rank, con
 moe_status_t swiglu_keep_gemm(const void* x, const void* W1, const int32_t* offsets, int E, int M_cap, int N, int K,
                               void* Y1, void* h, cudaStream_t stream);
 
+// moe_ffn_forward for few rows (ffn_few.cu), arguments checked by the caller.
+moe_status_t ffn_few_rows(const void* x, const void* W1, const void* W2, const int32_t* offsets, int E, int M_cap,
+                          int H, int I, void* Y1, void* h, void* y, cudaStream_t stream);
+
 // The weighted combine (data.cu); topk_w NULL: unit weights.
 moe_status_t combine_rows(const void* Y2, const int32_t* topk_ids, const float* topk_w, const int32_t* row_pos,
                           int T, int k, int H, int E, void* out, cudaStream_t stream);

@@ -452,7 +452,7 @@ moe_status_t run(const Args& a, void* dweight, void* dbias) {
     }
     MOE_CHECK_LAUNCH();
     if (a.partial) {
-        return moe::launch_after(norm_reduce_kernel<W>, dim3((a.H + 31) / 32, 2), 32 * kShares, a.stream,
+        return moe::launch_after(norm_reduce_kernel<W>, dim3((a.H + 31) / 32, 2), 32 * kShares, 0, a.stream,
                                  static_cast<const float*>(a.partial), blocks, a.H, static_cast<W*>(dweight),
                                  static_cast<W*>(dbias));
     }

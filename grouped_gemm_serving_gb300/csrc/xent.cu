@@ -650,7 +650,7 @@ extern "C" moe_status_t moe_cross_entropy_forward(const void* x, const void* W, 
     p.row_vecs = H / 8;
     const moe_status_t st = launch_logits<false>(x, W, H, V, p, s);
     if (st != MOE_OK) return st;
-    return moe::launch_after(join_kernel, dim3((T + kJoinTokens - 1) / kJoinTokens), 256, s,
+    return moe::launch_after(join_kernel, dim3((T + kJoinTokens - 1) / kJoinTokens), 256, 0, s,
                              static_cast<const float2*>(p.part), p.shares * l.voc_tiles,
                              static_cast<const float*>(p.at_label), labels, T, V, ignore_index, loss, lse, err);
 }
@@ -681,7 +681,7 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
     scale_kernel<<<1, 1024, 0, s>>>(dloss, labels, T, V, ignore_index, scale, offsets, err);
     MOE_CHECK_LAUNCH();
     moe_status_t st = MOE_OK;
-    if (dW && (st = moe::launch_after(scale_rows_kernel, dim3((T + 7) / 8), 256, s, static_cast<const uint4*>(x),
+    if (dW && (st = moe::launch_after(scale_rows_kernel, dim3((T + 7) / 8), 256, 0, s, static_cast<const uint4*>(x),
                                       static_cast<const float*>(scale), T, H / 8, static_cast<uint4*>(xs))) != MOE_OK)
         return st;
     for (int i = 0; i < l.pieces; ++i) {
