@@ -323,32 +323,34 @@ norm_backward_wide_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, in
     }
 }
 
-// out[c] = sum of the blocks' partial rows, in order within each of 32
-// interleaved shares, then over the shares.  blockIdx.y: 0 dweight, 1 dbias.
-constexpr int kShares = 32;
+// out[c] = sum of the blocks' partial rows, in order within each of 64
+// interleaved shares, then over the shares in a fixed tree; 16 columns (whole
+// sectors of a partial row) a block.  blockIdx.y: 0 dweight, 1 dbias.
+constexpr int kShares = 64, kCols = 16;
 template <typename W>
-__global__ void __launch_bounds__(32 * kShares)
+__global__ void __launch_bounds__(kCols * kShares)
 norm_reduce_kernel(const float* __restrict__ partial, int blocks, int H, W* __restrict__ dweight,
                    W* __restrict__ dbias) {
-    __shared__ float share[kShares][33];
+    __shared__ float share[kCols][kShares + 1];
     W* out = blockIdx.y == 0 ? dweight : dbias;
     moe::wait_for_primary();   // this grid may start while the blocks' last stores are under way
     if (!out) return;
-    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    const int col = threadIdx.x % kCols, part = threadIdx.x / kCols;
+    const int c = blockIdx.x * kCols + col;
     float s = 0.0f;
     if (c < H) {
         const float* p = partial + static_cast<int64_t>(blockIdx.y) * H + c;
-#pragma unroll 8
+#pragma unroll 4
         for (int b = part; b < blocks; b += kShares) s += p[static_cast<int64_t>(b) * 2 * H];
     }
-    share[part][lane] = s;
+    share[col][part] = s;
     __syncthreads();
-    // warp i: column i of the block, one share a lane
-    float v = share[lane][part];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp >= kCols) return;
+    float v = share[warp][lane] + share[warp][lane + 32];   // warp i: column i of the block
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (lane == 0 && blockIdx.x * 32 + part < H) store_vec<W, 1>(out + blockIdx.x * 32 + part, &v);
+    if (lane == 0 && blockIdx.x * kCols + warp < H) store_vec<W, 1>(out + blockIdx.x * kCols + warp, &v);
 }
 
 // Blocks of a launch, each of which writes a partial row: as many as the GPU
@@ -452,7 +454,7 @@ moe_status_t run(const Args& a, void* dweight, void* dbias) {
     }
     MOE_CHECK_LAUNCH();
     if (a.partial) {
-        return moe::launch_after(norm_reduce_kernel<W>, dim3((a.H + 31) / 32, 2), 32 * kShares, 0, a.stream,
+        return moe::launch_after(norm_reduce_kernel<W>, dim3((a.H + kCols - 1) / kCols, 2), kCols * kShares, 0, a.stream,
                                  static_cast<const float*>(a.partial), blocks, a.H, static_cast<W*>(dweight),
                                  static_cast<W*>(dbias));
     }

@@ -376,37 +376,35 @@ logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     }
 }
 
-// Joins the vocabulary tiles' (m, s): eight tokens a block, 32 threads each,
-// whose shares are merged in thread order.  An ignored or invalid label gets
-// loss 0 (the latter is reported).
-constexpr int kJoinTokens = 8;
+// Joins the vocabulary tiles' (m, s): TOKENS tokens a block, 256 / TOKENS
+// threads each, whose shares are merged in a fixed tree.  An ignored or invalid
+// label gets loss 0 (the latter is reported).
+__device__ __forceinline__ float2 merge(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.0f : m;
+    return make_float2(m, a.y * expf(a.x - base) + b.y * expf(b.x - base));
+}
+template <int TOKENS>
 __global__ void __launch_bounds__(256)
 join_kernel(const float2* part, int parts, const float* at_label,
             const int32_t* __restrict__ labels, int T, int V, int ignore, float* __restrict__ loss,
             float* __restrict__ lse, int* err) {
-    __shared__ float2 share[32][kJoinTokens];
+    constexpr int kShares = 256 / TOKENS;
+    __shared__ float2 share[kShares][TOKENS];
     moe::wait_for_primary();
-    const int tok = threadIdx.x % kJoinTokens, g = threadIdx.x / kJoinTokens;
-    const int t = blockIdx.x * kJoinTokens + tok;
-    float m = -INFINITY, s = 0.0f;
+    const int tok = threadIdx.x % TOKENS, g = threadIdx.x / TOKENS;
+    const int t = blockIdx.x * TOKENS + tok;
+    float2 v = make_float2(-INFINITY, 0.0f);
     if (t < T) {
 #pragma unroll 4
-        for (int i = g; i < parts; i += 32) {
-            const float2 v = part[static_cast<int64_t>(i) * T + t];
-            const float nm = fmaxf(m, v.x), base = nm == -INFINITY ? 0.0f : nm;
-            s = s * expf(m - base) + v.y * expf(v.x - base);
-            m = nm;
-        }
+        for (int i = g; i < parts; i += kShares) v = merge(v, part[static_cast<int64_t>(i) * T + t]);
     }
-    share[g][tok] = make_float2(m, s);
-    __syncthreads();
+    share[g][tok] = v;
+    for (int n = kShares / 2; n > 0; n >>= 1) {
+        __syncthreads();
+        if (g < n) share[g][tok] = merge(share[g][tok], share[g + n][tok]);
+    }
     if (g != 0 || t >= T) return;
-    for (int i = 1; i < 32; ++i) {
-        const float2 v = share[i][tok];
-        const float nm = fmaxf(m, v.x), base = nm == -INFINITY ? 0.0f : nm;
-        s = s * expf(m - base) + v.y * expf(v.x - base);
-        m = nm;
-    }
+    const float m = share[0][tok].x, s = share[0][tok].y;
     const int label = labels[t];
     float out = 0.0f, l;
     if (label != ignore && label >= 0 && label < V) {
@@ -650,7 +648,10 @@ extern "C" moe_status_t moe_cross_entropy_forward(const void* x, const void* W, 
     p.row_vecs = H / 8;
     const moe_status_t st = launch_logits<false>(x, W, H, V, p, s);
     if (st != MOE_OK) return st;
-    return moe::launch_after(join_kernel, dim3((T + kJoinTokens - 1) / kJoinTokens), 256, 0, s,
+    // neighbouring tokens' pairs share a sector; with few tokens the latency of
+    // a token's own pairs counts
+    const bool few = T < 8 * moe::sm_count();
+    return moe::launch_after(few ? join_kernel<1> : join_kernel<8>, dim3(few ? T : (T + 7) / 8), 256, 0, s,
                              static_cast<const float2*>(p.part), p.shares * l.voc_tiles,
                              static_cast<const float*>(p.at_label), labels, T, V, ignore_index, loss, lse, err);
 }
