@@ -6,7 +6,8 @@
 //
 // CTA pairs (clusters of two, tcgen05 cta_group::2): a tile is 256 output rows
 // (128 per CTA, the MMA's M rows, from dC's columns) x up to 256 output columns
-// (half staged by each CTA, the MMA's N, from A's columns).
+// (half staged by each CTA, the MMA's N, from A's columns; the last tile's N is
+// what is left, rounded up to 16).
 // Both operands are read in place, MN-major, as 64-column x 64-row boxes of
 // 128-byte swizzled rows: four boxes (32 KB) a CTA and k-block, six stages.  A
 // lane of the accumulator is an output row, so a warp's 32 rows x 64 columns
@@ -45,7 +46,7 @@ struct Params {
     const float* scale;    // one factor for all of it, or NULL
     int* err;
     int E, M_cap, N, K;
-    int row_tiles, col_tiles, bc;   // bc: columns of a tile, a multiple of 16
+    int row_tiles, col_tiles;
     int tails;             // 0: rows past offsets[E] lie outside the tensor maps (zeros)
 };
 
@@ -67,6 +68,7 @@ struct Tile {
     int e, row0, col0;
     int first, rows;   // the expert's rows
     int nkb, last;     // its k-blocks, and the 16-row steps of the last one
+    int bc;            // the tile's columns, rounded up to 16
 };
 
 __device__ __forceinline__ Tile decode(int t, const Params& p) {
@@ -75,7 +77,8 @@ __device__ __forceinline__ Tile decode(int t, const Params& p) {
     ti.e = t / per;
     t -= ti.e * per;
     ti.row0 = t / p.col_tiles * BR;
-    ti.col0 = t % p.col_tiles * p.bc;
+    ti.col0 = t % p.col_tiles * BC;
+    ti.bc = min(BC, (p.K - ti.col0 + 15) & ~15);
     ti.first = p.offsets[ti.e];
     ti.rows = p.offsets[ti.e + 1] - ti.first;
     ti.nkb = (ti.rows + 63) / 64;
@@ -94,9 +97,9 @@ __device__ void producer(const Maps& maps, uint8_t* stages, Shared& S, const Par
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_par = 0;
     bool ok = true;
-    const int half = p.bc / 2, boxes = half > 64 ? 2 : 1;   // this CTA's columns of A
     for (int t = blockIdx.x >> 1; ok && t < total; t += gridDim.x >> 1) {
         const Tile ti = decode(t, p);
+        const int half = ti.bc / 2, boxes = half > 64 ? 2 : 1;   // this CTA's columns of A
         const int n0 = ti.row0 + static_cast<int>(rank) * 128, c0 = ti.col0 + static_cast<int>(rank) * half;
         const int whole = p.tails ? ti.rows / 64 : ti.nkb;   // k-blocks read in place
         for (int kb = 0; kb < ti.nkb; ++kb) {
@@ -139,12 +142,12 @@ __device__ void producer(const Maps& maps, uint8_t* stages, Shared& S, const Par
 }
 
 __device__ void mma_issuer(uint8_t* stages, Shared& S, const Params& p, int total, uint32_t tmem) {
-    const uint32_t idesc = moe::make_idesc_ab_mn(1u, BR, p.bc);
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true, issued = false;
     for (int t = blockIdx.x >> 1; ok && t < total; t += gridDim.x >> 1) {
         const Tile ti = decode(t, p);
+        const uint32_t idesc = moe::make_idesc_ab_mn(1u, BR, ti.bc);
         bool got = moe::mbar_wait_cluster(bar(S.acc_empty[acc]), acc_phase ^ 1u, &S.abort_flag, kWaitNs);
         if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
         moe::tc_fence_after();
@@ -199,7 +202,7 @@ __device__ void epilogue(uint8_t* transposes, Shared& S, const Params& p, int to
         const Tile ti = decode(t, p);
         const int n0 = ti.row0 + static_cast<int>(rank) * 128 + q * 32;   // the warp's first output row
         const int col0 = ti.col0 + hsel * 128;
-        const int ncols = min(128, min(p.bc - hsel * 128, p.K - col0));   // its columns that exist
+        const int ncols = min(128, p.K - col0);   // its columns that exist
         if (!moe::mbar_wait(bar(S.acc_full[acc]), acc_phase, &S.abort_flag, kWaitNs)) { fail(S, p); return; }
         moe::tc_fence_after();
         // the whole share is packed into registers at once, so that the
@@ -324,7 +327,6 @@ moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, const void*
     p.K = K;
     p.row_tiles = (N - 1) / BR + 1;
     p.col_tiles = (K - 1) / BC + 1;
-    p.bc = K >= BC ? BC : (K + 15) / 16 * 16;
     p.tails = tail_c && tail_a;
     const int64_t tiles = static_cast<int64_t>(E) * p.row_tiles * p.col_tiles;
     MOE_CHECK_ARG(tiles < INT_MAX);
