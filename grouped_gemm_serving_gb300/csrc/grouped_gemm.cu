@@ -1466,11 +1466,15 @@ namespace {
 
 using moe::encode_tile_map;
 
-// bf16 [rows, K] (dims/strides as for encode_tile_map) with boxes of 64 x 8(j + 1) rows.
+// bf16 [rows, K] (dims/strides as for encode_tile_map) with boxes of 64 x 8(j + 1)
+// rows: those that tiles of so many rows can take (an encoding costs the host
+// some tenths of a microsecond); the others are copies of the last.
 bool encode_token_maps(TokenMaps* t, const void* base, const cuuint64_t* dims, const cuuint64_t* strides) {
+    const int tallest = dims[1] < BT ? static_cast<int>((dims[1] + 31) / 32 * 2) : kTokenMaps;   // N rounds up to 32
     for (int j = 0; j < kTokenMaps; ++j) {
         const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(8 * (j + 1))};
-        if (!encode_tile_map(&t->m[j], false, base, 2, dims, strides, box)) return false;
+        if (j >= tallest) t->m[j] = t->m[tallest - 1];
+        else if (!encode_tile_map(&t->m[j], false, base, 2, dims, strides, box)) return false;
     }
     return true;
 }
@@ -1724,13 +1728,11 @@ struct SumPlan {
 };
 static SumPlan sum_plan(int M, int N, int K, int pairs) {
     const int n_tiles = (K + kSwapFeatStore - 1) / kSwapFeatStore, kb = (N + 63) / 64;
-    const int least = (M + BT - 1) / BT;
-    SumPlan best{least, 1};
+    SumPlan best{(M + BT - 1) / BT, 1};
     double best_ns = 1e30;
     for (int splits = 1; splits <= 16 && (splits == 1 || kb / splits >= 16); ++splits)
-        for (int mt = least; mt <= least + pairs && (mt == least || (mt - 1) * 16 < M); ++mt) {
-            const int ts = ((M + mt - 1) / mt + 15) & ~15;
-            if ((M + ts - 1) / ts != mt) continue;   // a tile without rows
+        for (int height = M < BT ? (M + 15) & ~15 : BT; height > 0; height -= 16) {
+            const int mt = (M + height - 1) / height, ts = ((M + mt - 1) / mt + 15) & ~15;
             const double rounds = static_cast<double>((static_cast<int64_t>(mt) * n_tiles * splits + pairs - 1) / pairs);
             const double ns = rounds * (ts + 32) / 288.0 * 340.0 * ((kb + splits - 1) / splits + 6) +
                               (splits > 1 ? static_cast<double>(splits) * M * K * 8 / 6800.0 : 0.0);
