@@ -45,8 +45,9 @@
 //   warps 2-3   idle (they complete warpgroup 0 for the FP8 register split),
 //               except with gathered A (below)
 //   warps 4-11  epilogue: tcgen05.ld the accumulator, apply the epilogue and
-//               store; warp w reads TMEM lanes 32*(w%4).., columns half
-//               (w-4)/4; then zero the sentinel rows [offsets[E], M_cap).
+//               store; warp w reads TMEM lanes 32*(w%4).. and half (w-4)/4
+//               of the columns (swapped: every other 32, so that both halves
+//               have work in a tile of few tokens); then zero the sentinel rows [offsets[E], M_cap).
 // The producer and MMA loops run on the whole warp and let one elected lane
 // issue: TMA and tcgen05 instructions take warp-uniform operands, and issued
 // from a single-thread branch they cost several times as many cycles.
@@ -895,7 +896,7 @@ __device__ void make_tails(const Params& p, int warp) {
 
 // Store M = 128 tile (forward and data gradient): lane l of this CTA holds
 // weight row (output feature) l % 64 for token (l / 64) * nh + column, columns
-// below nh = N/2.  Each half of the epilogue takes 64 columns.
+// below nh = N/2.  Each half of the epilogue takes every other 32 columns.
 template <int EPI>
 __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti, uint32_t ta, int q, int hsel,
                                                 int lane, uint32_t rank, float* buf) {
@@ -904,7 +905,7 @@ __device__ __forceinline__ void store_half_tile(const Params& p, const Tile& ti,
     const int f = ti.col0 + static_cast<int>(rank) * 64 + (q & 1) * 32 + lane;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
-        const int col = hsel * 64 + c * 32;
+        const int col = c * 64 + hsel * 32;
         if (col >= nh || tok0 + col >= ntok) break;   // the same for the whole warp
         const int jmax = min(32, min(nh - col, ntok - tok0 - col));   // token columns of the chunk
         uint32_t v[32];
@@ -959,7 +960,7 @@ __device__ __forceinline__ void keep_chunk(const Params& p, float* buf, int64_t 
 // SwiGLU M = 128 tile: lane l of this CTA holds weight row l % 64 (its 32
 // features' gate and up rows, interleaved in groups of 8 as in a full tile)
 // for token (l / 64) * nh + column, columns below nh = N/2.  Each half of the
-// epilogue takes 64 columns; gate and up lanes swap halves of each 32-column
+// epilogue takes every other 32 columns; gate and up lanes swap halves of each 32-column
 // chunk as in a full tile.
 template <bool KEEP>
 __device__ __forceinline__ void swiglu_half_tile(const Params& p, const Tile& ti, uint32_t ta, int q, int hsel,
@@ -968,7 +969,7 @@ __device__ __forceinline__ void swiglu_half_tile(const Params& p, const Tile& ti
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
-        const int col = hsel * 64 + c * 32;
+        const int col = c * 64 + hsel * 32;
         if (col >= nh || tok0 + col >= ntok) break;   // the same for the whole warp
         const int jmax = min(32, min(nh - col, ntok - tok0 - col));   // token columns of the chunk
         uint32_t v[32];
@@ -1026,7 +1027,7 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
             const int back_f0 = ti.col0 + static_cast<int>(rank) * 128 + q * 32;
             GateUp gu;   // the pre-activations of a chunk are fetched a chunk ahead
             if (EPI == EPI_SWIGLU_BACK && !ti.half)
-                load_gate_up(p, ti.row0 + hsel * 128, back_f0, min(32, ti.rows - hsel * 128), gu);
+                load_gate_up(p, ti.row0 + hsel * 32, back_f0, min(32, ti.rows - hsel * 32), gu);
             if (!moe::mbar_wait(bar(S.acc_full[acc]), acc_phase, &S.abort_flag, kWaitNs)) { fail(S, p); return; }
             moe::tc_fence_after();
             const uint32_t ta = lane_base + static_cast<uint32_t>(acc * BN);
@@ -1039,19 +1040,19 @@ __device__ void epilogue(Shared& S, const Params& p, int total, uint32_t tmem, u
             } else if (EPI == EPI_SWIGLU_BACK) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    const int col = hsel * 128 + c * 32;
+                    const int col = c * 64 + hsel * 32;
                     if (col >= ntok) break;                       // the same for the whole warp
                     uint32_t v[32];
                     moe::tmem_ld32(ta + col, v);
                     const GateUp now = gu;
-                    if (c < 3) load_gate_up(p, ti.row0 + col + 32, back_f0, min(32, ntok - col - 32), gu);
+                    if (c < 3) load_gate_up(p, ti.row0 + col + 64, back_f0, min(32, ntok - col - 64), gu);
                     moe::tmem_ld_wait();
                     swiglu_back_chunk(p, ti, buf, ti.row0 + col, back_f0, min(32, ntok - col), v, now);
                 }
             } else {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    const int col = hsel * 128 + c * 32;
+                    const int col = c * 64 + hsel * 32;
                     if (col >= ntok) break;                       // the same for the whole warp
                     uint32_t v[32];
                     moe::tmem_ld32(ta + col, v);
