@@ -31,8 +31,9 @@ namespace {
 // expert's rows at once (ffn_few.cu) instead of tiling them.  Measured, weights
 // from HBM, streamed / tiled, us: 32 experts H = I = 2880, a row in each of 1, 4,
 // 16 experts 16.4 / 37, 37.8 / 56, 124 / 138 (reading the weights takes 7.3, 29,
-// 117); one expert, H = 2048, I = 5632, 1 and 16 rows 21 / 43, 25 / 43 (10).
-constexpr int kFewRows = 16;
+// 117), and 32 rows in 32 experts 257 / 256 (234); one expert, H = 2048, I = 5632,
+// 1, 16 and 32 rows 21 / 43, 25 / 43, 33 / 43 (10).
+constexpr int kFewRows = 32;
 
 struct Layout {
     size_t dY1, h, tail_dY1, tail_h, tail_x, tail_dy, total;

@@ -1,5 +1,5 @@
 // The gated feed-forward block for a few rows (generating a token at a time):
-// every weight of the experts that have rows is read once and meets up to 16
+// every weight of the experts that have rows is read once and meets up to 32
 // rows, so the block is bound by HBM.  The grouped GEMM's tcgen05 tiles of 256
 // weight rows leave CTA pairs idle when the experts' tiles do not fill them, and
 // each pair's ring then has to fill from cold; fp32 FMAs on unpacked weights
@@ -68,10 +68,11 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 // This warp's share of one unit: weight rows w0 and w1 (this lane's two) against
 // NB groups of 8 rows of x from row p on, `rows` of which exist.  `wait`: the
 // kernel that writes x may still run.
-template <int NB>
+template <int NB, int R>
 __device__ __forceinline__ void share(const Args& a, const uint4* w0, const uint4* w1, int lo, int hi, int p, int rows,
-                                      bool wait, float (&d)[NB][4]) {
+                                      bool wait, float4 (&sums)[R / 8][kWarps][32]) {
     const int lane = threadIdx.x & 31, n = lane >> 2;
+    float d[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -101,13 +102,17 @@ __device__ __forceinline__ void share(const Args& a, const uint4* w0, const uint
         }
     }
     if (wait) moe::wait_for_primary();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) sums[b][threadIdx.x >> 5][lane] = make_float4(d[b][0], d[b][1], d[b][2], d[b][3]);
 }
 
-template <bool GATED>
+// R: the most rows an expert can have, 16 or 32 (the kernel for 16 has registers
+// and L1 to spare: 37.8 us for the token below that takes 41 with 32).
+template <bool GATED, int R>
 __global__ void __launch_bounds__(kThreads, 2)
 few_rows_kernel(const Args a) {
     __shared__ Live L;
-    __shared__ float4 red[2][2][kWarps][32];   // turn, group of 8 rows, warp, lane
+    __shared__ float4 red[2][R / 8][kWarps][32];   // turn, group of 8 rows, warp, lane
     __shared__ int bad;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (GATED) moe::launch_dependents();   // the second product may take its place beside this one
@@ -149,21 +154,14 @@ few_rows_kernel(const Args a) {
         const int64_t first = static_cast<int64_t>(e) * (GATED ? 2 : 1) * a.F;
         const uint4* w0 = a.W + (first + min(f0 + g, a.F - 1)) * a.nv;
         const uint4* w1 = a.W + (GATED ? first + a.F + min(f0 + g, a.F - 1) : first + min(f0 + g + 8, a.F - 1)) * a.nv;
-        if (rows <= 8) {
-            float d[1][4];
-            share<1>(a, w0, w1, lo, hi, p, rows, wait, d);
-            red[turn][0][warp][lane] = make_float4(d[0][0], d[0][1], d[0][2], d[0][3]);
-        } else {
-            float d[2][4];
-            share<2>(a, w0, w1, lo, hi, p, rows, wait, d);
-            red[turn][0][warp][lane] = make_float4(d[0][0], d[0][1], d[0][2], d[0][3]);
-            red[turn][1][warp][lane] = make_float4(d[1][0], d[1][1], d[1][2], d[1][3]);
-        }
+        if (rows <= 8) share<1, R>(a, w0, w1, lo, hi, p, rows, wait, red[turn]);
+        else if (R == 16 || rows <= 16) share<2, R>(a, w0, w1, lo, hi, p, rows, wait, red[turn]);
+        else share<R / 8, R>(a, w0, w1, lo, hi, p, rows, wait, red[turn]);
         wait = false;
         __syncthreads();
-        // warps 0 and 1 finish rows 0-7 and 8-15 while the others go on; this
+        // warp i finishes rows 8i to 8i + 7 while the others go on; this
         // buffer is written again two units on, behind the next unit's barrier
-        if (warp < 2 && 8 * warp < rows) {
+        if (8 * warp < rows) {
             float4 s = red[turn][warp][0][lane];
 #pragma unroll
             for (int i = 1; i < kWarps; ++i) {
@@ -204,29 +202,35 @@ few_rows_kernel(const Args a) {
         for (int64_t i = 2 * none + tid; i < 2 * end; i += all) a.keep[i] = __float2bfloat16_rn(0.0f);
 }
 
-}  // namespace
-
-moe_status_t moe::ffn_few_rows(const void* x, const void* W1, const void* W2, const int32_t* offsets, int E, int M_cap,
-                               int H, int I, void* Y1, void* h, void* y, cudaStream_t s) {
-    MOE_CHECK_ARG(M_cap <= 16);
-    int* err = moe::device_error_word();
+template <int R>
+moe_status_t launch(const Args& a1, const Args& a2, cudaStream_t s) {
     static std::atomic<int> resident[2][moe::kMaxDevices];
-    const int g1 = moe::resident_blocks(reinterpret_cast<const void*>(few_rows_kernel<true>), kThreads, 0, resident[0]);
-    const int g2 = moe::resident_blocks(reinterpret_cast<const void*>(few_rows_kernel<false>), kThreads, 0, resident[1]);
-    if (!err || g1 <= 0 || g2 <= 0) return MOE_ERR_CUDA;
+    const int g1 = moe::resident_blocks(reinterpret_cast<const void*>(few_rows_kernel<true, R>), kThreads, 0, resident[0]);
+    const int g2 = moe::resident_blocks(reinterpret_cast<const void*>(few_rows_kernel<false, R>), kThreads, 0, resident[1]);
+    if (g1 <= 0 || g2 <= 0) return MOE_ERR_CUDA;
     // As many blocks as give each the same number of units if every row has an
     // expert of its own: a last round that only some have leaves too few loads
     // in flight.
     const auto blocks = [&](int units_of_expert, int most) {
-        const int64_t units = static_cast<int64_t>(units_of_expert) * (M_cap < E ? M_cap : E);
+        const int64_t units = static_cast<int64_t>(units_of_expert) * (a1.M_cap < a1.E ? a1.M_cap : a1.E);
         const int64_t rounds = (units + most - 1) / most;
         return static_cast<int>((units + rounds - 1) / rounds);
     };
+    few_rows_kernel<true, R><<<blocks((a1.F + 7) / 8, g1), kThreads, 0, s>>>(a1);
+    MOE_CHECK_LAUNCH();
+    return moe::launch_after(few_rows_kernel<false, R>, dim3(blocks((a2.F + 15) / 16, g2)), kThreads, 0, s, a2);
+}
+
+}  // namespace
+
+moe_status_t moe::ffn_few_rows(const void* x, const void* W1, const void* W2, const int32_t* offsets, int E, int M_cap,
+                               int H, int I, void* Y1, void* h, void* y, cudaStream_t s) {
+    MOE_CHECK_ARG(M_cap <= 32);
+    int* err = moe::device_error_word();
+    if (!err) return MOE_ERR_CUDA;
     const Args a1{static_cast<const uint4*>(x), static_cast<const uint4*>(W1), offsets, static_cast<__nv_bfloat16*>(h),
                   static_cast<__nv_bfloat16*>(Y1), err, E, M_cap, H / 8, I};
     const Args a2{static_cast<const uint4*>(h), static_cast<const uint4*>(W2), offsets, static_cast<__nv_bfloat16*>(y),
                   nullptr, err, E, M_cap, I / 8, H};
-    few_rows_kernel<true><<<blocks((I + 7) / 8, g1), kThreads, 0, s>>>(a1);
-    MOE_CHECK_LAUNCH();
-    return moe::launch_after(few_rows_kernel<false>, dim3(blocks((H + 15) / 16, g2)), kThreads, 0, s, a2);
+    return M_cap <= 16 ? launch<16>(a1, a2, s) : launch<32>(a1, a2, s);
 }

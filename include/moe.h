@@ -378,8 +378,8 @@ moe_status_t moe_grouped_gemm_wgrad(const void* A, const void* dC, const int32_t
  *   h bf16 [M_cap, I] scratch (holds h afterwards).  Y1 bf16 [M_cap, 2I] out:
  *   the pre-activations [g | u], which moe_ffn_backward needs; NULL for
  *   inference.  h is computed from the unrounded g and u, as in
- *   moe_grouped_gemm, whose results h and y equal bit for bit above 16 rows (up
- *   to M_cap = 16 every product is summed in fp32 by one warp).
+ *   moe_grouped_gemm, whose results h and y equal bit for bit above 32 rows (up
+ *   to M_cap = 32 the contraction is summed in eight shares).
  *   Rows p >= offsets[E] of x are never read; those of y, h and Y1 are zeros.
  * moe_ffn_backward:  from x, W1, W2, Y1 and the gradient dy of y:
  *   dx bf16 [M_cap, H], dW1 bf16 [E, 2I, H], dW2 bf16 [E, H, I], the
