@@ -106,8 +106,8 @@ extern "C" moe_status_t moe_ffn_backward(const void* x, const void* W1, const vo
     moe_status_t st = moe::swiglu_back_gemm(dy, W2, offsets, E, M_cap, H, I, back, s);
     if (st == MOE_OK && dx) st = moe::dgrad_gemm(dY1, W1, offsets, E, M_cap, 2 * I, H, dx, s);
     if (st == MOE_OK && dW1)
-        st = moe::wgrad_gemm(dY1, 2 * I, x, back.tail_dY1, back.tail_x, offsets, E, M_cap, 2 * I, H, dW1, s);
+        st = moe::wgrad_gemm(dY1, 2 * I, x, H, back.tail_dY1, back.tail_x, offsets, E, M_cap, 2 * I, H, dW1, s);
     if (st == MOE_OK && dW2)
-        st = moe::wgrad_gemm(dy, H, h, back.tail_dy, back.tail_h, offsets, E, M_cap, H, I, dW2, s);
+        st = moe::wgrad_gemm(dy, H, h, I, back.tail_dy, back.tail_h, offsets, E, M_cap, H, I, dW2, s);
     return st;
 }

@@ -96,5 +96,5 @@ extern "C" moe_status_t moe_grouped_gemm_wgrad(const void* A, const void* dC, co
         static_cast<uint16_t*>(ws), err);
     MOE_CHECK_LAUNCH();
     const auto* tails = static_cast<const uint16_t*>(ws);
-    return moe::wgrad_gemm(dC, N, A, tails, tails + static_cast<size_t>(64) * E * N, offsets, E, M_cap, N, K, dB, s);
+    return moe::wgrad_gemm(dC, N, A, K, tails, tails + static_cast<size_t>(64) * E * N, offsets, E, M_cap, N, K, dB, s);
 }

@@ -32,7 +32,7 @@ moe_status_t swiglu_back_gemm(const void* dy, const void* W2, const int32_t* off
 
 // Launches the weight-gradient GEMM (wgrad.cu):
 //   dB[e, n, c] = sum over expert e's rows p of dC[p, n] * A[p, c]
-// with dC bf16 [M_cap, N] (rows ldc elements apart) and A bf16 [M_cap, K] read
+// with dC bf16 [M_cap, N] and A bf16 [M_cap, K] (rows ldc and lda elements apart) read
 // in place in 64-row k-blocks from offsets[e].  An expert's last, partial
 // k-block (r = cnt_e mod 64 rows) comes instead from rows [64e, 64e + r) of the
 // tails, copies of those rows of dC and A (bf16 [64E, N] and [64E, K]) with zeros
@@ -40,7 +40,7 @@ moe_status_t swiglu_back_gemm(const void* dy, const void* W2, const int32_t* off
 // rows, whose last k-block reads zeros from outside the tensor maps.  dB bf16
 // [E, N, K]; an expert without rows gets zeros.  scale (one float on the
 // device, or NULL) multiplies dB in fp32 before it is rounded.
-moe_status_t wgrad_gemm(const void* dC, int ldc, const void* A, const void* tail_c, const void* tail_a,
+moe_status_t wgrad_gemm(const void* dC, int ldc, const void* A, int lda, const void* tail_c, const void* tail_a,
                         const int32_t* offsets, int E, int M_cap, int N, int K, void* dB, cudaStream_t stream,
                         const float* scale = nullptr);
 

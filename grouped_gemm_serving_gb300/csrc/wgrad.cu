@@ -308,11 +308,11 @@ bool encode_operand(CUtensorMap* map, const void* base, int cols, int ld, int64_
 
 }  // namespace
 
-moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, const void* tail_c, const void* tail_a,
+moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, int lda, const void* tail_c, const void* tail_a,
                              const int32_t* offsets, int E, int M_cap, int N, int K, void* dB, cudaStream_t s,
                              const float* scale) {
     MOE_CHECK_ARG(dC && A && (tail_c && tail_a ? true : E == 1) && offsets && dB && E >= 1 && E <= kMaxE && M_cap >= 1);
-    MOE_CHECK_ARG(N >= 1 && ldc >= N && ldc % 8 == 0 && K >= 8 && K % 8 == 0);
+    MOE_CHECK_ARG(N >= 1 && ldc >= N && ldc % 8 == 0 && K >= 8 && K % 8 == 0 && lda >= K && lda % 8 == 0);
     MOE_CHECK_ARG(moe::aligned16(dC) && moe::aligned16(A) && moe::aligned16(tail_c) && moe::aligned16(tail_a) &&
                   moe::aligned16(dB));
     Params p{};
@@ -331,7 +331,7 @@ moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, const void*
     const int64_t tiles = static_cast<int64_t>(E) * p.row_tiles * p.col_tiles;
     MOE_CHECK_ARG(tiles < INT_MAX);
     Maps maps;
-    if (!encode_operand(&maps.c, dC, N, ldc, M_cap) || !encode_operand(&maps.a, A, K, K, M_cap)) return MOE_ERR_CUDA;
+    if (!encode_operand(&maps.c, dC, N, ldc, M_cap) || !encode_operand(&maps.a, A, K, lda, M_cap)) return MOE_ERR_CUDA;
     maps.tail_c = maps.c;
     maps.tail_a = maps.a;
     if (p.tails && (!encode_operand(&maps.tail_c, tail_c, N, N, 64ll * E) || !encode_operand(&maps.tail_a, tail_a, K, K, 64ll * E)))

@@ -226,8 +226,8 @@ __device__ void epilogue(uint8_t* stages, Shared& S, const Params& p, int total,
         const int col0 = vt * p.bv + shift;                  // first of its columns within the launch's
         const int ncols = min(width, p.cols - col0);         // those that exist
         const int label = row < p.T ? p.labels[row] : p.ignore;
-        const int rel = label - p.v0 - col0;                 // the label's column, in the tile if 0 <= rel < ncols
         const bool counts = label != p.ignore && label >= 0;
+        const int rel = counts ? label - p.v0 - col0 : -1;   // the label's column, in the tile if 0 <= rel < ncols
         float neg_lse = 0.0f;
         if (BACK && row < p.T) neg_lse = -p.lse[row] * kLog2e;
         if (!moe::mbar_wait(bar(S.acc_full[acc]), acc_phase, &S.abort_flag, kWaitNs)) { fail(S, p); return; }
@@ -454,9 +454,12 @@ scale_kernel(const float* __restrict__ dloss, const int32_t* __restrict__ labels
     }
 }
 
-// xs[t] = bf16(scale[t] / scale[T] * x[t]), zeros where scale[t] is 0.
+// xs[t] = bf16(scale[t] / scale[T] * x[t]), zeros where scale[t] is 0, and a copy
+// xa of x (either may be NULL), rows ld_vecs vectors apart: whole 128-byte
+// lines, so that no box of the products that read them straddles two.
 __global__ void __launch_bounds__(256)
-scale_rows_kernel(const uint4* __restrict__ x, const float* scale, int T, int row_vecs, uint4* __restrict__ xs) {
+scale_rows_kernel(const uint4* __restrict__ x, const float* scale, int T, int row_vecs, int ld_vecs,
+                  uint4* __restrict__ xs, uint4* __restrict__ xa) {
     moe::wait_for_primary();
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -464,12 +467,14 @@ scale_rows_kernel(const uint4* __restrict__ x, const float* scale, int T, int ro
     const float d = scale[t], r = d == 0.0f ? 0.0f : __fdiv_rn(d, scale[T]);
     for (int c = lane; c < row_vecs; c += 32) {
         const uint4 v = __ldg(x + static_cast<int64_t>(t) * row_vecs + c);
+        if (xa) xa[static_cast<int64_t>(t) * ld_vecs + c] = v;
+        if (!xs) continue;
         const uint32_t a[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             o[i] = d == 0.0f ? 0u : moe::pack_bf16x2(r * moe::bf16_lo(a[i]), r * moe::bf16_hi(a[i]));
-        xs[static_cast<int64_t>(t) * row_vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
+        xs[static_cast<int64_t>(t) * ld_vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -512,14 +517,15 @@ int tile_width(int cols, int T) {
     return bv;
 }
 
+// x's rows start ldx elements apart.
 template <bool BACK>
-moe_status_t launch_logits(const void* x, const void* W, int H, int V, Params p, cudaStream_t s) {
+moe_status_t launch_logits(const void* x, int ldx, const void* W, int H, int V, Params p, cudaStream_t s) {
     CUtensorMap tmX, tmW;
-    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(H) * 2};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(H) * 2}, stride_x[1] = {static_cast<cuuint64_t>(ldx) * 2};
     const cuuint64_t dx[2] = {static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(p.T)};
     const cuuint64_t dw[2] = {static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(V)};
     const cuuint32_t bx[2] = {64, static_cast<cuuint32_t>(p.bt / 2)}, bw[2] = {64, static_cast<cuuint32_t>(p.bv / 2)};
-    if (!moe::encode_tile_map(&tmX, false, x, 2, dx, stride, bx) ||
+    if (!moe::encode_tile_map(&tmX, false, x, 2, dx, stride_x, bx) ||
         !moe::encode_tile_map(&tmW, false, W, 2, dw, stride, bw))
         return MOE_ERR_CUDA;
     auto kern = logits_kernel<BACK>;
@@ -586,8 +592,8 @@ constexpr int64_t kPieceBytes = 256ll << 20;
 constexpr int kPieceMin = 2048;
 
 struct BackwardLayout {
-    int piece, pieces, ldg, splits;
-    size_t G, xs, scale, offsets, sum, total;
+    int piece, pieces, ldg, splits, ldx;
+    size_t G, xs, xa, scale, offsets, sum, total;
 };
 BackwardLayout backward_layout(int T, int H, int V) {
     BackwardLayout l{};
@@ -600,7 +606,9 @@ BackwardLayout backward_layout(int T, int H, int V) {
     l.ldg = (l.piece + 63) / 64 * 64;   // rows of whole 128-byte lines
     Carver c;
     l.G = c.take(static_cast<size_t>(T) * l.ldg * 2);
-    l.xs = c.take(static_cast<size_t>(T) * H * 2);
+    l.ldx = (H + 63) / 64 * 64;
+    l.xs = c.take(static_cast<size_t>(T) * l.ldx * 2);
+    l.xa = c.take(l.ldx == H ? 0 : static_cast<size_t>(T) * l.ldx * 2);
     l.scale = c.take((static_cast<size_t>(T) + 1) * sizeof(float));
     l.offsets = c.take(2 * sizeof(int32_t));
     l.splits = moe::dgrad_sum_splits(T, l.piece, H);
@@ -646,7 +654,7 @@ extern "C" moe_status_t moe_cross_entropy_forward(const void* x, const void* W, 
     p.W = static_cast<const uint4*>(W);
     p.V = V;
     p.row_vecs = H / 8;
-    const moe_status_t st = launch_logits<false>(x, W, H, V, p, s);
+    const moe_status_t st = launch_logits<false>(x, H, W, H, V, p, s);
     if (st != MOE_OK) return st;
     // neighbouring tokens' pairs share a sector; with few tokens the latency of
     // a token's own pairs counts
@@ -676,14 +684,16 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
     auto* base = static_cast<uint8_t*>(ws);
     auto* G = reinterpret_cast<__nv_bfloat16*>(base + l.G);
     void* xs = base + l.xs;
+    void* xa = l.ldx == H ? nullptr : base + l.xa;   // x in whole lines (1021 x 1000, V = 50257: 283 -> 275 us)
     auto* scale = reinterpret_cast<float*>(base + l.scale);
     auto* offsets = reinterpret_cast<int32_t*>(base + l.offsets);
     auto* sum = l.pieces > 1 || l.splits > 1 ? reinterpret_cast<float*>(base + l.sum) : nullptr;
     scale_kernel<<<1, 1024, 0, s>>>(dloss, labels, T, V, ignore_index, scale, offsets, err);
     MOE_CHECK_LAUNCH();
     moe_status_t st = MOE_OK;
-    if (dW && (st = moe::launch_after(scale_rows_kernel, dim3((T + 7) / 8), 256, 0, s, static_cast<const uint4*>(x),
-                                      static_cast<const float*>(scale), T, H / 8, static_cast<uint4*>(xs))) != MOE_OK)
+    if ((dW || xa) && (st = moe::launch_after(scale_rows_kernel, dim3((T + 7) / 8), 256, 0, s, static_cast<const uint4*>(x),
+                                              static_cast<const float*>(scale), T, H / 8, l.ldx / 8,
+                                              static_cast<uint4*>(dW ? xs : nullptr), static_cast<uint4*>(xa))) != MOE_OK)
         return st;
     for (int i = 0; i < l.pieces; ++i) {
         Params p{};
@@ -701,7 +711,7 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
         p.lse = lse;
         p.G = G;
         p.ldg = l.ldg;
-        st = launch_logits<true>(x, W, H, V, p, s);
+        st = launch_logits<true>(xa ? xa : x, l.ldx, W, H, V, p, s);
         if (st != MOE_OK) return st;
         const auto* Wp = static_cast<const __nv_bfloat16*>(W) + static_cast<int64_t>(p.v0) * H;
         if (dx && (st = moe::dgrad_sum_gemm(G, l.ldg, Wp, offsets, T, p.cols, H, sum, l.splits, i == 0,
@@ -709,7 +719,7 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
             return st;
         if (dW) {
             auto* dWp = static_cast<__nv_bfloat16*>(dW) + static_cast<int64_t>(p.v0) * H;
-            st = moe::wgrad_gemm(G, l.ldg, xs, nullptr, nullptr, offsets, 1, T, p.cols, H, dWp, s, scale + T);
+            st = moe::wgrad_gemm(G, l.ldg, xs, l.ldx, nullptr, nullptr, offsets, 1, T, p.cols, H, dWp, s, scale + T);
             if (st != MOE_OK) return st;
         }
     }
