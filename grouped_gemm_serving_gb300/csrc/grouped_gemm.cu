@@ -1783,7 +1783,11 @@ moe_status_t moe::dgrad_sum_gemm(const void* dC, int ldc, const void* B, const i
     p.sum_first = first;
     p.sum_last = last;
     p.row_scale = row_scale;
-    p.splits = splits;
+    // a range has at least one k-block: one without would add an accumulator that
+    // no MMA wrote.  A shorter product than the one `splits` was planned for adds to
+    // the first ranges' sums; the first launch has to set them all.
+    p.splits = splits < p.k_blocks ? splits : p.k_blocks;
+    MOE_CHECK_ARG(!first || p.splits == splits);
     p.token_tiles = sum_plan(M, N, K, pairs).token_tiles;
     return launch<false, EPI_SUM, true>(tmB, tmB, tmX, p, s);
 }

@@ -143,6 +143,19 @@ def test_more_logits_than_32_bits(moe):
     _check_backward(dx[rows], None, x[rows], W, labels[rows], lse[rows], dloss[rows])
 
 
+# The vocabulary goes in pieces and the contraction of each piece in two ranges of
+# 64 rows' blocks; the last piece is a single row, so that one range has nothing.
+@pytest.mark.parametrize("T,H,V", [(26941, 8, 92417), (19815, 64, 173057)])
+def test_a_last_piece_of_one_row(moe, T, H, V):
+    g, x, W, labels = _make(T, H, V, 7)
+    loss, lse = _forward(moe, x, W, labels)
+    dloss = torch.ones(T, device="cuda")
+    dx, _ = _backward(moe, x, W, labels, lse, dloss, want=(True, False))
+    assert moe.moe_get_device_error() == 0
+    rows = torch.cat([torch.arange(0, T, 997), torch.tensor([T - 1])]).cuda()
+    _check_backward(dx[rows], None, x[rows], W, labels[rows], lse[rows], dloss[rows])
+
+
 def test_nothing_counts(moe):
     _, x, W, labels = _make(33, 64, 500, 7)
     labels[:] = IGNORE
