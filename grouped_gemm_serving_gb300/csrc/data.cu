@@ -338,7 +338,7 @@ moe_status_t moe::combine_rows(const void* Y2, const int32_t* topk_ids, const fl
     if (!err) return MOE_ERR_CUDA;
     const int sm = moe::sm_count() > 0 ? moe::sm_count() : 148;
     if (T >= sm * kWarpsPerBlock) {   // at least a block of tokens per SM: one warp per token
-        const int blocks = (T + kWarpsPerBlock - 1) / kWarpsPerBlock;
+        const int blocks = (T - 1) / kWarpsPerBlock + 1;
         auto kern = k <= 4 ? combine_kernel<4, 4> : combine_kernel<8, 1>;
         kern<<<blocks, kThreads, 0, s>>>(
             static_cast<const uint4*>(Y2), topk_ids, topk_w, row_pos, T, k, H / 8, E,

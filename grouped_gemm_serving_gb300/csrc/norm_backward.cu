@@ -382,7 +382,7 @@ int launch(const Args& a) {   // the blocks launched, 0 on failure
     static std::atomic<int> resident[moe::kMaxDevices];
     int grid = moe::resident_blocks(reinterpret_cast<const void*>(kern), kThreads, 0, resident);
     if (grid <= 0) return 0;
-    const int room = partial_rows(a.rows, a.H), need = (a.rows + kTeams - 1) / kTeams;
+    const int room = partial_rows(a.rows, a.H), need = (a.rows - 1) / kTeams + 1;
     if (room < grid) grid = room;
     if (need < grid) grid = need;
     kern<<<grid, kThreads, 0, a.stream>>>(

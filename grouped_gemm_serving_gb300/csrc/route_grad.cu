@@ -193,7 +193,7 @@ extern "C" moe_status_t moe_combine_backward(const void* dout, const void* Y2, c
     const auto* y = static_cast<const uint4*>(Y2);
     auto* o = static_cast<uint4*>(dY2);
     if (T >= sm * kWarps) {   // a warp a token fills the GPU
-        const int blocks = (T + kWarps - 1) / kWarps;
+        const int blocks = (T - 1) / kWarps + 1;
         if (k <= 4)
             combine_backward_kernel<32, 4><<<blocks, kThreads, 0, s>>>(d, y, topk_ids, topk_w, row_pos, T, k, H / 8, E, o, dtopk_w, err);
         else
@@ -216,7 +216,7 @@ extern "C" moe_status_t moe_route_backward(const float* logits, const float* exp
     MOE_CHECK_ARG(static_cast<int64_t>(T) * k < INT_MAX);
     MOE_CHECK_ARG(moe::aligned16(logits) && moe::aligned16(expert_bias) && moe::aligned16(dtopk_w) &&
                   moe::aligned16(dlogits));
-    const int blocks = (T + kWarps - 1) / kWarps;
+    const int blocks = (T - 1) / kWarps + 1;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto kern = E <= 32 ? route_backward_kernel<1> : E <= 64 ? route_backward_kernel<2>
               : E <= 128 ? route_backward_kernel<4> : route_backward_kernel<8>;
