@@ -40,6 +40,50 @@ int resident_blocks(const void* kernel, int threads, size_t smem, std::atomic<in
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// For the persistent kernels, whose blocks take an SM each, so that a block can
+// start only where one of the kernel before has ended.  launch_dependents() comes
+// after their own wait, if they have one: a kernel that starts behind one that
+// waited finds everything before that one finished and visible.
+enum class After : int {
+    kAll = 0,      // an ordinary launch
+    kPrimary = 1,  // reads what the kernel before writes: waits for it once its barriers and tensor memory are set up
+    kBeside = 2    // independent of the kernel before, which waited or was an ordinary launch (or runs beside such a
+                   // one): takes the SMs that it frees, and waits for it at the end, so that whatever follows finds
+                   // both finished
+};
+__device__ __forceinline__ void begin_after(After a) {
+    if (a == After::kPrimary) wait_for_primary();
+    launch_dependents();
+}
+__device__ __forceinline__ void end_after(After a) {
+    if (a == After::kBeside) wait_for_primary();
+}
+
+// Launches a kernel of CTA pairs.
+template <typename... P, typename... A>
+moe_status_t launch_pairs(void (*kernel)(P...), int blocks, int threads, size_t smem, cudaStream_t stream, After after,
+                          const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after == After::kAll ? 1 : 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
 template <typename... P, typename... A>
 moe_status_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};

@@ -70,7 +70,8 @@ extern "C" moe_status_t moe_grouped_gemm_dgrad(const void* dC, const void* B, co
     MOE_CHECK_ARG(dC && B && offsets && dA && E >= 1 && E <= kMaxE && M_cap >= 1);
     MOE_CHECK_ARG(N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0);
     MOE_CHECK_ARG(moe::aligned16(dC) && moe::aligned16(B) && moe::aligned16(dA));
-    return moe::dgrad_gemm(dC, B, offsets, E, M_cap, N, K, dA, reinterpret_cast<cudaStream_t>(stream));
+    return moe::dgrad_gemm(dC, B, offsets, E, M_cap, N, K, dA, reinterpret_cast<cudaStream_t>(stream),
+                           moe::After::kAll);
 }
 
 extern "C" size_t moe_grouped_gemm_wgrad_workspace_size(int E, int M_cap, int N, int K) {
@@ -96,5 +97,6 @@ extern "C" moe_status_t moe_grouped_gemm_wgrad(const void* A, const void* dC, co
         static_cast<uint16_t*>(ws), err);
     MOE_CHECK_LAUNCH();
     const auto* tails = static_cast<const uint16_t*>(ws);
-    return moe::wgrad_gemm(dC, N, A, K, tails, tails + static_cast<size_t>(64) * E * N, offsets, E, M_cap, N, K, dB, s);
+    return moe::wgrad_gemm(dC, N, A, K, tails, tails + static_cast<size_t>(64) * E * N, offsets, E, M_cap, N, K, dB, s,
+                           moe::After::kPrimary);
 }

@@ -173,6 +173,7 @@ struct Params {
     int sum_first, sum_last;
     const float* row_scale;
     int splits;
+    moe::After after;
     // EPI_SWIGLU_BACK: out is unused.  With d the tile's gradient of h, feature
     // f < out_cols of row p:  dY1[p, f] = dg, dY1[p, out_cols + f] = du and
     // h[p, f] = silu(g) u from Y1[p] = [g | u] [M_cap, 2 out_cols].  Rows of an
@@ -417,9 +418,34 @@ __device__ __forceinline__ int tile_step() { return PAIR ? gridDim.x >> 1 : grid
 template <int EPI>
 __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, const CUtensorMap* tmW64,
                               uint8_t* stages, Shared& S, const Params& p, int total, uint32_t rank) {
+    constexpr int kStages = Geo<true, EPI>::kStages;
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_par = 0;
     bool ok = true;
+    // one k-block's weights into stage st, by one lane
+    const auto load_weights = [&](const Tile& ti, int st, int kc, int bytes) {
+        const uint32_t fb = moe::map_to_cta(bar(S.full[st]), 0);
+        const uint32_t sa = moe::smem_u32(stages + st * Geo<true, EPI>::kStageBytes);
+        if (rank == 0) moe::mbar_arrive_expect_tx(bar(S.full[st]), bytes);
+        if (plain_tiles(EPI) && p.mn_a) {
+            // two 64-feature x 64-row swizzle atoms, 8 KB apart (one for M = 128)
+            const int f0 = ti.col0 + static_cast<int>(rank) * (ti.half ? 64 : 128);
+            moe::tma_load_3d_pair(sa, tmW, fb, f0, kc, ti.e);
+            if (!ti.half) moe::tma_load_3d_pair(sa + 8192, tmW, fb, f0 + 64, kc, ti.e);
+        } else if (plain_tiles(EPI) && ti.half) {   // 64 weight rows
+            moe::tma_load_3d_pair(sa, tmW64, fb, kc, ti.col0 + static_cast<int>(rank) * 64, ti.e);
+        } else if (plain_tiles(EPI)) {
+            moe::tma_load_3d_pair(sa, tmW, fb, kc, ti.col0 + static_cast<int>(rank) * 128, ti.e);
+        } else if (ti.half) {   // 4 groups: this CTA's 32 features
+            moe::tma_load_5d_pair(sa, tmW64, fb, kc, 0, 0, (ti.col0 + static_cast<int>(rank) * 32) / 8, ti.e);
+        } else {   // 8 groups of (8 gate rows, 8 up rows) of this CTA's 64 features
+            moe::tma_load_5d_pair(sa, tmW, fb, kc, 0, 0, (ti.col0 + static_cast<int>(rank) * 64) / 8, ti.e);
+        }
+    };
+    // behind a kernel that writes the tokens: the ring's first weights, which it
+    // does not write, are on their way while it drains
+    bool waiting = p.after == moe::After::kPrimary;
+    int early = 0;
     for (int t = tile_first<true>(); ok && t < total; t += tile_step<true>()) {
         const Tile ti = decode_tile<true, EPI == EPI_SUM>(t, S, p);
         const int nh = swap_n(ti) / 2;                 // token rows in each CTA: 8 .. 128
@@ -428,6 +454,16 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
         const int xbytes = nh * 128;
         const int abytes = ti.half ? kStageA / 2 : kStageA;   // M = 128: 64 weight rows per CTA
         const int nkb = EPI == EPI_SUM ? ti.nkb : p.k_blocks;
+        const int kb0 = EPI == EPI_SUM ? ti.kb0 : 0;
+        if (waiting) {
+            early = min(nkb, kStages);
+            for (int kb = 0; kb < early; ++kb) {
+                if (moe::elect_one()) load_weights(ti, kb, (kb0 + kb) * 64, 2 * (abytes + xbytes));
+                __syncwarp();
+            }
+            moe::wait_for_primary();
+            waiting = false;
+        }
         for (int kb = 0; kb < nkb; ++kb) {
             const bool got = moe::mbar_wait(bar(S.empty[stage]), phase ^ 1u, &S.abort_flag, kWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
@@ -435,38 +471,25 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
                 break;
             }
             const uint32_t fb = moe::map_to_cta(bar(S.full[stage]), 0);
-            const uint32_t sa = moe::smem_u32(stages + stage * Geo<true, EPI>::kStageBytes);
-            const uint32_t sb = sa + kStageA;
-            const int kc = (EPI == EPI_SUM ? ti.kb0 + kb : kb) * 64;
+            const int kc = (kb0 + kb) * 64;
             if (moe::elect_one()) {
-                if (rank == 0) moe::mbar_arrive_expect_tx(bar(S.full[stage]), 2 * (abytes + xbytes));
-                if (plain_tiles(EPI) && p.mn_a) {
-                    // two 64-feature x 64-row swizzle atoms, 8 KB apart (one for M = 128)
-                    const int f0 = ti.col0 + static_cast<int>(rank) * (ti.half ? 64 : 128);
-                    moe::tma_load_3d_pair(sa, tmW, fb, f0, kc, ti.e);
-                    if (!ti.half) moe::tma_load_3d_pair(sa + 8192, tmW, fb, f0 + 64, kc, ti.e);
-                } else if (plain_tiles(EPI) && ti.half) {   // 64 weight rows
-                    moe::tma_load_3d_pair(sa, tmW64, fb, kc, ti.col0 + static_cast<int>(rank) * 64, ti.e);
-                } else if (plain_tiles(EPI)) {
-                    moe::tma_load_3d_pair(sa, tmW, fb, kc, ti.col0 + static_cast<int>(rank) * 128, ti.e);
-                } else if (ti.half) {   // 4 groups: this CTA's 32 features
-                    moe::tma_load_5d_pair(sa, tmW64, fb, kc, 0, 0, (ti.col0 + static_cast<int>(rank) * 32) / 8, ti.e);
-                } else {   // 8 groups of (8 gate rows, 8 up rows) of this CTA's 64 features
-                    moe::tma_load_5d_pair(sa, tmW, fb, kc, 0, 0, (ti.col0 + static_cast<int>(rank) * 64) / 8, ti.e);
-                }
-                moe::tma_load_2d_pair(sb, tmXh, fb, kc, xrow);
+                if (early == 0) load_weights(ti, stage, kc, 2 * (abytes + xbytes));
+                moe::tma_load_2d_pair(moe::smem_u32(stages + stage * Geo<true, EPI>::kStageBytes) + kStageA, tmXh, fb,
+                                      kc, xrow);
             }
+            if (early > 0) --early;
             __syncwarp();
             issued |= 1u << stage;
             issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-            if (++stage == Geo<true, EPI>::kStages) { stage = 0; phase ^= 1u; }
+            if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
     }
+    if (waiting) moe::wait_for_primary();
     if (!ok && moe::elect_one()) {
         fail(S, p);
         int zero = 0;
         if (rank == 0) {
-            for (int s = 0; s < Geo<true, EPI>::kStages; ++s)
+            for (int s = 0; s < kStages; ++s)
                 if ((issued >> s) & 1u)
                     moe::mbar_wait(bar(S.full[s]), (issued_par >> s) & 1u, &zero, kDrainNs);
         } else {
@@ -1400,6 +1423,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     else __syncthreads();
     moe::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
+    // the pair's producers wait themselves, behind the first weights
+    if (SWAP && warp != 0) moe::begin_after(p.after);
     // tiles (pair tiles when SWAP)
     const int total = S.prefix[p.E] * p.n_tiles * (EPI == EPI_SUM ? p.splits : 1);
 
@@ -1425,6 +1450,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             make_tails(p, warp - 2);
         }
     }
+    if (SWAP) moe::end_after(p.after);
     moe::tc_fence_before();
     if (SWAP) moe::cluster_sync();   // no CTA of the pair leaves while its peer may still signal it
     else __syncthreads();
@@ -1502,23 +1528,7 @@ moe_status_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const TokenM
         MOE_CHECK_LAUNCH();
         return MOE_OK;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmX, p) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
-    return MOE_OK;
+    return moe::launch_pairs(kern, grid, kThreads, kSmemBytes, s, p.after, tmA, tmB, tmX, p);
 }
 
 // Shared by both entry points.  With gx set, A is gathered from token order
@@ -1544,7 +1554,7 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
                               const float* B_scales, const int32_t* offsets, int E, int M_cap, int N, int K,
                               moe_epilogue_t epilogue, void* C, float* C_scales, moe_stream_t stream,
                               bool weights_mn = false, const FusedCombine* fc = nullptr, void* keep = nullptr,
-                              const moe::SwigluBack* back = nullptr) {
+                              const moe::SwigluBack* back = nullptr, moe::After after = moe::After::kAll) {
     MOE_CHECK_ARG(A && B && offsets && (C || back) && E >= 1 && E <= kMaxE && M_cap >= 1 && N >= 8 && K >= 8);
     MOE_CHECK_ARG(moe::aligned16(A) && moe::aligned16(B) && moe::aligned16(C));
     const bool fp8 = dtype == MOE_FP8_E4M3_B128;
@@ -1655,6 +1665,7 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
     p.mn_a = weights_mn ? 1 : 0;
     p.fc = 0;
     p.keep = keep;
+    p.after = after;
     if (keep && (fp8 || !swiglu || gx)) return MOE_ERR_UNSUPPORTED;
     if (back) {
         if (!weights_mn) return MOE_ERR_UNSUPPORTED;
@@ -1700,13 +1711,21 @@ moe_status_t run_grouped_gemm(moe_dtype_t dtype, const void* A, const float* A_s
 
 }  // namespace
 
+moe_status_t moe::store_gemm(const void* A, const void* B, const int32_t* offsets, int E, int M_cap, int N, int K,
+                             void* C, cudaStream_t s, After after) {
+    return run_grouped_gemm(MOE_BF16, A, nullptr, nullptr, nullptr, 0, 0, B, nullptr, offsets, E, M_cap, N, K,
+                            MOE_EPI_STORE, C, nullptr, reinterpret_cast<moe_stream_t>(s), false, nullptr, nullptr,
+                            nullptr, after);
+}
+
 moe_status_t moe::dgrad_gemm(const void* dC, const void* B, const int32_t* offsets, int E, int M_cap, int N, int K,
-                             void* dA, cudaStream_t s) {
+                             void* dA, cudaStream_t s, After after) {
     // dA [M_cap, K] = dC [M_cap, N] x B[e] [N, K]: a store GEMM with K output
     // features over an N-long contraction, the weights B [E, N, K] read
     // MN-major in place
     return run_grouped_gemm(MOE_BF16, dC, nullptr, nullptr, nullptr, 0, 0, B, nullptr, offsets, E, M_cap, K, N,
-                            MOE_EPI_STORE, dA, nullptr, reinterpret_cast<moe_stream_t>(s), true);
+                            MOE_EPI_STORE, dA, nullptr, reinterpret_cast<moe_stream_t>(s), true, nullptr, nullptr, nullptr,
+                            after);
 }
 
 moe_status_t moe::swiglu_back_gemm(const void* dy, const void* W2, const int32_t* offsets, int E, int M_cap, int H,
@@ -1749,7 +1768,7 @@ int moe::dgrad_sum_splits(int M, int N, int K) {
 
 moe_status_t moe::dgrad_sum_gemm(const void* dC, int ldc, const void* B, const int32_t* offsets, int M, int N, int K,
                                  float* sum, int splits, bool first, bool last, const float* row_scale, void* dA,
-                                 cudaStream_t s) {
+                                 cudaStream_t s, After after) {
     MOE_CHECK_ARG(dC && B && offsets && M >= 1 && N >= 1 && ldc >= N && ldc % 8 == 0 && K >= 8 && K % 8 == 0);
     MOE_CHECK_ARG(splits >= 1 && (splits == 1 || !last) && (sum || (first && last)) && (dA || !last));
     MOE_CHECK_ARG(moe::aligned16(dC) && moe::aligned16(B) && moe::aligned16(sum) && moe::aligned16(dA));
@@ -1783,6 +1802,7 @@ moe_status_t moe::dgrad_sum_gemm(const void* dC, int ldc, const void* B, const i
     p.sum_first = first;
     p.sum_last = last;
     p.row_scale = row_scale;
+    p.after = after;
     // a range has at least one k-block: one without would add an accumulator that
     // no MMA wrote.  A shorter product than the one `splits` was planned for adds to
     // the first ranges' sums; the first launch has to set them all.

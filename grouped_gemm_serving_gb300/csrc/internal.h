@@ -8,12 +8,19 @@
 
 namespace moe {
 
+enum class After : int;   // what a kernel's start and end wait for (common.cuh)
+
+// C[p, n] = sum_k A[p, k] B[e, n, k]: the grouped GEMM without epilogue, bf16,
+// as one of several launches.
+moe_status_t store_gemm(const void* A, const void* B, const int32_t* offsets, int E, int M_cap, int N, int K, void* C,
+                        cudaStream_t stream, After after);
+
 // Launches the bf16 grouped GEMM for the data gradient (grouped_gemm.cu):
 //   dA[p, c] = sum_n dC[p, n] * B[e, n, c]   (rows p of expert e)
 // with B [E, N, K] read in place (MN-major); rows p >= offsets[E] of dA are
 // zeros.  dC bf16 [M_cap, N], dA bf16 [M_cap, K].
 moe_status_t dgrad_gemm(const void* dC, const void* B, const int32_t* offsets, int E, int M_cap, int N, int K,
-                        void* dA, cudaStream_t stream);
+                        void* dA, cudaStream_t stream, After after);
 
 // The data gradient of fc2 with the gradient of silu(gate) * up applied to it
 // in the epilogue (grouped_gemm.cu): with dh[p] = dy[p] W2[e] in fp32 and
@@ -42,7 +49,7 @@ moe_status_t swiglu_back_gemm(const void* dy, const void* W2, const int32_t* off
 // device, or NULL) multiplies dB in fp32 before it is rounded.
 moe_status_t wgrad_gemm(const void* dC, int ldc, const void* A, int lda, const void* tail_c, const void* tail_a,
                         const int32_t* offsets, int E, int M_cap, int N, int K, void* dB, cudaStream_t stream,
-                        const float* scale = nullptr);
+                        After after, const float* scale = nullptr);
 
 // The data gradient of one expert of M rows, its contraction split over
 // several launches and, within one, over `splits` ranges (grouped_gemm.cu): with
@@ -56,7 +63,7 @@ moe_status_t wgrad_gemm(const void* dC, int ldc, const void* A, int lda, const v
 int dgrad_sum_splits(int M, int N, int K);
 moe_status_t dgrad_sum_gemm(const void* dC, int ldc, const void* B, const int32_t* offsets, int M, int N, int K,
                             float* sum, int splits, bool first, bool last, const float* row_scale, void* dA,
-                            cudaStream_t stream);
+                            cudaStream_t stream, After after);
 
 // A tensor map for tiles staged with the 128-byte swizzle, zeros outside
 // (grouped_gemm.cu): bytes for FP8, else bf16; dims and box innermost first,

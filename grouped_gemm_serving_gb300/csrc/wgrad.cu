@@ -47,6 +47,7 @@ struct Params {
     int* err;
     int E, M_cap, N, K;
     int row_tiles, col_tiles;
+    moe::After after;
     int tails;             // 0: rows past offsets[E] lie outside the tensor maps (zeros)
 };
 
@@ -287,10 +288,12 @@ wgrad_kernel(const __grid_constant__ Maps maps, const Params p) {
     moe::cluster_sync();   // the peer's barriers exist before anyone signals them
     moe::tc_fence_after();
     const uint32_t tmem = S.tmem_base;
+    moe::begin_after(p.after);
     const int total = p.E * p.row_tiles * p.col_tiles;
     if (warp >= 4) epilogue(transposes, S, p, total, tmem, rank);
     else if (warp == 0) producer(maps, stages, S, p, total, rank);
     else if (warp == 1 && rank == 0) mma_issuer(stages, S, p, total, tmem);
+    moe::end_after(p.after);
     moe::tc_fence_before();
     moe::cluster_sync();   // no CTA of the pair leaves while its peer may still signal it
     if (warp == 1) {
@@ -310,7 +313,7 @@ bool encode_operand(CUtensorMap* map, const void* base, int cols, int ld, int64_
 
 moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, int lda, const void* tail_c, const void* tail_a,
                              const int32_t* offsets, int E, int M_cap, int N, int K, void* dB, cudaStream_t s,
-                             const float* scale) {
+                             After after, const float* scale) {
     MOE_CHECK_ARG(dC && A && (tail_c && tail_a ? true : E == 1) && offsets && dB && E >= 1 && E <= kMaxE && M_cap >= 1);
     MOE_CHECK_ARG(N >= 1 && ldc >= N && ldc % 8 == 0 && K >= 8 && K % 8 == 0 && lda >= K && lda % 8 == 0);
     MOE_CHECK_ARG(moe::aligned16(dC) && moe::aligned16(A) && moe::aligned16(tail_c) && moe::aligned16(tail_a) &&
@@ -319,6 +322,7 @@ moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, int lda, co
     p.offsets = offsets;
     p.out = static_cast<__nv_bfloat16*>(dB);
     p.scale = scale;
+    p.after = after;
     p.err = moe::device_error_word();
     if (!p.err) return MOE_ERR_CUDA;
     p.E = E;
@@ -348,21 +352,5 @@ moe_status_t moe::wgrad_gemm(const void* dC, int ldc, const void* A, int lda, co
     int pairs = moe::sm_count() / 2;
     if (pairs <= 0) return MOE_ERR_CUDA;
     if (tiles < pairs) pairs = static_cast<int>(tiles);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, wgrad_kernel, maps, p) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
-    return MOE_OK;
+    return moe::launch_pairs(wgrad_kernel, 2 * pairs, kThreads, kSmemBytes, s, p.after, maps, p);
 }
