@@ -4,7 +4,7 @@
 //
 //   z[t, v] = sum_c x[t, c] W[v, c],   lse[t] = log sum_v exp z[t, v],
 //   loss[t] = lse[t] - z[t, label[t]]
-//   G[t, v] = exp(z[t, v] - lse[t]) - [v = label[t]]
+//   G[t, v] = exp(z[t, v] - lse[t]) - [v = label[t]]   (the label's from the fp32 dot product below)
 //   dx[t] = dloss[t] sum_v G[t, v] W[v],   dW[v] = sum_t G[t, v] dloss[t] x[t]
 //
 // Forward: the logits kernel below computes z tile by tile in tensor memory
@@ -87,6 +87,7 @@ struct Params {
     int V, row_vecs;
     // backward
     const float* lse;
+    const float* g_label;   // [T]: the label's entry of G
     __nv_bfloat16* G;     // [T, ldg]; columns from cols on are never read
     int ldg;
 };
@@ -247,8 +248,11 @@ __device__ void epilogue(uint8_t* stages, Shared& S, const Params& p, int total,
         const int label = row < p.T ? p.labels[row] : p.ignore;
         const bool counts = label != p.ignore && label >= 0;
         const int rel = counts ? label - p.v0 - col0 : -1;   // the label's column, in the tile if 0 <= rel < ncols
-        float neg_lse = 0.0f;
-        if (BACK && row < p.T) neg_lse = -p.lse[row] * kLog2e;
+        float neg_lse = 0.0f, g_label = 0.0f;
+        if (BACK && row < p.T) {
+            neg_lse = -p.lse[row] * kLog2e;
+            g_label = p.g_label[row];
+        }
         if (!moe::mbar_wait(bar(S.acc_full[acc]), acc_phase, &S.abort_flag, kWaitNs)) { fail(S, p); return; }
         moe::tc_fence_after();
         const uint32_t ta = lane_base + static_cast<uint32_t>(acc * BV);
@@ -288,7 +292,7 @@ __device__ void epilogue(uint8_t* stages, Shared& S, const Params& p, int total,
                 if (counts && rel >= col && rel < min(col + 32, ncols))
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (rel == col + j) g[j] -= 1.0f;
+                        if (rel == col + j) g[j] = g_label;
                 if (!counts || col + 32 > ncols)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -324,28 +328,33 @@ __device__ void epilogue(uint8_t* stages, Shared& S, const Params& p, int total,
     }
 }
 
-// The labels' logits, a warp a token: x[t] and W[label] in fp32.
+// A label's logit, by a warp, from x[t] and W[label] in fp32: the same bits in
+// both passes.
+__device__ __forceinline__ float label_dot(const uint4* __restrict__ x, const uint4* __restrict__ w, int vecs) {
+    float dot = 0.0f;
+#pragma unroll 4
+    for (int c = threadIdx.x & 31; c < vecs; c += 32) {
+        const uint4 a = __ldg(x + c), b = __ldg(w + c);
+        const uint32_t a4[4] = {a.x, a.y, a.z, a.w}, b4[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dot = fmaf(moe::bf16_lo(a4[i]), moe::bf16_lo(b4[i]), dot);
+            dot = fmaf(moe::bf16_hi(a4[i]), moe::bf16_hi(b4[i]), dot);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    return dot;
+}
+
+// The labels' logits, a warp a token.
 __device__ void label_logits(const Params& p, int warp) {
-    const int lane = threadIdx.x & 31;
     for (int t = blockIdx.x * 2 + warp; t < p.T; t += gridDim.x * 2) {
         const int label = p.labels[t];
         if (label == p.ignore || label < 0 || label >= p.V) continue;
-        const uint4* x = p.x + static_cast<int64_t>(t) * p.row_vecs;
-        const uint4* w = p.W + static_cast<int64_t>(label) * p.row_vecs;
-        float dot = 0.0f;
-#pragma unroll 4
-        for (int c = lane; c < p.row_vecs; c += 32) {
-            const uint4 a = __ldg(x + c), b = __ldg(w + c);
-            const uint32_t a4[4] = {a.x, a.y, a.z, a.w}, b4[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dot = fmaf(moe::bf16_lo(a4[i]), moe::bf16_lo(b4[i]), dot);
-                dot = fmaf(moe::bf16_hi(a4[i]), moe::bf16_hi(b4[i]), dot);
-            }
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        if (lane == 0) p.at_label[t] = dot;
+        const float dot = label_dot(p.x + static_cast<int64_t>(t) * p.row_vecs,
+                                    p.W + static_cast<int64_t>(label) * p.row_vecs, p.row_vecs);
+        if ((threadIdx.x & 31) == 0) p.at_label[t] = dot;
     }
 }
 
@@ -388,8 +397,7 @@ logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     else if (warp == 0) producer<kStagesOf<BACK>>(&tmX, &tmW, stages, S, p, total, rank);
     else if (warp == 1 && rank == 0) mma_issuer<kStagesOf<BACK>>(stages, S, p, total, tmem);
     else if (!BACK && warp >= 2) label_logits(p, warp - 2);
-    if (BACK) moe::end_after(p.after);
-    else moe::launch_dependents();
+    if (!BACK) moe::launch_dependents();
     moe::tc_fence_before();
     moe::cluster_sync();   // no CTA of the pair leaves while its peer may still signal it
     if (warp == 1) {
@@ -477,16 +485,25 @@ scale_kernel(const float* __restrict__ dloss, const int32_t* __restrict__ labels
     }
 }
 
-// xs[t] = bf16(scale[t] / scale[T] * x[t]), zeros where scale[t] is 0, and a copy
-// xa of x (either may be NULL), rows ld_vecs vectors apart: whole 128-byte
-// lines, so that no box of the products that read them straddles two.
+// A warp a token:  g_label[t] = exp(z_l - lse[t]) - 1 with the label's logit as in
+// the forward pass (the tensor cores' would be off by more than a nearly certain
+// label's entry);  xs[t] = bf16(scale[t] / scale[T] * x[t]), zeros where scale[t] is
+// 0, and a copy xa of x (either may be NULL), rows ld_vecs vectors apart: whole
+// 128-byte lines, so that no box of the products that read them straddles two.
 __global__ void __launch_bounds__(256)
-scale_rows_kernel(const uint4* __restrict__ x, const float* scale, int T, int row_vecs, int ld_vecs,
-                  uint4* __restrict__ xs, uint4* __restrict__ xa) {
+token_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ W, const int32_t* __restrict__ labels,
+                  const float* __restrict__ lse, const float* scale, int T, int V, int ignore, int row_vecs, int ld_vecs,
+                  float* __restrict__ g_label, uint4* __restrict__ xs, uint4* __restrict__ xa) {
     moe::begin_after(moe::After::kPrimary);
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (t >= T) return;
+    const int label = labels[t];
+    if (label != ignore && label >= 0 && label < V) {   // the same for the whole warp
+        const float z = label_dot(x + static_cast<int64_t>(t) * row_vecs, W + static_cast<int64_t>(label) * row_vecs, row_vecs);
+        if (lane == 0) g_label[t] = expm1f(z - lse[t]);
+    }
+    if (!xs && !xa) return;
     const float d = scale[t], r = d == 0.0f ? 0.0f : __fdiv_rn(d, scale[T]);
     for (int c = lane; c < row_vecs; c += 32) {
         const uint4 v = __ldg(x + static_cast<int64_t>(t) * row_vecs + c);
@@ -601,7 +618,7 @@ constexpr int kPieceMin = 2048;
 
 struct BackwardLayout {
     int piece, pieces, ldg, splits, ldx;
-    size_t G, xs, xa, scale, offsets, sum, total;
+    size_t G, xs, xa, g_label, scale, offsets, sum, total;
 };
 BackwardLayout backward_layout(int T, int H, int V) {
     BackwardLayout l{};
@@ -617,6 +634,7 @@ BackwardLayout backward_layout(int T, int H, int V) {
     l.ldx = (H + 63) / 64 * 64;
     l.xs = c.take(static_cast<size_t>(T) * l.ldx * 2);
     l.xa = c.take(l.ldx == H ? 0 : static_cast<size_t>(T) * l.ldx * 2);
+    l.g_label = c.take(static_cast<size_t>(T) * sizeof(float));
     l.scale = c.take((static_cast<size_t>(T) + 1) * sizeof(float));
     l.offsets = c.take(2 * sizeof(int32_t));
     l.splits = moe::dgrad_sum_splits(T, l.piece, H);
@@ -693,16 +711,17 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
     auto* G = reinterpret_cast<__nv_bfloat16*>(base + l.G);
     void* xs = base + l.xs;
     void* xa = l.ldx == H ? nullptr : base + l.xa;   // x in whole lines (1021 x 1000, V = 50257: 283 -> 275 us)
+    auto* g_label = reinterpret_cast<float*>(base + l.g_label);
     auto* scale = reinterpret_cast<float*>(base + l.scale);
     auto* offsets = reinterpret_cast<int32_t*>(base + l.offsets);
     auto* sum = l.pieces > 1 || l.splits > 1 ? reinterpret_cast<float*>(base + l.sum) : nullptr;
     scale_kernel<<<1, 1024, 0, s>>>(dloss, labels, T, V, ignore_index, scale, offsets, err);
     MOE_CHECK_LAUNCH();
-    moe_status_t st = MOE_OK;
-    if ((dW || xa) && (st = moe::launch_after(scale_rows_kernel, dim3((T + 7) / 8), 256, 0, s, static_cast<const uint4*>(x),
-                                              static_cast<const float*>(scale), T, H / 8, l.ldx / 8,
-                                              static_cast<uint4*>(dW ? xs : nullptr), static_cast<uint4*>(xa))) != MOE_OK)
-        return st;
+    moe_status_t st = moe::launch_after(
+        token_rows_kernel, dim3((T + 7) / 8), 256, 0, s, static_cast<const uint4*>(x), static_cast<const uint4*>(W), labels,
+        lse, static_cast<const float*>(scale), T, V, ignore_index, H / 8, l.ldx / 8, g_label,
+        static_cast<uint4*>(dW ? xs : nullptr), static_cast<uint4*>(xa));
+    if (st != MOE_OK) return st;
     for (int i = 0; i < l.pieces; ++i) {
         Params p{};
         p.labels = labels;
@@ -719,9 +738,8 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
         p.lse = lse;
         p.G = G;
         p.ldg = l.ldg;
-        // the first piece's logits need nothing of the scaled rows, unless x is their
-        // copy (16 x 2048, V = 32000: 117 -> 110 us); scale_kernel has ended when they start
-        p.after = i == 0 && dW && !xa ? moe::After::kBeside : moe::After::kPrimary;
+        p.g_label = g_label;
+        p.after = moe::After::kPrimary;
         st = launch_logits<true>(xa ? xa : x, l.ldx, W, H, V, p, s);
         if (st != MOE_OK) return st;
         const auto* Wp = static_cast<const __nv_bfloat16*>(W) + static_cast<int64_t>(p.v0) * H;

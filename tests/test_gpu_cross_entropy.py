@@ -156,6 +156,35 @@ def test_a_last_piece_of_one_row(moe, T, H, V):
     _check_backward(dx[rows], None, x[rows], W, labels[rows], lse[rows], dloss[rows])
 
 
+@pytest.mark.parametrize("T,H,V,c", [(200, 2880, 5000, 18), (64, 4096, 3001, 20), (5, 1000, 1, 20), (300, 512, 2, 8)])
+def test_nearly_certain_labels(moe, T, H, V, c):
+    """The label's entry of the gradient is minus the little that the other words have."""
+    g, x, W, labels = _make(T, H, V, 11)
+    x = (W[labels.long()].double() * c).to(torch.bfloat16)
+    _, lse = _forward(moe, x, W, labels)
+    dloss = torch.ones(T, device="cuda")
+    dx, dW = _backward(moe, x, W, labels, lse, dloss)
+    assert moe.moe_get_device_error() == 0
+    X, M = x.double(), W.double()
+    z = X @ M.t()
+    G = torch.softmax(z, 1)
+    one = torch.nn.functional.one_hot(labels.long(), V).double()
+    P = G * (1 - one)
+    G = P - one * P.sum(1, keepdim=True)
+    # z_l: 2 H / 64 + 6 roundings of a warp's partial sums, independent, each at most EPS of a sum that stays below
+    # z_l (six standard deviations stay below 6 EPS of it); lse: its own rounding and a few of the logarithm's
+    dg = (6 * z.amax(1, keepdim=True) + 8 * lse.double().abs()[:, None] + 8) * EPS
+    # the other words' logits come from the tensor cores
+    zs = (X.square() @ M.square().t()).sqrt().amax()
+    dp = _acc(H) * zs + 8 * EPS * (1 + z.abs().amax())
+    noise = ((NOISE + 2.0 ** -12) * G).square()
+    ref = G @ M
+    within(dx, ref, rounded(ref, torch.bfloat16) + (noise @ M.square()).sqrt() + dg * M[labels.long()].abs() + dp * (P @ M.abs()))
+    ref = G.t() @ X
+    within(dW, ref, rounded(ref, torch.bfloat16) + (2 * noise.t() @ X.square()).sqrt() + (one * dg).t() @ X.abs()
+           + dp * (P.t() @ X.abs()))
+
+
 def test_nothing_counts(moe):
     _, x, W, labels = _make(33, 64, 500, 7)
     labels[:] = IGNORE
