@@ -93,7 +93,7 @@ class Block:
         moe.moe_ffn_backward(self.xp, w["W1"], w["W2"], self.Y1, self.dY2, r["offsets"], E, T * k, H, I, self.dxp, self.dW1,
                              self.dW2, *self.ws_ffn)
         moe.moe_permute_backward(self.dxp, r["ids"], r["row_pos"], T, k, H, E, self.dn1)
-        moe.moe_route_backward(self.logits, None, self.dw, T, E, k, True, self.dlogits)
+        moe.moe_route_backward_ids(self.logits, None, r["ids"], self.dw, T, E, k, True, self.dlogits)
         drouter = self.dlogits.t() @ self.n1.float()
         self.dn1 += (self.dlogits @ w["router"]).to(BF16)
         self.norm_backward(self.dn1, self.x, w["norm1"], self.mean1, self.rstd1, self.dx, self.dnorm1, self.dbias1)

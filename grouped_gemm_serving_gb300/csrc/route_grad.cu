@@ -10,10 +10,12 @@
 //           is read from HBM once however many slots there are; bound by HBM
 //           (dout and Y2 read, dY2 written).
 // permute   xp[p] = x[t]:  dx[t] = sum_j dxp[p], the combine with unit weights.
-// softmax   a warp a token: the picks are found again from the logits (a
-//           masked slot's expert is no longer in topk_ids), then
+// softmax   a warp a token:
 //             renormalised  dl[e_j] = p_j (dw_j - sum_i p_i dw_i), others 0
 //             full          dl[e] = p_e ([e picked as j] dw_j - sum_i p_{e_i} dw_i).
+//           With the caller's ids a live slot names its expert, and only a
+//           masked slot's (it is no longer in the ids) is found again from the
+//           logits; without them all picks are, in moe_route_sort's order.
 #include <climits>
 
 #include "common.cuh"
@@ -111,11 +113,11 @@ combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict_
         if (lane == g && j0 + g < k) dw[static_cast<int64_t>(t) * k + j0 + g] = dot[g];
 }
 
-template <int NV>   // logits per lane: E <= 32 * NV
+template <int NV, bool IDS>   // logits per lane: E <= 32 * NV
 __global__ void __launch_bounds__(kThreads)
 route_backward_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
-                      const float* __restrict__ dw, int T, int E, int k, int renormalize,
-                      float* __restrict__ dlogits) {
+                      const int32_t* __restrict__ ids, const float* __restrict__ dw, int T, int E, int k,
+                      int renormalize, float* __restrict__ dlogits, int* err) {
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= T) return;
@@ -131,9 +133,32 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         key[j] = e < E ? moe::order_key(v[j]) : 0u;
     }
     const float my_dw = lane < k ? dw[static_cast<int64_t>(t) * k + lane] : 0.0f;
+    const auto pick = [&](int e, float g) {
+        if ((e & 31) != lane) return;
+        picked |= 1u << (e >> 5);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (j == (e >> 5)) up[j] = g;
+    };
+    int open = k;   // picks that are still to be found
+    if (IDS) {
+        // an expert belongs to the first slot that names it; an id outside [0, E] and
+        // a repeated one are reported and their slots taken as masked
+        const int id = lane < k ? ids[static_cast<int64_t>(t) * k + lane] : E;
+        const bool names = id >= 0 && id < E;
+        const unsigned same = __match_any_sync(0xffffffffu, names ? id : -1 - lane);
+        const bool live = names && __ffs(same) - 1 == lane;
+        if (!live && id != E) moe::raise_device_error(err, MOE_DEVERR_ROUTE);
+        for (unsigned left = __ballot_sync(0xffffffffu, live); left; left &= left - 1) {
+            const int r = __ffs(left) - 1;
+            pick(__shfl_sync(0xffffffffu, id, r), __shfl_sync(0xffffffffu, my_dw, r));
+            --open;
+        }
+    }
     float top = -INFINITY;
-    // the picks, as moe_route_sort makes them: largest key, then lowest id
-    for (int r = 0; r < k; ++r) {
+    // the picks (with ids: the masked slots'), as moe_route_sort makes them: largest
+    // key, then lowest id
+    for (int r = 0; r < open; ++r) {
         uint32_t bk = 0u;
         int bj = 0;
 #pragma unroll
@@ -143,15 +168,17 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         }
         const uint32_t m = __reduce_max_sync(0xffffffffu, bk);
         if (m == 0u) break;   // fewer than k numbers among the logits: the same for the whole warp
-        const int bi = __reduce_min_sync(0xffffffffu, bk == m ? lane + 32 * bj : INT_MAX);
-        const float g = __shfl_sync(0xffffffffu, my_dw, r);
-        if (r == 0) top = moe::key_value(m);
-        if ((bi & 31) == lane) {
-            picked |= 1u << (bi >> 5);
+        if (!IDS && r == 0) top = moe::key_value(m);
+        pick(__reduce_min_sync(0xffffffffu, bk == m ? lane + 32 * bj : INT_MAX),
+             IDS ? 0.0f : __shfl_sync(0xffffffffu, my_dw, r));
+    }
+    if (IDS) {   // the largest logit that the softmax runs over
+        uint32_t bk = 0u;
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (j == (bi >> 5)) up[j] = g;
-        }
+        for (int j = 0; j < NV; ++j)
+            if (!renormalize || ((picked >> j) & 1u)) bk = max(bk, key[j]);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, bk);
+        if (m != 0u) top = moe::key_value(m);
     }
     float sum = 0.0f, dot = 0.0f, p[NV];
 #pragma unroll
@@ -173,6 +200,23 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         const bool in = renormalize ? (picked >> j) & 1u : true;
         if (e < E) dlogits[static_cast<int64_t>(t) * E + e] = in ? p[j] / sum * (up[j] - dot) : 0.0f;
     }
+}
+
+template <bool IDS>
+moe_status_t route_backward(const float* logits, const float* bias, const int32_t* ids, const float* dw, int T, int E,
+                            int k, int renormalize, float* dlogits, cudaStream_t s) {
+    MOE_CHECK_ARG(logits && dw && dlogits && T >= 1 && E >= 1 && E <= 256 && k >= 1 && k <= 32 && k <= E);
+    MOE_CHECK_ARG(static_cast<int64_t>(T) * k < INT_MAX);
+    MOE_CHECK_ARG(moe::aligned16(logits) && moe::aligned16(bias) && moe::aligned16(ids) && moe::aligned16(dw) &&
+                  moe::aligned16(dlogits));
+    int* err = IDS ? moe::device_error_word() : nullptr;
+    if (IDS && !err) return MOE_ERR_CUDA;
+    const int blocks = (T - 1) / kWarps + 1;
+    auto kern = E <= 32 ? route_backward_kernel<1, IDS> : E <= 64 ? route_backward_kernel<2, IDS>
+              : E <= 128 ? route_backward_kernel<4, IDS> : route_backward_kernel<8, IDS>;
+    kern<<<blocks, kThreads, 0, s>>>(logits, bias, ids, dw, T, E, k, renormalize, dlogits, err);
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
 }
 
 }  // namespace
@@ -212,15 +256,14 @@ extern "C" moe_status_t moe_permute_backward(const void* dxp, const int32_t* top
 
 extern "C" moe_status_t moe_route_backward(const float* logits, const float* expert_bias, const float* dtopk_w, int T,
                                            int E, int k, int renormalize, float* dlogits, moe_stream_t stream) {
-    MOE_CHECK_ARG(logits && dtopk_w && dlogits && T >= 1 && E >= 1 && E <= 256 && k >= 1 && k <= 32 && k <= E);
-    MOE_CHECK_ARG(static_cast<int64_t>(T) * k < INT_MAX);
-    MOE_CHECK_ARG(moe::aligned16(logits) && moe::aligned16(expert_bias) && moe::aligned16(dtopk_w) &&
-                  moe::aligned16(dlogits));
-    const int blocks = (T - 1) / kWarps + 1;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto kern = E <= 32 ? route_backward_kernel<1> : E <= 64 ? route_backward_kernel<2>
-              : E <= 128 ? route_backward_kernel<4> : route_backward_kernel<8>;
-    kern<<<blocks, kThreads, 0, s>>>(logits, expert_bias, dtopk_w, T, E, k, renormalize, dlogits);
-    MOE_CHECK_LAUNCH();
-    return MOE_OK;
+    return route_backward<false>(logits, expert_bias, nullptr, dtopk_w, T, E, k, renormalize, dlogits,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" moe_status_t moe_route_backward_ids(const float* logits, const float* expert_bias, const int32_t* topk_ids,
+                                               const float* dtopk_w, int T, int E, int k, int renormalize,
+                                               float* dlogits, moe_stream_t stream) {
+    MOE_CHECK_ARG(topk_ids);
+    return route_backward<true>(logits, expert_bias, topk_ids, dtopk_w, T, E, k, renormalize, dlogits,
+                                reinterpret_cast<cudaStream_t>(stream));
 }

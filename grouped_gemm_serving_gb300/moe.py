@@ -73,6 +73,7 @@ _SIGS = {
     "moe_combine_backward": (_S, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
     "moe_permute_backward": (_S, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_route_backward": (_S, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_route_backward_ids": (_S, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_layer_norm_forward": (_S, [_I, _P, _L, _I, _I, _I, _P, _P, _F, _P, _L, _P, _P, _P]),
     "moe_layer_norm_backward_workspace_size": (_Z, [_I, _I]),
     "moe_layer_norm_backward": (_S, [_I, _P, _L, _P, _L, _I, _I, _I, _P, _P, _P, _P, _L, _P, _P, _P, _Z, _P]),
@@ -281,6 +282,11 @@ def moe_permute_backward(dxp, topk_ids, row_pos, T, k, H, E, dx, stream=None):
 def moe_route_backward(logits, expert_bias, dtopk_w, T, E, k, renormalize, dlogits, stream=None):
     _check(lib().moe_route_backward(_p(logits), _p(expert_bias), _p(dtopk_w), T, E, k, int(renormalize),
                                     _p(dlogits), _stream(stream)), "moe_route_backward")
+
+
+def moe_route_backward_ids(logits, expert_bias, topk_ids, dtopk_w, T, E, k, renormalize, dlogits, stream=None):
+    _check(lib().moe_route_backward_ids(_p(logits), _p(expert_bias), _p(topk_ids), _p(dtopk_w), T, E, k,
+                                        int(renormalize), _p(dlogits), _stream(stream)), "moe_route_backward_ids")
 
 
 def moe_layer_norm_forward(dtype, x, ldx, rows, H, w_dtype, weight, bias, eps, y, ldy, mean, rstd, stream=None):

@@ -73,7 +73,7 @@ typedef enum {
 #define MOE_DEVERR_NONE 0
 #define MOE_DEVERR_OFFSETS 1 /* offsets[0] != 0, decreasing, or offsets[E] > M_cap */
 #define MOE_DEVERR_TIMEOUT 2 /* an mbarrier wait inside a GEMM exceeded its time limit */
-#define MOE_DEVERR_ROUTE 3   /* an expert id outside [0, E] reached the sort */
+#define MOE_DEVERR_ROUTE 3   /* an expert id outside [0, E] reached the sort or the routing's gradient */
 #define MOE_DEVERR_LABEL 4   /* a label outside [0, V) that is not ignore_index */
 
 typedef enum {
@@ -417,14 +417,23 @@ moe_status_t moe_ffn_backward(const void* x, const void* W1, const void* W2, con
  *   topk_ids[t, j] != E of dxp[row_pos[t*k + j], :], in fp32 in j order,
  *   rounded to bf16 (moe_combine with unit weights).  dxp bf16 [T*k, H]; dx
  *   bf16 [T, H].
- * moe_route_backward (of moe_route_sort's weights):  dlogits fp32 [T, E], the
+ * moe_route_backward_ids (of the router's weights):  dlogits fp32 [T, E], the
  *   gradient of the logits (and, summed over t, of expert_bias) from that of
- *   the weights.  The picks are found again from logits and expert_bias, by
- *   moe_route_sort's rule, so slots that a sentinel mask took out (their
- *   dtopk_w is 0) still count in the softmax as they did forward.  With p the
- *   softmax over the picks (renormalize != 0) or over E (== 0) and S = sum over
- *   picks of p_i dtopk_w_i:  dlogits[e] = p_e * (dtopk_w_j - S) for the pick j
- *   of expert e; elsewhere 0 (renormalize != 0) or -p_e * S.
+ *   the weights, for the picks in topk_ids: those of moe_route_sort or of any
+ *   other router, in any order of equal logits.  With p the softmax over the
+ *   picks (renormalize != 0) or over E (== 0) and S = sum over picks of p_i
+ *   dtopk_w_i:  dlogits[e] = p_e * (dtopk_w_j - S) for the pick j of expert e;
+ *   elsewhere 0 (renormalize != 0) or -p_e * S.  A sentinel slot (id E) had a
+ *   pick too when the weights were made, which still counts in the softmax: a
+ *   token with s of them gets the s largest logits among its other experts,
+ *   ties to the lower id, with a gradient of 0 (their dtopk_w is not read into
+ *   anything).  An id outside [0, E], or one that an earlier slot of the token
+ *   has, is recorded as MOE_DEVERR_ROUTE and its slot taken as a sentinel.
+ * moe_route_backward:  the same without topk_ids: all picks are found again
+ *   from logits and expert_bias by moe_route_sort's rule (ties to the lower
+ *   id), and dtopk_w has its slots in that order.  Only for picks that
+ *   moe_route_sort made from the same logits; another router's slots may be in
+ *   another order where logits are equal.
  * Limits: 1 <= E <= 256 (route), 1 <= k <= 32, k <= E (route), T >= 1,
  *   T*k < 2^31, H a positive multiple of 8.
  */
@@ -435,6 +444,9 @@ moe_status_t moe_permute_backward(const void* dxp, const int32_t* topk_ids, cons
                                   int H, int E, void* dx, moe_stream_t stream);
 moe_status_t moe_route_backward(const float* logits, const float* expert_bias, const float* dtopk_w, int T, int E,
                                 int k, int renormalize, float* dlogits, moe_stream_t stream);
+moe_status_t moe_route_backward_ids(const float* logits, const float* expert_bias, const int32_t* topk_ids,
+                                    const float* dtopk_w, int T, int E, int k, int renormalize, float* dlogits,
+                                    moe_stream_t stream);
 
 /*
  * moe_layer_norm_forward, moe_layer_norm_backward -- layer norm over the last
