@@ -77,14 +77,14 @@ struct Params {
     int v0, cols;         // the launch's vocabulary rows: [v0, v0 + cols)
     int bv;               // vocabulary rows of a tile (multiple of 16, <= BV)
     int tok_tiles, voc_tiles;
-    int ignore;
+    int ignore, V;
     moe::After after;
     // forward
     float2* part;         // [shares * voc_tiles, T]: maximum and sum of each share of a tile's columns
     int shares;           // 2, or 4 for tiles of 128 tokens
     float* at_label;      // [T]: the label's logit
     const uint4 *x, *W;
-    int V, row_vecs;
+    int row_vecs;
     // backward
     const float* lse;
     const float* g_label;   // [T]: the label's entry of G
@@ -246,7 +246,7 @@ __device__ void epilogue(uint8_t* stages, Shared& S, const Params& p, int total,
         const int col0 = vt * p.bv + shift;                  // first of its columns within the launch's
         const int ncols = min(width, p.cols - col0);         // those that exist
         const int label = row < p.T ? p.labels[row] : p.ignore;
-        const bool counts = label != p.ignore && label >= 0;
+        const bool counts = label != p.ignore && label >= 0 && label < p.V;
         const int rel = counts ? label - p.v0 - col0 : -1;   // the label's column, in the tile if 0 <= rel < ncols
         float neg_lse = 0.0f, g_label = 0.0f;
         if (BACK && row < p.T) {
@@ -735,6 +735,7 @@ extern "C" moe_status_t moe_cross_entropy_backward(const void* x, const void* W,
         p.bv = tile_width(p.cols, T);
         p.voc_tiles = (p.cols + p.bv - 1) / p.bv;
         p.ignore = ignore_index;
+        p.V = V;
         p.lse = lse;
         p.G = G;
         p.ldg = l.ldg;
