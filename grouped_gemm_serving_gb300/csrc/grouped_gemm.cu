@@ -461,6 +461,7 @@ __device__ void producer_swap(const TokenMaps* tmX, const CUtensorMap* tmW, cons
                 if (moe::elect_one()) load_weights(ti, kb, (kb0 + kb) * 64, 2 * (abytes + xbytes));
                 __syncwarp();
             }
+            issued |= (1u << early) - 1;   // in flight from here on (phase 0)
             moe::wait_for_primary();
             waiting = false;
         }

@@ -142,6 +142,7 @@ __device__ void producer(const CUtensorMap* tmX, const CUtensorMap* tmW, uint8_t
                 if (moe::elect_one()) load_w(kb, kb, voc);
                 __syncwarp();
             }
+            issued |= (1u << early) - 1;   // in flight from here on (phase 0)
             moe::wait_for_primary();
             waiting = false;
         }
