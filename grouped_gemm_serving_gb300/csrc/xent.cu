@@ -626,9 +626,9 @@ BackwardLayout backward_layout(int T, int H, int V) {
     int64_t piece = kPieceBytes / 2 / T / BV * BV;
     if (piece < kPieceMin) piece = kPieceMin;
     if (piece > V) piece = V;
-    l.pieces = static_cast<int>((V + piece - 1) / piece);
-    l.piece = l.pieces == 1 ? V : static_cast<int>(((V + l.pieces - 1) / l.pieces + BV - 1) / BV * BV);
-    l.pieces = (V + l.piece - 1) / l.piece;
+    const int64_t pieces = (V + piece - 1) / piece;   // V goes up to INT_MAX - BV: sums with it in 64 bits
+    l.piece = pieces == 1 ? V : static_cast<int>(((V + pieces - 1) / pieces + BV - 1) / BV * BV);
+    l.pieces = (V - 1) / l.piece + 1;
     l.ldg = (l.piece + 63) / 64 * 64;   // rows of whole 128-byte lines
     Carver c;
     l.G = c.take(static_cast<size_t>(T) * l.ldg * 2);

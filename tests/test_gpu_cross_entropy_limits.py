@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests.gpu_helpers import require_gpu
-from tests.train_helpers import gen, randn, workspace
+from tests.train_helpers import EPS, HALF, gen, randn, workspace
 
 pytestmark = pytest.mark.gpu
 IGNORE = -100
@@ -54,3 +54,32 @@ def test_invalid_labels_count_as_ignored_whatever_their_rows_hold(moe, T, at):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1][~out], want[1][~out])
         assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
         assert bool((got[2][out] == 0).all())
+
+
+@pytest.mark.parametrize("T,V", [(1, 2_100_000_000), (3, 2 ** 31 - 257)])
+def test_vocabularies_up_to_the_limit(moe, T, V):
+    """All logits are 0 but those of a few rows; the gradients at the label, those rows and the last one."""
+    H, g = 8, gen(V % 1000)
+    x = torch.ones(T, H, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(V, H, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 5, 2 ** 27 - 1, 2 ** 27, 2_013_265_919, V - 1], device="cuda")
+    W[rows] = randn(g, len(rows), H, std=3.0)
+    labels = rows[[1, 4, 5][:T]].int()
+    (loss, lse, dx, dW), err = _run(moe, x, W, labels, torch.ones(T, device="cuda"))
+    assert err == (0, 0)
+    z = W[rows].double().sum(1)
+    total = V - len(rows) + z.exp().sum()
+    # a thread of the join adds up to 2^17 parts one after the other, each of at most 128 terms
+    tol = 2.0 ** 18 * EPS
+    at = W[labels.long()].double().sum(1)
+    assert bool(((lse.double() - total.log()).abs() <= tol).all())
+    assert bool(((loss.double() - (total.log() - at)).abs() <= tol).all())
+    some = torch.cat([rows, torch.tensor([1, V // 2, V - 2], device="cuda")])
+    p = W[some].double().sum(1).exp() / total
+    G = p[None] - (labels[:, None] == some[None]).double()
+    assert bool(((dW[some].double() - G.sum(0)[:, None]).abs() <= 2 * T * (tol * p + HALF * G.abs().sum(0))[:, None]).all())
+    assert not bool((dW == 7).any())
+    q = z.exp() / total
+    want = (q[:, None] * W[rows].double()).sum(0) - W[labels.long()].double()
+    spread = (q[:, None] * W[rows].double().abs()).sum(0) + W[labels.long()].double().abs()
+    assert bool(((dx.double() - want).abs() <= 2 * (HALF + tol) * spread).all())
