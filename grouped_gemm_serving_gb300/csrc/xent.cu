@@ -350,10 +350,10 @@ __device__ __forceinline__ float label_dot(const uint4* __restrict__ x, const ui
 
 // The labels' logits, a warp a token.
 __device__ void label_logits(const Params& p, int warp) {
-    for (int t = blockIdx.x * 2 + warp; t < p.T; t += gridDim.x * 2) {
+    for (int64_t t = blockIdx.x * 2 + warp; t < p.T; t += gridDim.x * 2) {   // T goes up to INT_MAX - BT
         const int label = p.labels[t];
         if (label == p.ignore || label < 0 || label >= p.V) continue;
-        const float dot = label_dot(p.x + static_cast<int64_t>(t) * p.row_vecs,
+        const float dot = label_dot(p.x + t * p.row_vecs,
                                     p.W + static_cast<int64_t>(label) * p.row_vecs, p.row_vecs);
         if ((threadIdx.x & 31) == 0) p.at_label[t] = dot;
     }
@@ -461,7 +461,7 @@ scale_kernel(const float* __restrict__ dloss, const int32_t* __restrict__ labels
     moe::launch_dependents();
     float top = 0.0f;
     bool bad = false;
-    for (int t = threadIdx.x; t < T; t += 1024) {
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {   // T goes up to INT_MAX - BT
         const int label = labels[t];
         const bool counts = label != ignore && label >= 0 && label < V;
         const float d = counts ? dloss[t] : 0.0f;

@@ -1,5 +1,7 @@
 """moe_cross_entropy_forward / _backward where labels are no labels and where
 sizes come near what 32 bits count."""
+import math
+
 import pytest
 import torch
 
@@ -83,3 +85,28 @@ def test_vocabularies_up_to_the_limit(moe, T, V):
     want = (q[:, None] * W[rows].double()).sum(0) - W[labels.long()].double()
     spread = (q[:, None] * W[rows].double().abs()).sum(0) + W[labels.long()].double().abs()
     assert bool(((dx.double() - want).abs() <= 2 * (HALF + tol) * spread).all())
+
+
+def test_tokens_up_to_the_limit(moe):
+    """2^31 - 257 tokens, nearly all of them zeros without a label (a hundred GB of rows and partial sums)."""
+    T, H, V, g = 2 ** 31 - 257, 8, 2, gen(8)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    W = randn(g, V, H)
+    labels = torch.full((T,), IGNORE, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 1, 2 ** 30 + 3, T - 304, T - 303, T - 1], device="cuda")
+    x[at], labels[at] = randn(g, len(at), H), torch.tensor([0, 1, 1, 0, 1, 0], dtype=torch.int32, device="cuda")
+    loss, lse = torch.full((T,), 7.0, device="cuda"), torch.full((T,), 7.0, device="cuda")
+    n = moe.moe_cross_entropy_forward_workspace_size(T, H, V)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    moe.moe_cross_entropy_forward(x, W, labels, T, H, V, IGNORE, loss, lse, ws, n)
+    assert moe.moe_get_device_error() == 0
+    z = x[at].double() @ W.double().t()
+    zs = (x[at].double().square() @ W.double().square().t()).sqrt().amax(1)
+    want = torch.logsumexp(z, 1)
+    tol = 4 * (H / 16 + 16) * 2.0 ** -23 * zs + 8 * EPS * (1 + want.abs() + z.abs().amax(1))
+    assert bool(((lse[at].double() - want).abs() <= tol).all())
+    assert bool(((loss[at].double() - (want - z.gather(1, labels[at].long()[:, None])[:, 0])).abs() <= 2 * tol).all())
+    loss[at], lse[at] = 0.0, torch.tensor(2.0).log().cuda()
+    assert not bool(loss.any())
+    low, high = torch.aminmax(lse)
+    assert max(abs(low.item() - math.log(2)), abs(high.item() - math.log(2))) <= 16 * EPS
