@@ -37,6 +37,9 @@ int resident_blocks(const void* kernel, int threads, size_t smem, std::atomic<in
 // launch_after() lets the kernel's blocks start once every block of the kernel
 // before it has called launch_dependents() or ended, and wait_for_primary()
 // then waits until that kernel has ended and its stores are visible.
+// Pointers to what the kernel before writes are neither __restrict__ nor read by
+// __ldg(): either lets the compiler take them for read-only as long as the kernel
+// runs, and move their loads in front of the wait.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

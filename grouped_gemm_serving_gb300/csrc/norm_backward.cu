@@ -329,8 +329,7 @@ norm_backward_wide_kernel(const T* dy, int64_t lddy, const T* x, int64_t ldx, in
 constexpr int kShares = 64, kCols = 16;
 template <typename W>
 __global__ void __launch_bounds__(kCols * kShares)
-norm_reduce_kernel(const float* __restrict__ partial, int blocks, int H, W* __restrict__ dweight,
-                   W* __restrict__ dbias) {
+norm_reduce_kernel(const float* partial, int blocks, int H, W* __restrict__ dweight, W* __restrict__ dbias) {
     __shared__ float share[kCols][kShares + 1];
     W* out = blockIdx.y == 0 ? dweight : dbias;
     moe::wait_for_primary();   // this grid may start while the blocks' last stores are under way

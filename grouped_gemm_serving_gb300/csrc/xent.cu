@@ -521,8 +521,7 @@ token_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ W, cons
 
 // dx[t] = scale[t] * (the ranges' sums, in range order), four columns a thread.
 __global__ void __launch_bounds__(256)
-finish_kernel(const float4* __restrict__ sum, int splits, int64_t n, int row_quads, const float* __restrict__ scale,
-              uint2* __restrict__ dx) {
+finish_kernel(const float4* sum, int splits, int64_t n, int row_quads, const float* scale, uint2* dx) {
     moe::wait_for_primary();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= n) return;
