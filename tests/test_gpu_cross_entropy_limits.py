@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+from tests import test_gpu_cross_entropy as base
 from tests.gpu_helpers import require_gpu
 from tests.train_helpers import EPS, HALF, gen, randn, workspace
 
@@ -110,3 +111,44 @@ def test_tokens_up_to_the_limit(moe):
     assert not bool(loss.any())
     low, high = torch.aminmax(lse)
     assert max(abs(low.item() - math.log(2)), abs(high.item() - math.log(2))) <= 16 * EPS
+
+
+def _plan(moe, T, H, V):
+    """(pieces, vocabulary rows of the last one, ranges of dx's contraction) of a backward call, the ranges from
+    what its workspace holds: G of a piece, x in one or two copies, three values a token, a sum for each range."""
+    def up(n, m):
+        return -(-n // m) * m
+
+    piece = min(V, max(2048, 2 ** 27 // T // 256 * 256))
+    n = -(-V // piece)
+    if n > 1:
+        piece = up(-(-V // n), 256)
+    n = -(-V // piece)
+    rest, ld = moe.moe_cross_entropy_backward_workspace_size(T, H, V), up(H, 64)
+    for b in (T * up(piece, 64) * 2, T * ld * 2, 0 if ld == H else T * ld * 2, 4 * T, 4 * (T + 1), 8):
+        rest -= up(b, 256)
+    ranges = rest // (4 * T * H)
+    assert rest == up(4 * ranges * T * H, 256), "the workspace is not laid out as this test reads it"
+    return n, V - (n - 1) * piece, ranges
+
+
+def test_a_last_piece_with_fewer_blocks_than_ranges(moe):
+    """Sizes, looked for on this device, whose dx is cut into several ranges of 64-row blocks while the last
+    piece has one such block: the ranges past it must add nothing."""
+    found = []
+    for piece in range(2048, 9000, 256):
+        V = piece * (piece // 256) + 1
+        for H in (8, 64):
+            for T in range(2 ** 27 // (piece + 256) + 1, 2 ** 27 // piece + 1, 61):
+                n, last, ranges = _plan(moe, T, H, V)
+                if n > 1 and last <= 64 and ranges > 1:
+                    found.append((T * V * H, T, H, V))
+    assert found, "no size reaches the case on this device"
+    for _, T, H, V in sorted(found)[:1] + sorted(found)[-1:]:
+        _, x, W, labels = base._make(T, H, V, 7)
+        _, lse = base._forward(moe, x, W, labels)
+        dloss = torch.ones(T, device="cuda")
+        dx, _ = base._backward(moe, x, W, labels, lse, dloss, want=(True, False))
+        assert moe.moe_get_device_error() == 0
+        rows = torch.cat([torch.arange(0, T, 997), torch.tensor([T - 1])]).cuda()
+        base._check_backward(dx[rows], None, x[rows], W, labels[rows], lse[rows], dloss[rows])
