@@ -611,8 +611,9 @@ ForwardLayout forward_layout(int T, int V) {
     return l;
 }
 
-// A piece's G takes about kPieceBytes, but a piece has at least kPieceMin
-// vocabulary rows: every piece but the last reads and writes dx's fp32 sum.
+// A piece's G takes up to kPieceBytes, but a piece has at least kPieceMin
+// vocabulary rows, whatever G takes then (more than 65536 tokens): every piece
+// but the last reads and writes dx's fp32 sum.
 constexpr int64_t kPieceBytes = 256ll << 20;
 constexpr int kPieceMin = 2048;
 

@@ -489,8 +489,11 @@ moe_status_t moe_layer_norm_backward(moe_dtype_t dtype, const void* dy, int64_t 
  *   G[t, v] = exp(z[t, v] - lse[t]) - [v == labels[t]],
  *   dx[t] = dloss[t] * sum_v G[t, v] W[v],  dW[v] = sum_t G[t, v] dloss[t] x[t],
  *   written (not accumulated).  Either of dx and dW may be NULL and is then
- *   not computed.  The vocabulary is taken in pieces, so that the workspace
- *   stays near 256 MiB plus some copies of x (in bf16 and, summed, in fp32).
+ *   not computed.  The vocabulary is taken in pieces of at least 2048 rows
+ *   (V, if it has fewer), whose G in bf16, [T, rows of a piece], is the largest
+ *   part of the workspace: up to 256 MiB or, for more than 65536 tokens, 4096 T
+ *   bytes.  Beside it are one or two copies of x and, where dx is summed over
+ *   pieces or over ranges of a piece, 1 to 16 fp32 copies of dx.
  * A token whose label is ignore_index (any value, such as -100) has loss 0 and
  * zero gradients, whatever its dloss; its lse is written.  A label outside
  * [0, V) that is not ignore_index is recorded as MOE_DEVERR_LABEL and treated
