@@ -12,7 +12,10 @@
 // without the label's column.  The label's logit z_l comes from a dot product
 // of its own, in fp32 arithmetic that rounds to nearest, by warps that have
 // nothing else to do: the tensor cores' sums, which cut off, are off by some
-// 2e-6 of z_l, which the difference lse - z_l would keep.  A second, small
+// 2e-6 of z_l, which the difference lse - z_l would keep.  (lse has the other
+// logits' share of that: over 1 to 64 tokens and H up to 7168 it is off by 7e-8 in
+// the median and by 7e-6 at most, one token at H = 7032, and loss by 1.5e-5; fp32
+// products: 4e-8 and 8e-7.)  A second, small
 // kernel joins the vocabulary tiles' pairs (m, s) and the label:
 //   M = max m,  S = sum s exp(m - M),  lse = log(S exp M + exp z_l),
 //   loss = log(1 + S exp(M - z_l)),
