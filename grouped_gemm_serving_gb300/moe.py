@@ -85,6 +85,8 @@ _SIGS = {
     "moe_combine": (_S, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_forward_workspace_size": (_Z, [C.POINTER(ForwardArgs)]),
     "moe_forward": (_S, [C.POINTER(ForwardArgs), _P, _Z, _P]),
+    "moe_forward_few_workspace_size": (_Z, [C.POINTER(ForwardArgs)]),
+    "moe_forward_few": (_S, [C.POINTER(ForwardArgs), _P, _Z, _P]),
 }
 
 _lib = None
@@ -339,6 +341,14 @@ def moe_forward_workspace_size(args: ForwardArgs) -> int:
 
 def moe_forward(args: ForwardArgs, ws, ws_bytes, stream=None):
     _check(lib().moe_forward(C.byref(args), _p(ws), ws_bytes, _stream(stream)), "moe_forward")
+
+
+def moe_forward_few_workspace_size(args: ForwardArgs) -> int:
+    return lib().moe_forward_few_workspace_size(C.byref(args))
+
+
+def moe_forward_few(args: ForwardArgs, ws, ws_bytes, stream=None):
+    _check(lib().moe_forward_few(C.byref(args), _p(ws), ws_bytes, _stream(stream)), "moe_forward_few")
 
 
 # ---------------------------------------------------------------- torch helpers

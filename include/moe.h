@@ -638,6 +638,27 @@ size_t moe_forward_workspace_size(const moe_forward_args* args);
 moe_status_t moe_forward(const moe_forward_args* args, void* ws, size_t ws_bytes,
                          moe_stream_t stream);
 
+/*
+ * moe_forward_few -- moe_forward for a few tokens: generating a token at a time
+ * for each sequence of a batch.  Two kernels in all: routing, permutation and
+ * the weighted sum take none of their own, and the weights of the experts that
+ * some token picked are streamed once.  Same arguments and routing as
+ * moe_forward; out[t] = sum over j of topk_w[t, j] * W2[e] h in fp32, in slot
+ * order, rounded to bf16 once, h = silu(g) * u rounded to bf16.
+ * MOE_FP8_E4M3_B128: the weights are e4m3 with block scales as in moe_forward,
+ * but x and h stay bf16 (moe_forward quantises both), so the results lie
+ * closer to the unquantised layer's than moe_forward's do.
+ * Results do not equal moe_forward's bit for bit (it rounds each expert's rows to
+ * bf16 before it sums them).  A token without live slots gets a zero row.  ids
+ * given in topk_ids may name an expert twice for a token.
+ * Limits: those of moe_forward, and (else MOE_ERR_UNSUPPORTED, and a workspace
+ * size of 0) T <= 64, T*k <= 1024, H and I <= 2^20, flags = 0.  Calls that may
+ * run at the same time need a workspace each.
+ */
+size_t moe_forward_few_workspace_size(const moe_forward_args* args);
+moe_status_t moe_forward_few(const moe_forward_args* args, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
