@@ -652,7 +652,7 @@ moe_status_t moe_forward(const moe_forward_args* args, void* ws, size_t ws_bytes
  * bf16 before it sums them).  A token without live slots gets a zero row.  ids
  * given in topk_ids may name an expert twice for a token.
  * Limits: those of moe_forward, and (else MOE_ERR_UNSUPPORTED, and a workspace
- * size of 0) T <= 64, T*k <= 1024, H and I <= 2^20, flags = 0.  Calls that may
+ * size of 0) T <= 64, T*k <= 1024, H and I <= 32768, flags = 0.  Calls that may
  * run at the same time need a workspace each.
  */
 size_t moe_forward_few_workspace_size(const moe_forward_args* args);
