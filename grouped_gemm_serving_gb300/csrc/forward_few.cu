@@ -6,108 +6,157 @@
 // Every weight of an expert that some token picked is read once, which bounds the
 // layer: 2 operations a weight and token against 2 bytes (bf16) or 1 (e4m3).
 //
-// Routing takes no kernel of its own: every block of both kernels routes all
-// tokens itself (they are few) and keeps, per expert, the set of its tokens as a
-// 64-bit mask.  Row r of an expert is its r-th token in ascending order, so the
-// masks' bit counts are the offsets, the permutation and its inverse.
+// The first kernel, one block, routes: per expert the set of its tokens as a 64-bit
+// mask, whose bit counts are the offsets, the permutation and its inverse (row r of
+// an expert is its r-th token in ascending order).  It writes the list of chunks,
+// up to 8 or 16 rows of an expert each, the rows' tokens and the slots' rows.
 //
-// A block's unit is 16 weight rows (8 features' gate and up rows, or 16 output
-// features) of one expert against up to 32 of its rows of x; the units lie in
-// expert order and every block takes a run of them.  A producer warp brings the
-// weights 512 columns at a time into a ring in shared memory by TMA tiles of 128
-// bytes by 16 rows, so that the loads in flight do not depend on what the other
-// warps do.  Eight warps take 64 of the columns each (m16n8k16 MMAs; the order of
-// the contraction's elements within a step is the lanes' own, the same for both
-// operands), with their columns of the expert's rows of x in shared memory for as
-// long as the expert lasts.  Two more warps take turns at adding the eight partial
-// sums in warp order and finishing a unit while the others go on to the next.
+// The second, a cooperative launch of a block per SM, streams the weights of both
+// products.  A unit is 16 weight rows (8 features' gate and up rows, or 16 output
+// features) against a chunk; the units lie in expert order and every block takes a
+// run of them, first of the one product, then of the other.  A producer warp brings
+// the weights 16 KB at a time (1 KB of each row) into a ring in shared memory by TMA,
+// as eight tiles of 128 bytes by 16 rows, without regard to what the others do: when
+// the first product ends the ring is full of the second's weights.  Sixteen warps
+// multiply, a tile of every other stage each (m16n8k16 MMAs; the order of the
+// contraction's elements within a step is the lanes' own, the same for both
+// operands), with their columns of the chunk's rows of x in shared memory for as
+// long as the chunk lasts.  Two more take turns at adding the sixteen partial sums in
+// warp order and finishing a unit while the others go on to the next.  Between the
+// products all blocks wait for each other, as each needs rows of h from many.
 //
-// FP8 weights are converted to bf16 on the way (exact) and the partial sum of a
-// warp's 64 columns is multiplied by their block's scale in fp32.  x and h stay
-// bf16: quantising them would save no weight bytes, and cost accuracy.
+// FP8 weights are converted to fp16 on the way, one instruction for two of them
+// (exact), and meet x in fp16, scaled by a power of two; the partial sum of a tile's
+// 128 columns is multiplied by their block's scale in fp32.  x and h are not
+// quantised: it would save no weight bytes, and cost accuracy.
 //
-// The first kernel writes h, rounded to bf16 (the type of the MMA's operand).  The
-// second one is launched programmatically, beside the first if their shared memory
-// allows it, and has its ring full of weights when it waits for h.  It writes fp32
-// rows y; the block that brings the last of a 16-feature column's units sums each
-// token's rows in slot order and rounds once.
+// h is rounded to bf16, the type of the MMA's operand.  The second product leaves
+// fp32 rows y; the block that brings the last of a 16-feature column's units sums
+// each token's rows in slot order and rounds once.
 #include <cuda_fp8.h>
+
+#include <climits>
 
 #include "common.cuh"
 #include "internal.h"
-#include "route.cuh"
 
 namespace {
 
-constexpr int kProduct = 8;                     // warps that multiply
+constexpr int kTiles = 8;                       // of a stage
+constexpr int kProduct = 2 * kTiles;            // warps that multiply
 constexpr int kThreads = 32 * (kProduct + 3);   // two that finish units, and the producer
 constexpr int kRows = 16;                       // weight rows of a unit
-constexpr int kColumns = 512;                   // columns of a stage
-constexpr int kRowBytes = 128;                  // of a tile's row: 64 columns in bf16, 128 in e4m3
+constexpr int kRowBytes = 128;                  // of a tile's row
 constexpr int kTileBytes = kRows * kRowBytes;
+constexpr int kStageBytes = kTiles * kTileBytes;
 template <bool FP8>
-constexpr int kTiles = kColumns * (FP8 ? 1 : 2) / kRowBytes;   // of a stage
-constexpr int kMaxStages = 16;
+constexpr int kTileColumns = kRowBytes / (FP8 ? 1 : 2);
+template <bool FP8>
+constexpr int kColumns = kTiles * kTileColumns<FP8>;   // of a stage
+constexpr int kMaxStages = 12;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMaxT = 64;                       // tokens: the bits of a mask
 constexpr int kMaxSlots = 1024;
 constexpr int kMaxE = 256;
-constexpr int kMaxK = 32768;                     // columns of a product: a row of x takes 2 bytes each of a block
+constexpr int kMaxK = 32768;                    // columns of a product: a row of x takes 2 bytes each of a block
+constexpr int kRouteThreads = 1024;
 
-struct Args {
-    // routing
+// What the first kernel leaves for the second, in the workspace.
+struct Plan {
+    int chunks;
+    unsigned done;                // blocks' finishing warps that have written their last h
+    int pad[2];
+    int4 chunk[kMaxSlots];        // expert, first row, rows
+    float slot_w[kMaxSlots];
+    short slot_row[kMaxSlots];    // -1: a sentinel
+    uint8_t token[kMaxSlots];     // a row's token
+};
+
+struct Route {
     const float* logits;
     const float* bias;
     const uint8_t* mask;
     int32_t* ids;
     float* w;
     int T, E, k, renormalize;
-    // product
-    const uint4* x;           // GATED: x [T, K], else h [T*k, K]
-    const float* scales;      // FP8: a scale per 128 x 128 block of W
-    int K, F;                 // columns and features of W: [E, 2F, K] (GATED) or [E, F, K]
-    int xrows, stages;        // the most rows of a unit; depth of the ring
-    __nv_bfloat16* h;         // GATED: [T*k, F] out
-    float* part;              // else: y [ceil(F/16), T*k, 16], then summed into
-    __nv_bfloat16* out;       // [T, F]
-    int* arrived;             // per 16 output features: units done (zeroed by the first kernel)
-    int columns;              // their number
+    int chunk_rows;
+    Plan* plan;
+    int* arrived;
+    int columns;
     int* err;
 };
 
-// What a block knows of the routing.
-struct Plan {
-    uint32_t tokens[kMaxE][2];          // the expert's tokens
-    int base[kMaxE];                    // its first row
-    short chunk_expert[kMaxSlots];     // up to a.xrows rows of an expert each
-    short chunk_row[kMaxSlots];        // the first of them, counted from the expert's
-    uint8_t token[kMaxSlots];           // a row's token
-    short slot_id[kMaxSlots];
-    float slot_w[kMaxSlots];
-    int chunks;
-};
-
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// A token's k picks on one warp, moe_route_sort's bit for bit: the largest of
+// logits[e] + bias[e], e < E, ties to the lower id.  Lane j < k returns the id of the j-th and
+// its weight in w; a NaN is never picked, and a pick that too many of them left
+// unfilled is INT_MAX.  row: E words of the warp's own.  Every lane keeps the best
+// of its own experts; where one is taken all lanes look for the next among that
+// lane's.  Small loops on purpose: all this runs once, and instructions that come from L2 for
+// one use cost more than they do.
+__device__ __forceinline__ int picks(const float* logits, const float* bias, float* row, int E, int k, int renormalize, float& w) {
+    const int lane = threadIdx.x & 31;
+    uint32_t best = 0;
+    int id = INT_MAX;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) {
+        const float v = bias ? logits[e] + bias[e] : logits[e];
+        row[e] = v;
+        const uint32_t key = moe::order_key(v);
+        if (key > best) {
+            best = key;
+            id = e;
+        }
+    }
+    const uint32_t first = __reduce_max_sync(0xffffffffu, best);
+    const float top = first ? moe::key_value(first) : -INFINITY;
+    float part = 0.0f;
+    if (!renormalize)
+#pragma unroll 1
+        for (int e = lane; e < E; e += 32) part += expf(row[e] - top);
+    int my_id = INT_MAX;
+    float my_v = -INFINITY;
+#pragma unroll 1
+    for (int r = 0; r < k; ++r) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        if (m == 0) break;
+        const int e = __reduce_min_sync(0xffffffffu, best == m ? id : INT_MAX);
+        if (lane == r) {
+            my_v = moe::key_value(m);
+            my_id = e;
+        }
+        if (lane == (e & 31)) row[e] = NAN;   // taken
+        __syncwarp();
+        const int other = (e & 31) + 32 * lane;
+        const uint32_t key = other < E ? moe::order_key(row[other]) : 0u;
+        const uint32_t next = __reduce_max_sync(0xffffffffu, key);
+        const int at = __reduce_min_sync(0xffffffffu, key == next ? other : INT_MAX);
+        if (lane == (e & 31)) {
+            best = next;
+            id = at;
+        }
+    }
+    if (renormalize) part = lane < k ? expf(my_v - top) : 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+    w = expf(my_v - top) / part;
+    return my_id;
 }
 
-// Two e4m3 values as two bf16: through fp16 and fp32, both exact, and a bf16's
-// 8 significant bits hold an e4m3's 4, so cutting fp32 in half is exact too.
-__device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-    const float2 f = __half22float2(__half2(h));
-    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-}
-
-// Routes all tokens.  The first block of the first kernel (`record`) also writes
-// the picks and weights out and reports invalid ones.
-__device__ void make_plan(const Args& a, Plan& P, bool record) {
+// One block routes all tokens, a warp each at a time, and zeroes the counters of the
+// second kernel.
+__global__ void __launch_bounds__(kRouteThreads)
+few_route_kernel(const Route a) {
+    __shared__ uint32_t tokens[kMaxE][2];   // the expert's tokens
+    __shared__ int base[kMaxE];             // its first row
+    __shared__ short slot_id[kMaxSlots];
+    __shared__ float rows[kRouteThreads / 32][kMaxE];
+    __shared__ int sums[kMaxE / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < 2 * a.E; i += kThreads) (&P.tokens[0][0])[i] = 0;
+    if (tid < 2 * kMaxE) (&tokens[0][0])[tid] = 0;
+    moe::wait_for_primary();   // what wrote the logits or ids
+#pragma unroll 1
+    for (int i = tid; i < a.columns; i += kRouteThreads) a.arrived[i] = 0;
+    if (tid == 0) a.plan->done = 0;
     __syncthreads();
     const auto take = [&](int t, int s, int id, bool changed) {
         if (a.mask && a.mask[s]) {
@@ -115,84 +164,137 @@ __device__ void make_plan(const Args& a, Plan& P, bool record) {
             id = a.E;
         }
         if (id < 0 || id > a.E) {
-            if (record) moe::raise_device_error(a.err, MOE_DEVERR_ROUTE);
+            moe::raise_device_error(a.err, MOE_DEVERR_ROUTE);
             changed = true;
             id = a.E;
         }
-        if (record && changed && a.ids) a.ids[s] = id;
-        P.slot_id[s] = static_cast<short>(id);
-        if (id < a.E) atomicOr(&P.tokens[id][t >> 5], 1u << (t & 31));
+        if (changed && a.ids) a.ids[s] = id;
+        slot_id[s] = static_cast<short>(id);
+        if (id < a.E) atomicOr(&tokens[id][t >> 5], 1u << (t & 31));
     };
     if (a.logits) {
-        for (int t = warp; t < a.T; t += kProduct + 3) {
-            const float* row = a.logits + static_cast<int64_t>(t) * a.E;
+#pragma unroll 1
+        for (int t = warp; t < a.T; t += kRouteThreads / 32) {
             float w;
-            int id;
-            if (a.E <= 32) id = moe::top_picks<1>(row, a.bias, a.E, a.k, a.renormalize, w);
-            else if (a.E <= 64) id = moe::top_picks<2>(row, a.bias, a.E, a.k, a.renormalize, w);
-            else if (a.E <= 128) id = moe::top_picks<4>(row, a.bias, a.E, a.k, a.renormalize, w);
-            else id = moe::top_picks<8>(row, a.bias, a.E, a.k, a.renormalize, w);
+            const int id = picks(a.logits + static_cast<int64_t>(t) * a.E, a.bias, rows[warp], a.E, a.k, a.renormalize, w);
             if (lane < a.k) {
                 const int s = t * a.k + lane;
-                P.slot_w[s] = w;
-                if (record && a.w) a.w[s] = w;
+                a.plan->slot_w[s] = w;
+                if (a.w) a.w[s] = w;
                 take(t, s, id, true);
             }
         }
     } else {
-        for (int s = tid; s < a.T * a.k; s += kThreads) {
-            P.slot_w[s] = a.w[s];
+        for (int s = tid; s < a.T * a.k; s += kRouteThreads) {
+            a.plan->slot_w[s] = a.w[s];
             take(s / a.k, s, a.ids[s], false);
         }
     }
     __syncthreads();
-    if (warp == 0) {
-        int rows = 0, chunks = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int n = e < a.E ? __popc(P.tokens[e][0]) + __popc(P.tokens[e][1]) : 0;
-            const int c = (n + a.xrows - 1) / a.xrows;
-            int at = n, first = c;   // inclusive sums over the lanes
+    // thread e: rows (low half) and chunks (high half) of the experts up to e
+    int n = 0, c = 0, upto = 0;
+    if (tid < kMaxE) {
+        n = __popc(tokens[tid][0]) + __popc(tokens[tid][1]);
+        c = n > a.chunk_rows ? (n + a.chunk_rows - 1) / a.chunk_rows : (n > 0);
+        upto = n | c << 16;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int p = __shfl_up_sync(0xffffffffu, at, off), q = __shfl_up_sync(0xffffffffu, first, off);
-                if (lane >= off) {
-                    at += p;
-                    first += q;
-                }
-            }
-            if (n) {
-                P.base[e] = rows + at - n;
-                for (int i = 0; i < c; ++i) {
-                    P.chunk_expert[chunks + first - c + i] = static_cast<short>(e);
-                    P.chunk_row[chunks + first - c + i] = static_cast<short>(i * a.xrows);
-                }
-            }
-            rows += __shfl_sync(0xffffffffu, at, 31);
-            chunks += __shfl_sync(0xffffffffu, first, 31);
+        for (int off = 1; off < 32; off <<= 1) {
+            const int below = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += below;
         }
-        if (lane == 0) P.chunks = chunks;
+        if (lane == 31) sums[warp] = upto;
     }
     __syncthreads();
-    for (int e = tid; e < a.E; e += kThreads) {
-        uint64_t left = P.tokens[e][0] | static_cast<uint64_t>(P.tokens[e][1]) << 32;
-        if (left == 0) continue;   // base is not set
-        for (int r = P.base[e]; left; ++r, left &= left - 1) P.token[r] = static_cast<uint8_t>(__ffsll(left) - 1);
+    if (tid < kMaxE) {
+#pragma unroll 1
+        for (int i = 0; i < warp; ++i) upto += sums[i];
+        if (tid == kMaxE - 1) a.plan->chunks = upto >> 16;
+        if (n) {
+            const int row = (upto & 0xFFFF) - n, first = (upto >> 16) - c;
+            base[tid] = row;
+#pragma unroll 1
+            for (int i = 0; i < c; ++i)
+                a.plan->chunk[first + i] = make_int4(tid, row + i * a.chunk_rows, min(a.chunk_rows, n - i * a.chunk_rows), 0);
+        }
     }
     __syncthreads();
+    for (int s = tid; s < a.T * a.k; s += kRouteThreads) {
+        const int id = slot_id[s], t = s / a.k;
+        int row = -1;
+        if (id < a.E) {   // the row of token t among the expert's
+            const uint32_t below = (1u << (t & 31)) - 1;
+            row = base[id] + (t < 32 ? __popc(tokens[id][0] & below) : __popc(tokens[id][0]) + __popc(tokens[id][1] & below));
+            a.plan->token[row] = static_cast<uint8_t>(t);   // slots of the same expert and token write the same
+        }
+        a.plan->slot_row[s] = static_cast<short>(row);
+    }
 }
 
-__device__ __forceinline__ int rows_of(const Plan& P, int e) { return __popc(P.tokens[e][0]) + __popc(P.tokens[e][1]); }
-
-// The row of token t among the rows of expert e, which it picked.
-__device__ __forceinline__ int row_of(const Plan& P, int e, int t) {
-    const uint32_t below = (1u << (t & 31)) - 1;
-    return P.base[e] + (t < 32 ? __popc(P.tokens[e][0] & below) : __popc(P.tokens[e][0]) + __popc(P.tokens[e][1] & below));
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+// Four e4m3 values as two pairs of fp16 (exact).
+__device__ __forceinline__ void f16x2_of_e4m3x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+
+// FP8's scaling of x: the exponent that takes the largest magnitude (bits of a
+// bf16) to [2^14, 2^15), within what a float's exponent holds; 0 for zero and for
+// what is not finite.
+__device__ __forceinline__ int scale_exponent(int bits) {
+    const int e = bits >> 7;
+    return e == 255 || bits == 0 ? 0 : min(141 - max(e, 1), 126);
+}
+__device__ __forceinline__ uint32_t scaled_f16x2(uint32_t two, float f) {
+    const __half2 h = __floats2half2_rn(moe::bf16_lo(two) * f, moe::bf16_hi(two) * f);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The weights' tiles: `whole` copies kTiles of them at once, [tile][row][128 bytes] in
+// shared memory; `rest` one tile of the columns that fill none, zeros behind them (a
+// stage of its own: a copy of whole tiles writes zeros where a tile is missing).
+struct Maps {
+    CUtensorMap whole, rest;
+};
+
+// One of the two products, y = W x, for all experts.
+struct Product {
+    const __nv_bfloat16* x;   // [rows, K]: x [T, K], or h [T*k, K]
+    const float* scales;      // FP8: a scale per 128 x 128 block of W
+    int K, F;                 // columns and features of W: [E, 2F, K] (first) or [E, F, K]
+    int whole;                // columns in whole tiles
+    int whole_steps, steps;   // stages of a unit: of those, and in all, an even number (the last may be empty)
+};
+
+struct Args {
+    Product p[2];
+    Plan* plan;
+    __nv_bfloat16* h;         // [T*k, F of the first]
+    float* part;              // y [ceil(F / 16), T*k, 16], F of the second, then summed into
+    __nv_bfloat16* out;       // [T, F of the second]
+    int* arrived;             // per 16 output features: units done
+    int T, E, k;
+    int xrows, stages;        // the most rows of a chunk; depth of the ring
+    int* err;
+};
 
 // Named barriers between the warps that multiply and those that finish, two of
-// each kind for the two buffers of partial sums.
-constexpr int kFull = 1, kEmpty = 3, kBarThreads = 32 * (kProduct + 1);
+// each kind for the two buffers of partial sums, and one for the second product.
+constexpr int kFull = 1, kEmpty = 3, kReady = 5, kBarThreads = 32 * (kProduct + 1);
 __device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kBarThreads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBarThreads) : "memory"); }
 
@@ -201,89 +303,294 @@ struct Ring {
     int abort_flag;
 };
 
-// Where a unit is: rows p to p + rows - 1 of expert e, and its first feature.
-struct Unit {
-    int chunk, e, f0, p, rows;
-};
-template <bool GATED>
-__device__ __forceinline__ Unit unit_at(const Args& a, const Plan& P, int unit, int per) {
-    Unit u;
-    u.chunk = unit / per;
-    u.f0 = (unit - u.chunk * per) * (GATED ? kRows / 2 : kRows);
-    u.e = P.chunk_expert[u.chunk];
-    u.p = P.base[u.e] + P.chunk_row[u.chunk];
-    u.rows = min(a.xrows, rows_of(P, u.e) - P.chunk_row[u.chunk]);
-    return u;
+// What the plan says, within bounds whatever it says: calls that share a workspace
+// by mistake get wrong results, not wrong addresses.
+__device__ __forceinline__ int chunks_of(const Args& a) { return max(0, min(a.plan->chunks, a.T * a.k)); }
+__device__ __forceinline__ int4 chunk_of(const Args& a, int i) {   // expert, first row, rows
+    int4 c = __ldcg(&a.plan->chunk[i]);
+    c.x = max(0, min(c.x, a.E - 1));
+    c.z = max(1, min(c.z, a.xrows));
+    c.y = max(0, min(c.y, a.T * a.k - c.z));
+    return c;
 }
 
-// A warp's 64 columns of a stage.  Tiles are swizzled: vector j of row r is at
-// j ^ (r mod 8).  bf16: the tile's 8 vectors, lane l taking 2 (l mod 4) and the one
-// after it of rows l / 4 and l / 4 + 8: the 8 lanes that are served together find
-// theirs in different banks.  e4m3: two warps share a tile, one with the even
-// vectors, one with the odd.  x: [row][8 vectors], swizzled alike; rows past the
-// last one read the last (their sums are not used).
-template <int NB>
-__device__ __forceinline__ void multiply(const uint8_t* tile, const uint8_t* xs, int rows, float (&d)[NB][4]) {
-    const int g = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = ((2 * c + i) ^ g) * 16;
-        const uint4 r0 = *reinterpret_cast<const uint4*>(tile + g * kRowBytes + at);
-        const uint4 r1 = *reinterpret_cast<const uint4*>(tile + (g + 8) * kRowBytes + at);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int r = min(8 * b + g, rows - 1);
-            const uint4 xv = *reinterpret_cast<const uint4*>(xs + r * kRowBytes + ((2 * c + i) ^ (r & 7)) * 16);
-            mma(d[b], r0.x, r1.x, r0.y, r1.y, xv.x, xv.y);
-            mma(d[b], r0.z, r1.z, r0.w, r1.w, xv.z, xv.w);
+// A block's run of units, in order.
+template <bool FIRST>
+struct Run {
+    static constexpr int kFeatures = FIRST ? kRows / 2 : kRows;
+    int chunk, f, per, left;   // feature block f of `per`
+    __device__ __forceinline__ Run(int chunks, int F) {
+        per = (F + kFeatures - 1) / kFeatures;
+        const int64_t units = static_cast<int64_t>(chunks) * per;
+        const int64_t begin = units * blockIdx.x / gridDim.x;
+        left = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - begin);
+        chunk = static_cast<int>(begin / per);
+        f = static_cast<int>(begin - static_cast<int64_t>(chunk) * per);
+    }
+    __device__ __forceinline__ int f0() const { return f * kFeatures; }
+    __device__ __forceinline__ void next() {
+        --left;
+        if (++f == per) {
+            f = 0;
+            ++chunk;
+        }
+    }
+};
+
+template <bool FP8, bool FIRST>
+__device__ __forceinline__ void produce(const Maps& maps, const Product& p, const Args& a, Ring& S, uint32_t ring, int& slot,
+                                        uint32_t& turn, int64_t& filled, bool& gave_up) {
+    const int chunks = chunks_of(a);
+    int at = -1, e = 0;
+    for (Run<FIRST> u(chunks, p.F); u.left > 0 && !gave_up; u.next()) {
+        if (u.chunk != at) {
+            at = u.chunk;
+            e = chunk_of(a, at).x;
+        }
+        const int f0 = u.f0();
+        for (int step = 0; step < p.steps; ++step, ++filled) {
+            if (filled >= a.stages && !moe::mbar_wait(moe::smem_u32(&S.empty[slot]), turn ^ 1u, &S.abort_flag, kWaitNs)) {
+                gave_up = true;
+                break;
+            }
+            const uint32_t bar = moe::smem_u32(&S.full[slot]), dst = ring + slot * kStageBytes;
+            if (moe::elect_one()) {
+                if (step < p.whole_steps) {   // tiles past the last one come as zeros
+                    moe::mbar_arrive_expect_tx(bar, kStageBytes);
+                    if (FIRST) moe::tma_load_5d(dst, &maps.whole, bar, 0, f0, 0, step * kTiles, e);
+                    else moe::tma_load_4d(dst, &maps.whole, bar, 0, f0, step * kTiles, e);
+                } else if (step > p.whole_steps || p.whole == p.K) {
+                    moe::mbar_arrive(bar);
+                } else {
+                    moe::mbar_arrive_expect_tx(bar, kTileBytes);
+                    if (FIRST) moe::tma_load_4d(dst, &maps.rest, bar, p.whole, f0, 0, e);
+                    else moe::tma_load_3d(dst, &maps.rest, bar, p.whole, f0, e);
+                }
+            }
+            __syncwarp();
+            if (++slot == a.stages) {
+                slot = 0;
+                turn ^= 1u;
+            }
         }
     }
 }
+
+// Shared memory behind the ring: two buffers of partial sums, and every product
+// warp's columns of x.
 template <int NB>
-__device__ __forceinline__ void multiply_fp8(const uint8_t* tile, int odd, const uint8_t* xs, int rows, float s0, float s1,
-                                             float (&d)[NB][4]) {
-    const int g = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
-    const int at = ((2 * c + odd) ^ g) * 16;
-    const uint4 q0 = *reinterpret_cast<const uint4*>(tile + g * kRowBytes + at);
-    const uint4 q1 = *reinterpret_cast<const uint4*>(tile + (g + 8) * kRowBytes + at);
-    const uint32_t a0[4] = {q0.x, q0.y, q0.z, q0.w}, a1[4] = {q1.x, q1.y, q1.z, q1.w};
-    float t[NB][4];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[b][i] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint4 xv[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int r = min(8 * b + g, rows - 1);
-            xv[b] = *reinterpret_cast<const uint4*>(xs + r * kRowBytes + ((2 * c + i) ^ (r & 7)) * 16);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t m0 = bf16x2_of_e4m3x2(a0[2 * i + j] & 0xFFFF), m2 = bf16x2_of_e4m3x2(a0[2 * i + j] >> 16);
-            const uint32_t m1 = bf16x2_of_e4m3x2(a1[2 * i + j] & 0xFFFF), m3 = bf16x2_of_e4m3x2(a1[2 * i + j] >> 16);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) mma(t[b], m0, m1, m2, m3, j ? xv[b].z : xv[b].x, j ? xv[b].w : xv[b].y);
+using Sums = float4[NB][kProduct][32];   // group of 8 rows, warp, lane
+
+// Where a product warp is in the ring.
+struct Place {
+    int stage, slot;   // the stage's number, and its slot
+    uint32_t phase;
+    __device__ __forceinline__ void go_to(int to, int stages) {
+        slot += to - stage;
+        stage = to;
+        while (slot >= stages) {
+            slot -= stages;
+            phase ^= 1u;
         }
     }
+};
+
+// One product on one of its warps: tile `warp mod 8` of every other stage.  Units have
+// an even number of stages and so has the ring, so that a slot is always the same
+// warps' turn: a wait for a phase's parity tells only neighbouring phases apart, and
+// would run ahead of phases that were others' to take.  `first`: the number of the
+// product's first stage; `count`: units before, whose partial sums took the buffers
+// in turn.
+template <bool FP8, bool FIRST, int NBMAX>
+__device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& S, const uint8_t* ring, Sums<NBMAX>* red, uint8_t* xcols,
+                                         float (&unscale)[kProduct][8 * NBMAX], Place& place, int first, int& count) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = warp % kTiles, half = warp / kTiles;
+    const int g = lane >> 2, c = lane & 3;
+    constexpr int kXRow = FP8 ? 2 * kRowBytes : kRowBytes;   // of a tile's columns of a row of x
+    constexpr int kVectors = kXRow / 16;
+    const int mine = p.steps / 2;                             // this warp's steps of a unit
+    uint8_t* const xs = xcols + static_cast<size_t>(warp) * mine * a.xrows * kXRow;
+    // Tiles are swizzled: vector j of row r is at j ^ (r mod 8).  Lane l takes vectors
+    // 2 (l mod 4) and the one after it of rows l / 4 and l / 4 + 8: the 8 lanes that are
+    // served together find theirs in different banks.
+    const int w_at = tile * kTileBytes + g * kRowBytes + ((2 * c) ^ g) * 16;
+    const int blocks_k = p.K / 128;   // FP8: scales of a row, one a tile
+    const int64_t blocks_n = ((FIRST ? 2 : 1) * static_cast<int64_t>(p.F) + 127) / 128;
+    int held = -1, rows = 0, row0 = 0, e = 0;
+    int x_at[NBMAX];
+    float s0 = 0.0f, s1 = 0.0f;
+    // lane i's scales of this warp's step i (at most 16), for rows of the first and of the second 8
+    const auto scales_of = [&](int f0) {
+        const int k = (2 * lane + half) * kTiles + tile;
+        if (k < blocks_k) {
+            const float* row = p.scales + e * blocks_n * blocks_k + k;
+            s0 = __ldg(row + static_cast<int64_t>(f0 / 128) * blocks_k);
+            s1 = FIRST ? __ldg(row + static_cast<int64_t>((p.F + f0) / 128) * blocks_k) : s0;
+        }
+    };
+    // This warp's columns of the chunk's rows of x: [step][row][half][8 vectors], swizzled
+    // like the tiles; an FP8 vector of weights meets two of x, the halves.  FP8: scaled
+    // by a power of two per row to at most 2^15 and held in fp16, which loses nothing of
+    // a bf16 within 2^29 of the largest, and of the others less than 2^-39 of that; a
+    // row with infinities or NaN is not scaled.  A few rows, two vectors each, on their
+    // way at a time; FP8 looks at them once for the scale and once to convert them.
+    const auto take_x = [&]() {
+        constexpr int NR = NBMAX == 1 ? 2 : 4, NV = 2;
+        const int vectors = mine * kVectors;
+        __syncwarp();
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += NR) {
+            const uint4* from[NR];
+            int bits[NR];   // the largest magnitude, in bf16
+            float f[NR];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        d[b][0] = fmaf(s0, t[b][0], d[b][0]);
-        d[b][1] = fmaf(s0, t[b][1], d[b][1]);
-        d[b][2] = fmaf(s1, t[b][2], d[b][2]);
-        d[b][3] = fmaf(s1, t[b][3], d[b][3]);
+            for (int j = 0; j < NR; ++j) {
+                const int r = row0 + min(r0 + j, rows - 1);
+                from[j] = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(FIRST ? min(a.plan->token[r], a.T - 1) : r) * p.K);
+                bits[j] = 0;
+            }
+#pragma unroll 1
+            for (int look = FP8 ? 0 : 1; look < 2; ++look) {
+                if (FP8 && look == 1)
+#pragma unroll
+                    for (int j = 0; j < NR; ++j) {
+                        const int x = scale_exponent(__reduce_max_sync(0xffffffffu, bits[j]));
+                        f[j] = moe::exp2_int(x);
+                        if (lane == 0 && r0 + j < rows) unscale[warp][r0 + j] = moe::exp2_int(-x);
+                    }
+#pragma unroll 1
+                for (int i0 = lane; i0 < vectors; i0 += 32 * NV) {
+                    uint4 v[NR][NV];
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int at = i0 + 32 * i, step = 2 * (at / kVectors) + half;
+                        const int k = (step < p.whole_steps ? step * kColumns<FP8> : p.whole) + tile * kTileColumns<FP8> + 8 * (at % kVectors);
+                        const bool in = at < vectors && k < (step < p.whole_steps ? p.whole : p.K);
+#pragma unroll
+                        for (int j = 0; j < NR; ++j) v[j][i] = in ? __ldcg(from[j] + k / 8) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int at = i0 + 32 * i, q = at % kVectors;
+#pragma unroll
+                        for (int j = 0; j < NR; ++j) {
+                            const int r = r0 + j;
+                            uint4 t = v[j][i];
+                            if (look == 0) {
+                                const uint32_t m = __vmaxu2(__vmaxu2(t.x & 0x7FFF7FFFu, t.y & 0x7FFF7FFFu), __vmaxu2(t.z & 0x7FFF7FFFu, t.w & 0x7FFF7FFFu));
+                                bits[j] = max(bits[j], static_cast<int>(max(m & 0xFFFFu, m >> 16)));
+                            } else if (at < vectors && r < rows) {
+                                if (FP8) t = make_uint4(scaled_f16x2(t.x, f[j]), scaled_f16x2(t.y, f[j]), scaled_f16x2(t.z, f[j]), scaled_f16x2(t.w, f[j]));
+                                const int to = FP8 ? (q & 1) * kRowBytes + ((q / 2) ^ (r & 7)) * 16 : (q ^ (r & 7)) * 16;
+                                *reinterpret_cast<uint4*>(xs + ((at / kVectors) * a.xrows + r) * kXRow + to) = t;
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    };
+    int stage = first;
+    for (Run<FIRST> u(chunks_of(a), p.F); u.left > 0; u.next(), stage += p.steps, ++count) {
+        if (u.chunk != held) {
+            held = u.chunk;
+            const int4 chunk = chunk_of(a, held);
+            e = chunk.x;
+            row0 = chunk.y;
+            rows = chunk.z;
+            if (FP8) scales_of(u.f0());
+            take_x();
+#pragma unroll
+            for (int b = 0; b < NBMAX; ++b) {   // rows past the last one read the last: their sums are not used
+                const int r = min(8 * b + g, rows - 1);
+                x_at[b] = r * kXRow + ((2 * c) ^ (r & 7)) * 16;
+            }
+        } else if (FP8 && u.f0() % 128 == 0) {   // the next block of 128 weight rows
+            scales_of(u.f0());
+        }
+        const auto unit = [&](auto nb) {
+            constexpr int NB = decltype(nb)::value;
+            float d[NB][4];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[b][i] = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < mine; ++i) {
+                const int step = 2 * i + half;
+                place.go_to(stage + step, a.stages);
+                if (!moe::mbar_wait(moe::smem_u32(&S.full[place.slot]), place.phase, &S.abort_flag, kWaitNs)) {
+                    if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
+                    S.abort_flag = 1;   // what follows is not waited for as long
+                }
+                uint4 w[2][2];   // vector, row
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint8_t* at = ring + place.slot * kStageBytes + (w_at ^ 16 * j);
+                    w[j][0] = *reinterpret_cast<const uint4*>(at);
+                    w[j][1] = *reinterpret_cast<const uint4*>(at + 8 * kRowBytes);
+                }
+                __syncwarp();
+                if (lane == 0) moe::mbar_arrive(moe::smem_u32(&S.empty[place.slot]));
+                if (step < p.whole_steps ? step * kColumns<FP8> + tile * kTileColumns<FP8> >= p.whole : step > p.whole_steps || tile > 0 || p.whole == p.K) continue;
+                const uint8_t* x = xs + i * a.xrows * kXRow;
+                float t[NB][4];
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) t[b][j] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t top[4] = {w[j][0].x, w[j][0].y, w[j][0].z, w[j][0].w}, bottom[4] = {w[j][1].x, w[j][1].y, w[j][1].z, w[j][1].w};
+#pragma unroll
+                    for (int q = 0; q < (FP8 ? 2 : 1); ++q) {
+                        uint4 v[NB];
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) v[b] = *reinterpret_cast<const uint4*>(x + (x_at[b] ^ 16 * j) + q * kRowBytes);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            uint32_t a0, a1, a2, a3;
+                            if (FP8) {
+                                f16x2_of_e4m3x4(top[2 * q + m], a0, a2);
+                                f16x2_of_e4m3x4(bottom[2 * q + m], a1, a3);
+                            } else {
+                                a0 = top[2 * m], a2 = top[2 * m + 1], a1 = bottom[2 * m], a3 = bottom[2 * m + 1];
+                            }
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) mma<FP8>(FP8 ? t[b] : d[b], a0, a1, a2, a3, m ? v[b].z : v[b].x, m ? v[b].w : v[b].y);
+                        }
+                    }
+                }
+                if (FP8) {
+                    const float f0 = __shfl_sync(0xffffffffu, s0, i), f1 = __shfl_sync(0xffffffffu, s1, i);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) d[b][j] = fmaf(j < 2 ? f0 : f1, t[b][j], d[b][j]);
+                }
+            }
+            const int turn = count & 1;
+            if (count >= 2) bar_sync(kEmpty + turn);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float f0 = FP8 ? unscale[warp][8 * b + 2 * c] : 1.0f, f1 = FP8 ? unscale[warp][8 * b + 2 * c + 1] : 1.0f;
+                red[turn][b][warp][lane] = make_float4(d[b][0] * f0, d[b][1] * f1, d[b][2] * f0, d[b][3] * f1);
+            }
+            bar_arrive(kFull + turn);
+        };
+        if (NBMAX == 1 || rows <= 8) unit(std::integral_constant<int, 1>());
+        else unit(std::integral_constant<int, NBMAX>());
     }
 }
 
 // One warp sums every token's rows of 16 features, in slot order: 4 lanes a token,
 // TP of 8 tokens each at a time with 4 slots' loads in flight.  (A block that falls
 // behind brings its columns' last units and has to sum them too: at 11 us for 64
-// tokens, one load at a time, it fell ever further behind, and the second kernel
-// took 211 us instead of 100.)
+// tokens, one load at a time, it fell ever further behind, and the second product
+// took 211 us instead of 120.)
 template <int TP>
-__device__ __forceinline__ void sum_rows(const Args& a, const Plan& P, const float* y, int f0) {
+__device__ __forceinline__ void sum_rows(const Args& a, const float* slot_w, const short* slot_row, const float* y, int f0) {
     const int lane = threadIdx.x & 31, f = 4 * (lane & 3);
     for (int t0 = lane >> 2; t0 < a.T; t0 += 8 * TP) {
         float4 sum[TP];
@@ -297,12 +604,12 @@ __device__ __forceinline__ void sum_rows(const Args& a, const Plan& P, const flo
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int t = t0 + 8 * i, s = t * a.k + j0 + j;
-                    const bool in = t < a.T && j0 + j < a.k && P.slot_id[s] != a.E;
+                    const int row = t < a.T && j0 + j < a.k ? slot_row[s] : -1;
                     v[i][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     w[i][j] = 0.0f;
-                    if (in) {
-                        v[i][j] = __ldcg(reinterpret_cast<const float4*>(y + row_of(P, P.slot_id[s], t) * kRows + f));
-                        w[i][j] = P.slot_w[s];
+                    if (row >= 0) {
+                        v[i][j] = __ldcg(reinterpret_cast<const float4*>(y + row * kRows + f));
+                        w[i][j] = slot_w[s];
                     }
                 }
 #pragma unroll
@@ -318,78 +625,95 @@ __device__ __forceinline__ void sum_rows(const Args& a, const Plan& P, const flo
 #pragma unroll
         for (int i = 0; i < TP; ++i) {
             const int t = t0 + 8 * i;
-            if (t < a.T && f0 + f < a.F)
-                *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(t) * a.F + f0 + f) =
+            if (t < a.T && f0 + f < a.p[1].F)
+                *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(t) * a.p[1].F + f0 + f) =
                     make_uint2(moe::pack_bf16x2(sum[i].x, sum[i].y), moe::pack_bf16x2(sum[i].z, sum[i].w));
         }
     }
 }
 
-// R: the most rows of a unit (8, 16 or 32; a.xrows <= R).  Dynamic shared memory:
-// the ring (tiles want 1024-byte boundaries), two buffers of partial sums, and
-// every product warp's columns of x, [warp][step][row][8 vectors].
-template <bool FP8, bool GATED, int R>
-__global__ void __launch_bounds__(kThreads, R == 8 ? 2 : 1)
-few_tokens_kernel(const __grid_constant__ CUtensorMap map, const Args a) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    using Sums = float4[R / 8][kProduct][32];   // group of 8 rows, warp, lane
-    constexpr int kStageBytes = kTiles<FP8> * kTileBytes;
-    uint8_t* ring = smem + (-moe::smem_u32(smem) & 1023u);
-    Sums* red = reinterpret_cast<Sums*>(ring + a.stages * kStageBytes);
-    uint8_t* xcols = ring + a.stages * kStageBytes + 2 * sizeof(Sums);
-    __shared__ Plan P;
-    __shared__ Ring S;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
-    if (GATED) {
-        if (blockIdx.x == 0)
-            for (int i = threadIdx.x; i < a.columns; i += kThreads) a.arrived[i] = 0;
-        moe::launch_dependents();   // the second product may take its place beside this one
+// One product on one of the two finishing warps: every other unit.
+template <bool FIRST, int NBMAX>
+__device__ __forceinline__ void finish(const Product& p, const Args& a, const Sums<NBMAX>* red, const float* slot_w, const short* slot_row,
+                                       int& count) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, own = (threadIdx.x >> 5) - kProduct, rows_all = a.T * a.k;
+    const int chunks = chunks_of(a);
+    for (Run<FIRST> u(chunks, p.F); u.left > 0; u.next(), ++count) {
+        const int turn = count & 1, f0 = u.f0();
+        if (turn != own) continue;
+        const int4 chunk = chunk_of(a, u.chunk);
+        bar_sync(kFull + turn);
+        for (int b = 0; 8 * b < chunk.z; ++b) {
+            float4 s = red[turn][b][0][lane];
+#pragma unroll
+            for (int i = 1; i < kProduct; ++i) {
+                const float4 v = red[turn][b][i][lane];
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
+            const float top[2] = {s.x, s.y}, bottom[2] = {s.z, s.w};   // weight rows l / 4 and l / 4 + 8
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = 8 * b + 2 * (lane & 3) + j;
+                if (row >= chunk.z) continue;
+                if (FIRST) {
+                    if (f0 + g < p.F)
+                        a.h[static_cast<int64_t>(chunk.y + row) * p.F + f0 + g] =
+                            __float2bfloat16_rn(top[j] / (1.0f + expf(-top[j])) * bottom[j]);
+                } else {
+                    float* y = a.part + (static_cast<int64_t>(u.f) * rows_all + chunk.y + row) * kRows;
+                    y[g] = top[j];
+                    y[g + 8] = bottom[j];
+                }
+            }
+        }
+        bar_arrive(kEmpty + turn);
+        if (FIRST) continue;
+        // the last of this column's units sums every token's rows
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(&a.arrived[u.f], 1);
+        if (__shfl_sync(0xffffffffu, before, 0) != chunks - 1) continue;
+        __threadfence();
+        sum_rows<NBMAX == 1 ? 1 : 4>(a, slot_w, slot_row, a.part + static_cast<int64_t>(u.f) * rows_all * kRows, f0);
     }
-    if (threadIdx.x == 0) {
+}
+
+// NBMAX: the most groups of 8 rows of a chunk (a.xrows <= 8 NBMAX).
+template <bool FP8, int NBMAX>
+__global__ void __launch_bounds__(kThreads, 1)
+few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m2, const Args a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* ring = smem + (-moe::smem_u32(smem) & 1023u);   // swizzled tiles
+    auto* red = reinterpret_cast<Sums<NBMAX>*>(ring + a.stages * kStageBytes);
+    uint8_t* xcols = ring + a.stages * kStageBytes + 2 * sizeof(Sums<NBMAX>);
+    __shared__ Ring S;
+    __shared__ float unscale[kProduct][8 * NBMAX];   // FP8: of a warp's columns of a row of x
+    __shared__ float slot_w[kMaxSlots];
+    __shared__ short slot_row[kMaxSlots];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp == kProduct + 2 && lane == 0) {
         S.abort_flag = 0;
         for (int i = 0; i < a.stages; ++i) {
             moe::mbar_init(moe::smem_u32(&S.full[i]), 1);
-            moe::mbar_init(moe::smem_u32(&S.empty[i]), kProduct);
+            moe::mbar_init(moe::smem_u32(&S.empty[i]), kTiles);
         }
         moe::fence_barrier_init();
-        moe::prefetch_tensormap(&map);
+        moe::prefetch_tensormap(&m1.whole);
+        moe::prefetch_tensormap(&m2.whole);
     }
-    make_plan(a, P, GATED && blockIdx.x == 0);
-    constexpr int kFeatures = GATED ? kRows / 2 : kRows;
-    const int per = (a.F + kFeatures - 1) / kFeatures;   // units of a chunk
-    const int64_t units = static_cast<int64_t>(P.chunks) * per;
-    const int begin = static_cast<int>(units * blockIdx.x / gridDim.x), end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
-    const int steps = (a.K + kColumns - 1) / kColumns;   // stages of a unit
-    constexpr int kTileColumns = kRowBytes / (FP8 ? 1 : 2);
+    __syncthreads();
+    const int chunks = chunks_of(a);
     if (warp == kProduct + 2) {
-        // ---- producer
         int slot = 0;
         uint32_t turn = 0;
         int64_t filled = 0;
         bool gave_up = false;
-        for (int unit = begin; unit < end && !gave_up; ++unit) {
-            const int c = unit / per, f0 = (unit - c * per) * kFeatures, e = P.chunk_expert[c];
-            for (int k0 = 0; k0 < a.K; k0 += kColumns, ++filled) {
-                if (filled >= a.stages && !moe::mbar_wait(moe::smem_u32(&S.empty[slot]), turn ^ 1u, &S.abort_flag, kWaitNs)) {
-                    gave_up = true;
-                    break;
-                }
-                const int tiles = min(kTiles<FP8>, (a.K - k0 + kTileColumns - 1) / kTileColumns);
-                const uint32_t bar = moe::smem_u32(&S.full[slot]), dst = moe::smem_u32(ring) + slot * kStageBytes;
-                if (moe::elect_one()) {
-                    moe::mbar_arrive_expect_tx(bar, tiles * kTileBytes);
-                    for (int i = 0; i < tiles; ++i) {
-                        if (GATED) moe::tma_load_4d(dst + i * kTileBytes, &map, bar, k0 + i * kTileColumns, f0, 0, e);
-                        else moe::tma_load_3d(dst + i * kTileBytes, &map, bar, k0 + i * kTileColumns, f0, e);
-                    }
-                }
-                __syncwarp();
-                if (++slot == a.stages) {
-                    slot = 0;
-                    turn ^= 1u;
-                }
-            }
-        }
+        produce<FP8, true>(m1, a.p[0], a, S, moe::smem_u32(ring), slot, turn, filled, gave_up);
+        if (!gave_up) produce<FP8, false>(m2, a.p[1], a, S, moe::smem_u32(ring), slot, turn, filled, gave_up);
         if (gave_up) {   // no copy may land after the block has ended
             if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
             S.abort_flag = 1;
@@ -398,233 +722,156 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap map, const Args a) {
                 moe::mbar_wait(moe::smem_u32(&S.full[i]), static_cast<uint32_t>((filled - 1 - i) / a.stages) & 1u, &never, kWaitNs / 16);
         }
     } else if (warp < kProduct) {
-        // ---- this warp's 64 columns of every stage
-        int turn = 0, slot = 0, held = -1;
-        uint32_t phase = 0;
-        uint8_t* const mine = xcols + static_cast<size_t>(warp) * steps * a.xrows * kRowBytes;
-        // vector q of a step's 64 columns, counted from the step's first
-        const auto column = [&](int q) { return FP8 ? 128 * (warp / 2) + 16 * ((q & ~1) + (warp & 1)) + 8 * (q & 1) : 64 * warp + 8 * q; };
-        const int blocks_k = a.K / 128, block0 = warp / 2;   // FP8: scales of a row, and of this warp's first columns
-        const int64_t blocks_n = ((GATED ? 2 : 1) * static_cast<int64_t>(a.F) + 127) / 128;
-        // lane i's scales of step i, fetched a unit ahead
-        float s0 = 0.0f, s1 = 0.0f;
-        const auto scales_of = [&](int unit, int step, float& v0, float& v1) {
-            const int c = unit / per, f0 = (unit - c * per) * kFeatures;
-            const float* row = a.scales + P.chunk_expert[c] * blocks_n * blocks_k;
-            const int k = (step + lane) * (kColumns / 128) + block0;
-            if (k < blocks_k) {
-                v0 = __ldg(row + static_cast<int64_t>(f0 / 128) * blocks_k + k);
-                v1 = GATED ? __ldg(row + static_cast<int64_t>((a.F + f0) / 128) * blocks_k + k) : v0;
-            }
-        };
-        if (FP8 && begin < end) scales_of(begin, 0, s0, s1);
-        for (int unit = begin; unit < end; ++unit, turn ^= 1) {
-            const Unit u = unit_at<GATED>(a, P, unit, per);
-            float n0 = 0.0f, n1 = 0.0f;
-            if (FP8 && unit + 1 < end) scales_of(unit + 1, 0, n0, n1);
-            if (u.chunk != held) {   // this warp's columns of the next rows of x
-                if (!GATED && held < 0) moe::wait_for_primary();
-                held = u.chunk;
-                __syncwarp();
-                const int vectors = steps * u.rows * 8;
-                for (int v0 = 0; v0 < vectors; v0 += 32 * 8) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int at = v0 + 32 * i + lane, q = at & 7, step = (at >> 3) / u.rows, r = (at >> 3) - step * u.rows;
-                        const int k = step * kColumns + column(q);
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (at < vectors && k < a.K)
-                            v[i] = a.x[(static_cast<int64_t>(GATED ? P.token[u.p + r] : u.p + r) * a.K + k) / 8];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int at = v0 + 32 * i + lane, q = at & 7, step = (at >> 3) / u.rows, r = (at >> 3) - step * u.rows;
-                        if (at < vectors)
-                            *reinterpret_cast<uint4*>(mine + (step * a.xrows + r) * kRowBytes + (q ^ (r & 7)) * 16) = v[i];
-                    }
-                }
-                __syncwarp();
-            }
-            const auto go = [&](auto nb) {
-                constexpr int NB = decltype(nb)::value;
-                float d[NB][4];
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[b][i] = 0.0f;
-                for (int step = 0; step < steps; ++step) {
-                    if (FP8 && step > 0 && step % 32 == 0) scales_of(unit, step, s0, s1);
-                    if (!moe::mbar_wait(moe::smem_u32(&S.full[slot]), phase, &S.abort_flag, kWaitNs)) {
-                        if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
-                        S.abort_flag = 1;   // what follows is not waited for as long
-                    }
-                    const uint8_t* tile = ring + slot * kStageBytes + (FP8 ? warp / 2 : warp) * kTileBytes;
-                    const uint8_t* xs = mine + step * a.xrows * kRowBytes;
-                    if (step * kColumns + (FP8 ? 128 * (warp / 2) : 64 * warp) < a.K) {
-                        if (FP8)
-                            multiply_fp8<NB>(tile, warp & 1, xs, u.rows, __shfl_sync(0xffffffffu, s0, step & 31),
-                                             __shfl_sync(0xffffffffu, s1, step & 31), d);
-                        else multiply<NB>(tile, xs, u.rows, d);
-                    }
-                    __syncwarp();
-                    if (lane == 0) moe::mbar_arrive(moe::smem_u32(&S.empty[slot]));
-                    if (++slot == a.stages) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
-                }
-                if (unit - begin >= 2) bar_sync(kEmpty + turn);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) red[turn][b][warp][lane] = make_float4(d[b][0], d[b][1], d[b][2], d[b][3]);
-            };
-            if (R == 8 || u.rows <= 8) go(std::integral_constant<int, 1>());
-            else if (R == 16 || u.rows <= 16) go(std::integral_constant<int, (R >= 16 ? 2 : 1)>());
-            else go(std::integral_constant<int, R / 8>());
-            bar_arrive(kFull + turn);
-            s0 = n0;
-            s1 = n1;
-        }
+        Place place{0, 0, 0};
+        int count = 0;
+        multiply<FP8, true, NBMAX>(a.p[0], a, S, ring, red, xcols, unscale, place, 0, count);
+        const int first = count * a.p[0].steps;
+        bar_sync(kReady);
+        multiply<FP8, false, NBMAX>(a.p[1], a, S, ring, red, xcols, unscale, place, first, count);
         // the finishing warps arrive once for every unit: take the last two as well
-        for (int i = max(0, end - begin - 2); i < end - begin; ++i) bar_sync(kEmpty + (i & 1));
+        for (int i = max(0, count - 2); i < count; ++i) bar_sync(kEmpty + (i & 1));
     } else {
-        // ---- finishing: every other unit
-        if (!GATED) moe::wait_for_primary();
-        const int turn = warp - kProduct, rows_all = a.T * a.k;
-        for (int unit = begin + turn; unit < end; unit += 2) {
-            const Unit u = unit_at<GATED>(a, P, unit, per);
-            bar_sync(kFull + turn);
-            for (int b = 0; 8 * b < u.rows; ++b) {
-                float4 s = red[turn][b][0][lane];
-#pragma unroll
-                for (int i = 1; i < kProduct; ++i) {
-                    const float4 v = red[turn][b][i][lane];
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
-                }
-                const float top[2] = {s.x, s.y}, bottom[2] = {s.z, s.w};   // weight rows l / 4 and l / 4 + 8
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int row = 8 * b + 2 * (lane & 3) + j;
-                    if (row >= u.rows) continue;
-                    if (GATED) {
-                        if (u.f0 + g < a.F)
-                            a.h[static_cast<int64_t>(u.p + row) * a.F + u.f0 + g] =
-                                __float2bfloat16_rn(top[j] / (1.0f + expf(-top[j])) * bottom[j]);
-                    } else {
-                        float* y = a.part + (static_cast<int64_t>(u.f0 / kRows) * rows_all + u.p + row) * kRows;
-                        y[g] = top[j];
-                        y[g + 8] = bottom[j];
-                    }
+        const int own = warp - kProduct;
+        for (int s = 32 * own + lane; s < a.T * a.k; s += 64) {
+            slot_w[s] = __ldcg(&a.plan->slot_w[s]);
+            slot_row[s] = static_cast<short>(min(static_cast<int>(__ldcg(&a.plan->slot_row[s])), a.T * a.k - 1));
+        }
+        asm volatile("bar.sync 6, 64;" ::: "memory");
+        int count = 0;
+        finish<true, NBMAX>(a.p[0], a, red, slot_w, slot_row, count);
+        // every row of h is written before any is read
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) atomicAdd(&a.plan->done, 1u);
+        if (own == 0) {
+            const unsigned all = 2 * gridDim.x;
+            const uint64_t t0 = moe::global_timer_ns();
+            for (unsigned i = 1;; ++i) {
+                unsigned done;
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(done) : "l"(&a.plan->done) : "memory");
+                if (done >= all) break;
+                if ((i & 63u) == 0 && (S.abort_flag || moe::global_timer_ns() - t0 > kWaitNs)) {
+                    if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
+                    S.abort_flag = 1;
+                    break;
                 }
             }
-            bar_arrive(kEmpty + turn);
-            if (GATED) continue;
-            // the last of this column's units sums every token's rows
             __threadfence();
-            __syncwarp();
-            int before = 0;
-            if (lane == 0) before = atomicAdd(&a.arrived[u.f0 / kRows], 1);
-            if (__shfl_sync(0xffffffffu, before, 0) != P.chunks - 1) continue;
-            __threadfence();
-            sum_rows<R == 8 ? 1 : 4>(a, P, a.part + static_cast<int64_t>(u.f0 / kRows) * rows_all * kRows, u.f0);
+            bar_arrive(kReady);
         }
+        finish<false, NBMAX>(a.p[1], a, red, slot_w, slot_row, count);
     }
-    if (!GATED && P.chunks == 0) {   // no token has an expert
-        moe::wait_for_primary();
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < static_cast<int64_t>(a.T) * a.F;
+    if (chunks == 0)   // no token has an expert
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < static_cast<int64_t>(a.T) * a.p[1].F;
              i += static_cast<int64_t>(gridDim.x) * kThreads)
             a.out[i] = __float2bfloat16_rn(0.0f);
-    }
 }
 
-// The kernel may take that much dynamic shared memory; remembered per device.
-bool allow_smem(const void* kernel, std::atomic<int> (&cache)[moe::kMaxDevices], size_t smem) {
+constexpr size_t kSmem = 227 * 1024, kLeastRing = 64 * 1024;
+
+template <bool FP8>
+Product product(const __nv_bfloat16* x, const float* scales, int K, int F) {
+    Product p{x, scales, K, F, K / kTileColumns<FP8> * kTileColumns<FP8>, 0, 0};
+    p.whole_steps = (p.whole + kColumns<FP8> - 1) / kColumns<FP8>;
+    p.steps = (p.whole_steps + (p.whole < K) + 1) / 2 * 2;
+    return p;
+}
+
+// Shared memory: as deep a ring as partial sums and rows of x leave, and no fewer
+// than kLeastRing bytes: longer rows are taken fewer at a time.
+template <bool FP8, int NBMAX>
+size_t shape(int T, const Product (&p)[2], int& xrows, int& stages) {
+    const size_t steps = p[0].steps > p[1].steps ? p[0].steps : p[1].steps;
+    const size_t row = steps / 2 * kProduct * kRowBytes * (FP8 ? 2 : 1);   // of x, all warps
+    const size_t fixed = sizeof(Ring) + kProduct * 8 * NBMAX * sizeof(float) + kMaxSlots * (sizeof(float) + sizeof(short)) + 64 + 1024;
+    const size_t sums = 2 * sizeof(Sums<NBMAX>), most = (kSmem - fixed - sums - kLeastRing) / row;
+    xrows = T < 8 * NBMAX ? T : 8 * NBMAX;
+    if (most < static_cast<size_t>(xrows)) xrows = static_cast<int>(most);
+    const size_t n = (kSmem - fixed - sums - xrows * row) / kStageBytes;
+    stages = static_cast<int>(n < kMaxStages ? n / 2 * 2 : kMaxStages);   // even, at least 4
+    return 1024 + static_cast<size_t>(stages) * kStageBytes + sums + xrows * row;
+}
+
+// The kernel may take all of an SM's shared memory; remembered per device.
+bool allow_smem(const void* kernel, std::atomic<int> (&cache)[moe::kMaxDevices]) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= moe::kMaxDevices) return false;
-    if (cache[dev].load(std::memory_order_relaxed) >= static_cast<int>(smem)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+    if (cache[dev].load(std::memory_order_relaxed)) return true;
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem - at.sharedSizeBytes)) != cudaSuccess) {
         (void)cudaGetLastError();
         return false;
     }
-    cache[dev].store(static_cast<int>(smem), std::memory_order_relaxed);
+    cache[dev].store(1, std::memory_order_relaxed);
     return true;
 }
 
-constexpr size_t kHalf = 113 * 1024, kWhole = 227 * 1024;   // shared memory of a block, with another one beside it or not
-constexpr size_t kLeastRing = 64 * 1024;
-
-// Shared memory of a product of K columns and at most T rows an expert: R, a.xrows
-// and a.stages.  Room for a block of the other kernel beside this one if the ring
-// is still deep enough; else the whole SM, with as many rows of x as leave the ring
-// that depth.
-template <bool FP8>
-size_t shape(Args& a, int& R) {
-    const size_t row = static_cast<size_t>((a.K + kColumns - 1) / kColumns) * kProduct * kRowBytes, stage = kTiles<FP8> * kTileBytes;
-    const size_t fixed = sizeof(Plan) + sizeof(Ring) + 64 + 1024;   // with what alignment takes
-    const auto sums = [](int r) { return static_cast<size_t>(2 * r / 8) * kProduct * 32 * sizeof(float4); };
-    size_t all = kWhole;
-    R = a.T <= 8 ? 8 : a.T <= 16 ? 16 : 32;
-    if (R == 8 && fixed + sums(8) + a.T * row + kLeastRing <= kHalf) {
-        all = kHalf;
-        a.xrows = a.T;
-    } else {
-        while (R > 8 && fixed + sums(R) + (a.T < R ? a.T : R) * row + kLeastRing > kWhole) R /= 2;
-        const size_t most = (kWhole - fixed - sums(R) - kLeastRing) / row;
-        a.xrows = a.T < R ? a.T : R;
-        if (most < static_cast<size_t>(a.xrows)) a.xrows = static_cast<int>(most);
-    }
-    const size_t n = (all - fixed - sums(R) - a.xrows * row) / stage;
-    a.stages = static_cast<int>(n < kMaxStages ? n : kMaxStages);
-    return 1024 + a.stages * stage + sums(R) + a.xrows * row;
-}
-
-// x and W of 16 rows by 128 bytes; GATED: 8 gate rows and the same 8 up rows.
-bool weight_map(CUtensorMap* map, bool fp8, bool gated, const void* W, int E, int F, int K) {
-    const cuuint64_t e = fp8 ? 1 : 2, k = K, f = F;
-    const cuuint32_t columns = fp8 ? kRowBytes : kRowBytes / 2;
+// 16 weight rows (gated: 8 gate rows and the same 8 up rows) by kTiles or one tile
+// of 128 bytes.  One copy brings a stage: sixteen, one a row, took a producer 1.2 us
+// of the 0.4 us that the memory takes for a stage, and eight, one a tile, 0.6 us.
+// A matrix without whole tiles has no copies of them.
+bool weight_maps(Maps* m, bool fp8, bool gated, const void* W, int E, int F, int K) {
+    const cuuint64_t e = fp8 ? 1 : 2, k = K, f = F, n = E;
+    const cuuint32_t columns = kRowBytes / (fp8 ? 1 : 2);
+    const cuuint64_t tiles = K / columns;
+    bool ok = true;
     if (gated) {
-        const cuuint64_t dims[4] = {k, f, 2, static_cast<cuuint64_t>(E)}, strides[3] = {k * e, f * k * e, 2 * f * k * e};
-        const cuuint32_t box[4] = {columns, kRows / 2, 2, 1};
-        return moe::encode_tile_map(map, fp8, W, 4, dims, strides, box);
+        const cuuint64_t dims[5] = {columns, f, 2, tiles, n}, strides[4] = {k * e, f * k * e, kRowBytes, 2 * f * k * e};
+        const cuuint32_t box[5] = {columns, kRows / 2, 2, kTiles, 1};
+        if (tiles) ok = moe::encode_tile_map(&m->whole, fp8, W, 5, dims, strides, box);
+        const cuuint64_t rest_dims[4] = {k, f, 2, n}, rest_strides[3] = {k * e, f * k * e, 2 * f * k * e};
+        const cuuint32_t rest_box[4] = {columns, kRows / 2, 2, 1};
+        if (K % columns) ok = ok && moe::encode_tile_map(&m->rest, fp8, W, 4, rest_dims, rest_strides, rest_box);
+    } else {
+        const cuuint64_t dims[4] = {columns, f, tiles, n}, strides[3] = {k * e, kRowBytes, f * k * e};
+        const cuuint32_t box[4] = {columns, kRows, kTiles, 1};
+        if (tiles) ok = moe::encode_tile_map(&m->whole, fp8, W, 4, dims, strides, box);
+        const cuuint64_t rest_dims[3] = {k, f, n}, rest_strides[2] = {k * e, f * k * e};
+        const cuuint32_t rest_box[3] = {columns, kRows, 1};
+        if (K % columns) ok = ok && moe::encode_tile_map(&m->rest, fp8, W, 3, rest_dims, rest_strides, rest_box);
     }
-    const cuuint64_t dims[3] = {k, f, static_cast<cuuint64_t>(E)}, strides[2] = {k * e, f * k * e};
-    const cuuint32_t box[3] = {columns, kRows, 1};
-    return moe::encode_tile_map(map, fp8, W, 3, dims, strides, box);
+    if (!tiles) m->whole = m->rest;
+    else if (K % columns == 0) m->rest = m->whole;
+    return ok;
 }
 
-template <bool FP8, bool GATED, int R>
-moe_status_t launch(const CUtensorMap& map, const Args& a, size_t smem, cudaStream_t s) {
+template <bool FP8, int NBMAX>
+moe_status_t launch(const moe_forward_args* f, Route r, Args a, const Maps& m1, const Maps& m2, cudaStream_t s) {
     static std::atomic<int> allowed[moe::kMaxDevices];
+    const auto kernel = few_layer_kernel<FP8, NBMAX>;
     const int sms = moe::sm_count();
-    if (sms <= 0 || !allow_smem(reinterpret_cast<const void*>(few_tokens_kernel<FP8, GATED, R>), allowed, smem)) return MOE_ERR_CUDA;
-    // a block per SM, if every slot has an expert of its own
-    const int chunks = a.T * a.k < a.E ? a.T * a.k : a.E, features = GATED ? kRows / 2 : kRows;
-    const int64_t units = static_cast<int64_t>((a.F + features - 1) / features) * chunks;
-    const int blocks = static_cast<int>(units < sms ? units : sms);
-    if (!GATED) return moe::launch_after(few_tokens_kernel<FP8, GATED, R>, dim3(blocks), kThreads, smem, s, map, a);
-    few_tokens_kernel<FP8, GATED, R><<<blocks, kThreads, smem, s>>>(map, a);
-    MOE_CHECK_LAUNCH();
+    if (sms <= 0 || !allow_smem(reinterpret_cast<const void*>(kernel), allowed)) return MOE_ERR_CUDA;
+    const size_t smem = shape<FP8, NBMAX>(f->T, a.p, a.xrows, a.stages);
+    r.chunk_rows = a.xrows;
+    const moe_status_t st = moe::launch_after(few_route_kernel, dim3(1), kRouteThreads, 0, s, r);
+    if (st != MOE_OK) return st;
+    // a block per SM, or per unit of the first product if every slot has an expert of its own
+    const int64_t units = static_cast<int64_t>((a.p[0].F + kRows / 2 - 1) / (kRows / 2)) * (f->T * f->k < f->E ? f->T * f->k : f->E);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;   // its blocks wait for one another
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, m1, m2, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
     return MOE_OK;
 }
 
-template <bool FP8, bool GATED>
-moe_status_t product(Args a, const void* W, cudaStream_t s) {
-    CUtensorMap map;
-    if (!weight_map(&map, FP8, GATED, W, a.E, a.F, a.K)) return MOE_ERR_CUDA;
-    int R;
-    const size_t smem = shape<FP8>(a, R);
-    if (R == 8) return launch<FP8, GATED, 8>(map, a, smem, s);
-    if (R == 16) return launch<FP8, GATED, 16>(map, a, smem, s);
-    return launch<FP8, GATED, 32>(map, a, smem, s);
-}
-
 template <bool FP8>
-moe_status_t both(const Args& a1, const void* W1, const Args& a2, const void* W2, cudaStream_t s) {
-    const moe_status_t st = product<FP8, true>(a1, W1, s);
-    return st != MOE_OK ? st : product<FP8, false>(a2, W2, s);
+moe_status_t run(const moe_forward_args* f, const Route& r, Args a, cudaStream_t s) {
+    a.p[0] = product<FP8>(static_cast<const __nv_bfloat16*>(f->x), f->W1_scales, f->H, f->I);
+    a.p[1] = product<FP8>(a.h, f->W2_scales, f->I, f->H);
+    Maps m1, m2;
+    if (!weight_maps(&m1, FP8, true, f->W1, f->E, f->I, f->H) || !weight_maps(&m2, FP8, false, f->W2, f->E, f->H, f->I)) return MOE_ERR_CUDA;
+    return f->T <= 8 ? launch<FP8, 1>(f, r, a, m1, m2, s) : launch<FP8, 2>(f, r, a, m1, m2, s);
 }
 
 bool valid_sizes(const moe_forward_args* a) {
@@ -640,7 +887,7 @@ bool supported(const moe_forward_args* a) {
 }
 
 struct Layout {
-    size_t arrived, h, part, total;
+    size_t plan, arrived, h, part, total;
 };
 
 Layout layout(const moe_forward_args* a) {
@@ -652,6 +899,7 @@ Layout layout(const moe_forward_args* a) {
         return at;
     };
     const size_t rows = static_cast<size_t>(a->T) * a->k, columns = (a->H + kRows - 1) / kRows;
+    l.plan = take(sizeof(Plan));
     l.arrived = take(columns * sizeof(int));
     l.h = take(rows * a->I * 2);
     l.part = take(columns * rows * kRows * sizeof(float));
@@ -681,26 +929,19 @@ extern "C" moe_status_t moe_forward_few(const moe_forward_args* a, void* ws, siz
     int* err = moe::device_error_word();
     if (!err) return MOE_ERR_CUDA;
     auto* base = static_cast<uint8_t*>(ws);
-    Args a1{};
-    a1.logits = a->logits;
-    a1.bias = a->expert_bias;
-    a1.mask = a->sentinel_mask;
-    a1.ids = a->topk_ids;
-    a1.w = a->topk_w;
-    a1.T = a->T, a1.E = a->E, a1.k = a->k, a1.renormalize = a->renormalize;
-    a1.h = reinterpret_cast<__nv_bfloat16*>(base + l.h);
-    a1.part = reinterpret_cast<float*>(base + l.part);
-    a1.out = static_cast<__nv_bfloat16*>(a->out);
-    a1.arrived = reinterpret_cast<int*>(base + l.arrived);
-    a1.columns = (a->H + kRows - 1) / kRows;
-    a1.err = err;
-    Args a2 = a1;
-    a1.x = static_cast<const uint4*>(a->x);
-    a1.scales = a->W1_scales;
-    a1.K = a->H, a1.F = a->I;
-    a2.x = reinterpret_cast<const uint4*>(a1.h);
-    a2.scales = a->W2_scales;
-    a2.K = a->I, a2.F = a->H;
+    const int columns = (a->H + kRows - 1) / kRows;
+    auto* plan = reinterpret_cast<Plan*>(base + l.plan);
+    auto* arrived = reinterpret_cast<int*>(base + l.arrived);
+    const Route r{a->logits, a->expert_bias, a->sentinel_mask, a->topk_ids, a->topk_w, a->T,   a->E,
+                  a->k,      a->renormalize, 0,                plan,        arrived,   columns, err};
+    Args args{};
+    args.plan = plan;
+    args.arrived = arrived;
+    args.h = reinterpret_cast<__nv_bfloat16*>(base + l.h);
+    args.part = reinterpret_cast<float*>(base + l.part);
+    args.out = static_cast<__nv_bfloat16*>(a->out);
+    args.T = a->T, args.E = a->E, args.k = a->k;
+    args.err = err;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return fp8 ? both<true>(a1, a->W1, a2, a->W2, s) : both<false>(a1, a->W1, a2, a->W2, s);
+    return fp8 ? run<true>(a, r, args, s) : run<false>(a, r, args, s);
 }

@@ -26,7 +26,6 @@
 #include <mutex>
 
 #include "common.cuh"
-#include "route.cuh"
 
 namespace {
 
@@ -49,6 +48,9 @@ SortGeometry geometry(int T, int k) {
     g.blocks = (T + g.tokens_per_block - 1) / g.tokens_per_block;
     return g;
 }
+
+using moe::key_value;
+using moe::order_key;
 
 // Ids outside [0, E] cannot be placed: they are sorted as sentinels and the
 // error word records the bad input.
@@ -76,10 +78,52 @@ __device__ __forceinline__ int route_token(const float* __restrict__ logits, con
     int my_id = E;  // lane j < k: the id of slot j
 
     if (logits) {
-        float my_w;
-        my_id = moe::top_picks<NV>(logits + static_cast<int64_t>(t) * E, bias, E, k, renormalize, my_w);
+        const float* row = logits + static_cast<int64_t>(t) * E;
+        float v[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int e = lane + 32 * j;
+            if (e < E) {
+                const float l = row[e];
+                v[j] = bias ? l + bias[e] : l;
+            } else {
+                v[j] = -INFINITY;
+            }
+        }
+        // each pick: the largest key over the warp (one warp reduction), then
+        // the lowest expert id holding it (a second one); a lane's candidate
+        // is its first slot with its largest key, the lowest id of the lane
+        uint32_t key[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) key[j] = lane + 32 * j < E ? order_key(v[j]) : 0u;
+        uint32_t taken = 0;   // bit j: this lane's slot j was picked
+        float my_v = -INFINITY;
+        for (int r = 0; r < k; ++r) {
+            uint32_t bk = 0u;
+            int bj = 0;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const uint32_t kj = (taken >> j) & 1u ? 0u : key[j];
+                if (kj > bk) { bk = kj; bj = j; }
+            }
+            const uint32_t m = __reduce_max_sync(0xffffffffu, bk);
+            const int bi = __reduce_min_sync(0xffffffffu, m != 0u && bk == m ? lane + 32 * bj : INT_MAX);
+            if (m != 0u && (bi & 31) == lane) taken |= 1u << (bi >> 5);
+            if (lane == r) { my_v = m != 0u ? key_value(m) : -INFINITY; my_id = bi; }
+        }
+        const float mx = __shfl_sync(0xffffffffu, my_v, 0);  // pick 0 is the maximum
+        float part = 0.0f;
+        if (renormalize) {
+            part = lane < k ? expf(my_v - mx) : 0.0f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (lane + 32 * j < E) part += expf(v[j] - mx);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
         if (lane < k) {
-            w[slot0 + lane] = my_w;
+            w[slot0 + lane] = expf(my_v - mx) / part;
             if (mask && mask[slot0 + lane]) my_id = E;
             my_id = checked_id(my_id, E, err);
             ids[slot0 + lane] = my_id;
