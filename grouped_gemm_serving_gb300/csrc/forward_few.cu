@@ -59,14 +59,16 @@ constexpr int kMaxT = 64;                       // tokens: the bits of a mask
 constexpr int kMaxSlots = 1024;
 constexpr int kMaxE = 256;
 constexpr int kMaxK = 32768;                    // columns of a product: a row of x takes 2 bytes each of a block
-constexpr int kRouteThreads = 1024;
+// Threads of the routing kernel; up to kLight tokens few enough, and little enough
+// shared memory, that the second kernel's block fits beside it on its SM.
+constexpr int kRouteThreads = 1024, kLightThreads = 128, kLight = 8;
 
 // What the first kernel leaves for the second, in the workspace.
 struct Plan {
     int chunks;
     unsigned done;                // blocks' finishing warps that have written their last h
     int pad[2];
-    int4 chunk[kMaxSlots];        // expert, first row, rows
+    int4 chunk[kMaxSlots];        // expert, first row, rows, first row's token
     float slot_w[kMaxSlots];
     short slot_row[kMaxSlots];    // -1: a sentinel
     uint8_t token[kMaxSlots];     // a row's token
@@ -87,21 +89,20 @@ struct Route {
 };
 
 // A token's k picks on one warp, moe_route_sort's bit for bit: the largest of
-// logits[e] + bias[e], e < E, ties to the lower id.  Lane j < k returns the id of the j-th and
+// row[e], e < E (logit and bias), ties to the lower id.  Lane j < k returns the id of the j-th and
 // its weight in w; a NaN is never picked, and a pick that too many of them left
-// unfilled is INT_MAX.  row: E words of the warp's own.  Every lane keeps the best
+// unfilled is INT_MAX.  row is in shared memory and is
+// overwritten.  Every lane keeps the best
 // of its own experts; where one is taken all lanes look for the next among that
 // lane's.  Small loops on purpose: all this runs once, and instructions that come from L2 for
 // one use cost more than they do.
-__device__ __forceinline__ int picks(const float* logits, const float* bias, float* row, int E, int k, int renormalize, float& w) {
+__device__ __forceinline__ int picks(float* row, int E, int k, int renormalize, float& w) {
     const int lane = threadIdx.x & 31;
     uint32_t best = 0;
     int id = INT_MAX;
 #pragma unroll 1
     for (int e = lane; e < E; e += 32) {
-        const float v = bias ? logits[e] + bias[e] : logits[e];
-        row[e] = v;
-        const uint32_t key = moe::order_key(v);
+        const uint32_t key = moe::order_key(row[e]);
         if (key > best) {
             best = key;
             id = e;
@@ -143,19 +144,26 @@ __device__ __forceinline__ int picks(const float* logits, const float* bias, flo
 }
 
 // One block routes all tokens, a warp each at a time, and zeroes the counters of the
-// second kernel.
+// second kernel.  Dynamic shared memory: the logits, with their biases.
 __global__ void __launch_bounds__(kRouteThreads)
 few_route_kernel(const Route a) {
-    __shared__ uint32_t tokens[kMaxE][2];   // the expert's tokens
-    __shared__ int base[kMaxE];             // its first row
+    extern __shared__ __align__(16) float logits[];   // [T, E]
+    __shared__ uint32_t tokens[kMaxE][2];             // the expert's tokens
+    __shared__ int base[kMaxE];                       // its first row
     __shared__ short slot_id[kMaxSlots];
-    __shared__ float rows[kRouteThreads / 32][kMaxE];
     __shared__ int sums[kMaxE / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < 2 * kMaxE) (&tokens[0][0])[tid] = 0;
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < 2 * kMaxE; i += threads) (&tokens[0][0])[i] = 0;
     moe::wait_for_primary();   // what wrote the logits or ids
-#pragma unroll 1
-    for (int i = tid; i < a.columns; i += kRouteThreads) a.arrived[i] = 0;
+    moe::launch_dependents();
+    if (a.logits) {
+#pragma unroll 4
+        for (int i = tid; i < a.T * a.E; i += threads) {
+            const float l = a.logits[i];
+            logits[i] = a.bias ? l + a.bias[i % a.E] : l;
+        }
+    }
+    for (int i = tid; i < a.columns; i += threads) a.arrived[i] = 0;
     if (tid == 0) a.plan->done = 0;
     __syncthreads();
     const auto take = [&](int t, int s, int id, bool changed) {
@@ -174,9 +182,9 @@ few_route_kernel(const Route a) {
     };
     if (a.logits) {
 #pragma unroll 1
-        for (int t = warp; t < a.T; t += kRouteThreads / 32) {
+        for (int t = warp; t < a.T; t += threads / 32) {
             float w;
-            const int id = picks(a.logits + static_cast<int64_t>(t) * a.E, a.bias, rows[warp], a.E, a.k, a.renormalize, w);
+            const int id = picks(logits + t * a.E, a.E, a.k, a.renormalize, w);
             if (lane < a.k) {
                 const int s = t * a.k + lane;
                 a.plan->slot_w[s] = w;
@@ -185,46 +193,55 @@ few_route_kernel(const Route a) {
             }
         }
     } else {
-        for (int s = tid; s < a.T * a.k; s += kRouteThreads) {
+        for (int s = tid; s < a.T * a.k; s += threads) {
             a.plan->slot_w[s] = a.w[s];
             take(s / a.k, s, a.ids[s], false);
         }
     }
     __syncthreads();
-    // thread e: rows (low half) and chunks (high half) of the experts up to e
-    int n = 0, c = 0, upto = 0;
-    if (tid < kMaxE) {
-        n = __popc(tokens[tid][0]) + __popc(tokens[tid][1]);
-        c = n > a.chunk_rows ? (n + a.chunk_rows - 1) / a.chunk_rows : (n > 0);
-        upto = n | c << 16;
+    // rows (low half) and chunks (high half) of the experts up to e, in blocks of 32 experts
+    const auto rows_of = [&](int e) { return e < a.E ? __popc(tokens[e][0]) + __popc(tokens[e][1]) : 0; };
+    const auto chunks_of = [&](int n) { return n > a.chunk_rows ? (n + a.chunk_rows - 1) / a.chunk_rows : (n > 0); };
+#pragma unroll 1
+    for (int block = warp; block < kMaxE / 32; block += threads / 32) {
+        const int n = rows_of(32 * block + lane);
+        int all = n | chunks_of(n) << 16;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+        if (lane == 0) sums[block] = all;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int block = warp; block < kMaxE / 32; block += threads / 32) {
+        const int e = 32 * block + lane, n = rows_of(e), c = chunks_of(n);
+        int upto = n | c << 16;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int below = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += below;
         }
-        if (lane == 31) sums[warp] = upto;
-    }
-    __syncthreads();
-    if (tid < kMaxE) {
 #pragma unroll 1
-        for (int i = 0; i < warp; ++i) upto += sums[i];
-        if (tid == kMaxE - 1) a.plan->chunks = upto >> 16;
+        for (int i = 0; i < block; ++i) upto += sums[i];
+        if (e == kMaxE - 1) a.plan->chunks = upto >> 16;
         if (n) {
             const int row = (upto & 0xFFFF) - n, first = (upto >> 16) - c;
-            base[tid] = row;
+            base[e] = row;
+            uint64_t left = tokens[e][0] | static_cast<uint64_t>(tokens[e][1]) << 32;
 #pragma unroll 1
-            for (int i = 0; i < c; ++i)
-                a.plan->chunk[first + i] = make_int4(tid, row + i * a.chunk_rows, min(a.chunk_rows, n - i * a.chunk_rows), 0);
+            for (int r = 0; r < n; ++r, left &= left - 1) {
+                const int t = __ffsll(left) - 1, i = r / a.chunk_rows;
+                a.plan->token[row + r] = static_cast<uint8_t>(t);
+                if (r == i * a.chunk_rows) a.plan->chunk[first + i] = make_int4(e, row + r, min(a.chunk_rows, n - r), t);
+            }
         }
     }
     __syncthreads();
-    for (int s = tid; s < a.T * a.k; s += kRouteThreads) {
+    for (int s = tid; s < a.T * a.k; s += threads) {
         const int id = slot_id[s], t = s / a.k;
         int row = -1;
         if (id < a.E) {   // the row of token t among the expert's
             const uint32_t below = (1u << (t & 31)) - 1;
             row = base[id] + (t < 32 ? __popc(tokens[id][0] & below) : __popc(tokens[id][0]) + __popc(tokens[id][1] & below));
-            a.plan->token[row] = static_cast<uint8_t>(t);   // slots of the same expert and token write the same
         }
         a.plan->slot_row[s] = static_cast<short>(row);
     }
@@ -306,11 +323,12 @@ struct Ring {
 // What the plan says, within bounds whatever it says: calls that share a workspace
 // by mistake get wrong results, not wrong addresses.
 __device__ __forceinline__ int chunks_of(const Args& a) { return max(0, min(a.plan->chunks, a.T * a.k)); }
-__device__ __forceinline__ int4 chunk_of(const Args& a, int i) {   // expert, first row, rows
+__device__ __forceinline__ int4 chunk_of(const Args& a, int i) {   // expert, first row, rows, first row's token
     int4 c = __ldcg(&a.plan->chunk[i]);
     c.x = max(0, min(c.x, a.E - 1));
     c.z = max(1, min(c.z, a.xrows));
     c.y = max(0, min(c.y, a.T * a.k - c.z));
+    c.w = max(0, min(c.w, a.T - 1));
     return c;
 }
 
@@ -416,7 +434,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
     const int w_at = tile * kTileBytes + g * kRowBytes + ((2 * c) ^ g) * 16;
     const int blocks_k = p.K / 128;   // FP8: scales of a row, one a tile
     const int64_t blocks_n = ((FIRST ? 2 : 1) * static_cast<int64_t>(p.F) + 127) / 128;
-    int held = -1, rows = 0, row0 = 0, e = 0;
+    int held = -1, rows = 0, row0 = 0, token0 = 0, e = 0;
     int x_at[NBMAX];
     float s0 = 0.0f, s1 = 0.0f;
     // lane i's scales of this warp's step i (at most 16), for rows of the first and of the second 8
@@ -445,8 +463,9 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
             float f[NR];
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
-                const int r = row0 + min(r0 + j, rows - 1);
-                from[j] = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(FIRST ? min(a.plan->token[r], a.T - 1) : r) * p.K);
+                const int r = min(r0 + j, rows - 1);
+                const int row = FIRST ? (r ? min(a.plan->token[row0 + r], a.T - 1) : token0) : row0 + r;
+                from[j] = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(row) * p.K);
                 bits[j] = 0;
             }
 #pragma unroll 1
@@ -467,7 +486,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
                         const int k = (step < p.whole_steps ? step * kColumns<FP8> : p.whole) + tile * kTileColumns<FP8> + 8 * (at % kVectors);
                         const bool in = at < vectors && k < (step < p.whole_steps ? p.whole : p.K);
 #pragma unroll
-                        for (int j = 0; j < NR; ++j) v[j][i] = in ? __ldcg(from[j] + k / 8) : make_uint4(0, 0, 0, 0);
+                        for (int j = 0; j < NR; ++j) v[j][i] = in ? from[j][k / 8] : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
@@ -499,6 +518,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
             e = chunk.x;
             row0 = chunk.y;
             rows = chunk.z;
+            token0 = chunk.w;
             if (FP8) scales_of(u.f0());
             take_x();
 #pragma unroll
@@ -638,6 +658,24 @@ __device__ __forceinline__ void finish(const Product& p, const Args& a, const Su
                                        int& count) {
     const int lane = threadIdx.x & 31, g = lane >> 2, own = (threadIdx.x >> 5) - kProduct, rows_all = a.T * a.k;
     const int chunks = chunks_of(a);
+    // Columns whose units have been stored but not yet counted, in lanes 0 to waiting - 1:
+    // a fence and an atomic take longer than a short unit.
+    constexpr int kWaiting = 4;
+    int column = 0, waiting = 0;
+    const auto count_in = [&]() {
+        __threadfence();
+        __syncwarp();
+        const bool last = lane < waiting && atomicAdd(&a.arrived[column], 1) == chunks - 1;
+        unsigned mine = __ballot_sync(0xffffffffu, last);
+        waiting = 0;
+        if (mine == 0) return;
+        __threadfence();
+#pragma unroll 1
+        for (; mine; mine &= mine - 1) {   // the last of this column's units sums every token's rows
+            const int f = __shfl_sync(0xffffffffu, column, __ffs(mine) - 1);
+            sum_rows<NBMAX == 1 ? 1 : 4>(a, slot_w, slot_row, a.part + static_cast<int64_t>(f) * rows_all * kRows, f * kRows);
+        }
+    };
     for (Run<FIRST> u(chunks, p.F); u.left > 0; u.next(), ++count) {
         const int turn = count & 1, f0 = u.f0();
         if (turn != own) continue;
@@ -671,15 +709,10 @@ __device__ __forceinline__ void finish(const Product& p, const Args& a, const Su
         }
         bar_arrive(kEmpty + turn);
         if (FIRST) continue;
-        // the last of this column's units sums every token's rows
-        __threadfence();
-        __syncwarp();
-        int before = 0;
-        if (lane == 0) before = atomicAdd(&a.arrived[u.f], 1);
-        if (__shfl_sync(0xffffffffu, before, 0) != chunks - 1) continue;
-        __threadfence();
-        sum_rows<NBMAX == 1 ? 1 : 4>(a, slot_w, slot_row, a.part + static_cast<int64_t>(u.f) * rows_all * kRows, f0);
+        if (lane == waiting) column = u.f;
+        if (++waiting == kWaiting) count_in();
     }
+    if (!FIRST && waiting) count_in();
 }
 
 // NBMAX: the most groups of 8 rows of a chunk (a.xrows <= 8 NBMAX).
@@ -705,6 +738,7 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
         moe::prefetch_tensormap(&m1.whole);
         moe::prefetch_tensormap(&m2.whole);
     }
+    moe::wait_for_primary();   // the plan
     __syncthreads();
     const int chunks = chunks_of(a);
     if (warp == kProduct + 2) {
@@ -767,7 +801,9 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
             a.out[i] = __float2bfloat16_rn(0.0f);
 }
 
-constexpr size_t kSmem = 227 * 1024, kLeastRing = 64 * 1024;
+constexpr size_t kSmem = 227 * 1024, kLeastRing = 96 * 1024;
+// What the routing kernel of up to kLight tokens takes of it, its 1 KB of overhead too.
+constexpr size_t kLightSmem = 2 * kMaxE * 4 + kMaxE * 4 + kMaxSlots * 2 + kLight * kMaxE * 4 + 64 + 1024;
 
 template <bool FP8>
 Product product(const __nv_bfloat16* x, const float* scales, int K, int F) {
@@ -784,10 +820,11 @@ size_t shape(int T, const Product (&p)[2], int& xrows, int& stages) {
     const size_t steps = p[0].steps > p[1].steps ? p[0].steps : p[1].steps;
     const size_t row = steps / 2 * kProduct * kRowBytes * (FP8 ? 2 : 1);   // of x, all warps
     const size_t fixed = sizeof(Ring) + kProduct * 8 * NBMAX * sizeof(float) + kMaxSlots * (sizeof(float) + sizeof(short)) + 64 + 1024;
-    const size_t sums = 2 * sizeof(Sums<NBMAX>), most = (kSmem - fixed - sums - kLeastRing) / row;
+    const size_t all = T <= kLight ? kSmem - kLightSmem : kSmem;
+    const size_t sums = 2 * sizeof(Sums<NBMAX>), most = (all - fixed - sums - kLeastRing) / row;
     xrows = T < 8 * NBMAX ? T : 8 * NBMAX;
     if (most < static_cast<size_t>(xrows)) xrows = static_cast<int>(most);
-    const size_t n = (kSmem - fixed - sums - xrows * row) / kStageBytes;
+    const size_t n = (all - fixed - sums - xrows * row) / kStageBytes;
     stages = static_cast<int>(n < kMaxStages ? n / 2 * 2 : kMaxStages);   // even, at least 4
     return 1024 + static_cast<size_t>(stages) * kStageBytes + sums + xrows * row;
 }
@@ -844,7 +881,10 @@ moe_status_t launch(const moe_forward_args* f, Route r, Args a, const Maps& m1, 
     if (sms <= 0 || !allow_smem(reinterpret_cast<const void*>(kernel), allowed)) return MOE_ERR_CUDA;
     const size_t smem = shape<FP8, NBMAX>(f->T, a.p, a.xrows, a.stages);
     r.chunk_rows = a.xrows;
-    const moe_status_t st = moe::launch_after(few_route_kernel, dim3(1), kRouteThreads, 0, s, r);
+    static std::atomic<int> route_allowed[moe::kMaxDevices];
+    if (!allow_smem(reinterpret_cast<const void*>(few_route_kernel), route_allowed)) return MOE_ERR_CUDA;
+    const size_t logits = f->logits ? static_cast<size_t>(f->T) * f->E * sizeof(float) : 0;
+    const moe_status_t st = moe::launch_after(few_route_kernel, dim3(1), f->T <= kLight ? kLightThreads : kRouteThreads, logits, s, r);
     if (st != MOE_OK) return st;
     // a block per SM, or per unit of the first product if every slot has an expert of its own
     const int64_t units = static_cast<int64_t>((a.p[0].F + kRows / 2 - 1) / (kRows / 2)) * (f->T * f->k < f->E ? f->T * f->k : f->E);
@@ -853,11 +893,13 @@ moe_status_t launch(const moe_forward_args* f, Route r, Args a, const Maps& m1, 
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;   // its blocks wait for one another
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, m1, m2, a) != cudaSuccess) {
         (void)cudaGetLastError();
         return MOE_ERR_CUDA;
