@@ -31,8 +31,10 @@
 // quantised: it would save no weight bytes, and cost accuracy.
 //
 // h is rounded to bf16, the type of the MMA's operand.  The second product leaves
-// fp32 rows y; the block that brings the last of a 16-feature column's units sums
-// each token's rows in slot order and rounds once.
+// fp32 rows y; when all blocks are done each sums its share of the tokens' rows, in
+// slot order, and rounds once.  (Sums by whichever block brought the last of a
+// column's units fell to those that were behind already: 292 us instead of REPLACE64
+// for 64 tokens of 32 experts, 109 instead of REPLACE11 for 11 of 128.)
 #include <cuda_fp8.h>
 
 #include <climits>
@@ -66,8 +68,8 @@ constexpr int kRouteThreads = 1024, kLightThreads = 128, kLight = 8;
 // What the first kernel leaves for the second, in the workspace.
 struct Plan {
     int chunks;
-    unsigned done;                // blocks' finishing warps that have written their last h
-    int pad[2];
+    unsigned met[2];              // finishing warps that are done with the first product, and with the second
+    int pad;
     int4 chunk[kMaxSlots];        // expert, first row, rows, first row's token
     float slot_w[kMaxSlots];
     short slot_row[kMaxSlots];    // -1: a sentinel
@@ -83,8 +85,6 @@ struct Route {
     int T, E, k, renormalize;
     int chunk_rows;
     Plan* plan;
-    int* arrived;
-    int columns;
     int* err;
 };
 
@@ -143,8 +143,8 @@ __device__ __forceinline__ int picks(float* row, int E, int k, int renormalize, 
     return my_id;
 }
 
-// One block routes all tokens, a warp each at a time, and zeroes the counters of the
-// second kernel.  Dynamic shared memory: the logits, with their biases.
+// One block routes all tokens, a warp each at a time, and zeroes the second kernel's
+// counters.  Dynamic shared memory: the logits, with their biases.
 __global__ void __launch_bounds__(kRouteThreads)
 few_route_kernel(const Route a) {
     extern __shared__ __align__(16) float logits[];   // [T, E]
@@ -163,8 +163,7 @@ few_route_kernel(const Route a) {
             logits[i] = a.bias ? l + a.bias[i % a.E] : l;
         }
     }
-    for (int i = tid; i < a.columns; i += threads) a.arrived[i] = 0;
-    if (tid == 0) a.plan->done = 0;
+    if (tid < 2) a.plan->met[tid] = 0;
     __syncthreads();
     const auto take = [&](int t, int s, int id, bool changed) {
         if (a.mask && a.mask[s]) {
@@ -303,7 +302,6 @@ struct Args {
     __nv_bfloat16* h;         // [T*k, F of the first]
     float* part;              // y [ceil(F / 16), T*k, 16], F of the second, then summed into
     __nv_bfloat16* out;       // [T, F of the second]
-    int* arrived;             // per 16 output features: units done
     int T, E, k;
     int xrows, stages;        // the most rows of a chunk; depth of the ring
     int* err;
@@ -604,78 +602,66 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
     }
 }
 
-// One warp sums every token's rows of 16 features, in slot order: 4 lanes a token,
-// TP of 8 tokens each at a time with 4 slots' loads in flight.  (A block that falls
-// behind brings its columns' last units and has to sum them too: at 11 us for 64
-// tokens, one load at a time, it fell ever further behind, and the second product
-// took 211 us instead of 120.)
-template <int TP>
-__device__ __forceinline__ void sum_rows(const Args& a, const float* slot_w, const short* slot_row, const float* y, int f0) {
-    const int lane = threadIdx.x & 31, f = 4 * (lane & 3);
-    for (int t0 = lane >> 2; t0 < a.T; t0 += 8 * TP) {
-        float4 sum[TP];
-#pragma unroll
-        for (int i = 0; i < TP; ++i) sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+// All blocks wait here for each other, each with its two finishing warps, behind
+// what they have written; own == 0 waits for all the others'.
+__device__ __forceinline__ void meet(const Args& a, Ring& S, unsigned* arrived, int own) {
+    const int lane = threadIdx.x & 31;
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) atomicAdd(arrived, 1u);
+    if (own != 0) return;
+    const unsigned all = 2 * gridDim.x;
+    const uint64_t t0 = moe::global_timer_ns();
+    for (unsigned i = 1;; ++i) {
+        unsigned now;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(arrived) : "memory");
+        if (now >= all) break;
+        if ((i & 63u) == 0 && (S.abort_flag || moe::global_timer_ns() - t0 > kWaitNs)) {
+            if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
+            S.abort_flag = 1;
+            break;
+        }
+    }
+    __threadfence();
+}
+
+// This block's share of the tokens' sums: a thread takes 4 features of a token and
+// adds its slots' rows in their order, four loads on their way at a time.
+__device__ __forceinline__ void sum_rows(const Args& a, const float* slot_w, const short* slot_row) {
+    const int F = a.p[1].F, per = F / 4;
+    const int64_t rows_all = static_cast<int64_t>(a.T) * a.k, items = static_cast<int64_t>(a.T) * per;
+    const int64_t begin = items * blockIdx.x / gridDim.x, end = items * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
+        const int t = static_cast<int>(i / per), f = 4 * static_cast<int>(i - static_cast<int64_t>(t) * per);
+        const float* y = a.part + f / kRows * rows_all * kRows + f % kRows;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int j0 = 0; j0 < a.k; j0 += 4) {
-            float4 v[TP][4];
-            float w[TP][4];
+            float4 v[4];
+            float w[4];
 #pragma unroll
-            for (int i = 0; i < TP; ++i)
+            for (int j = 0; j < 4; ++j) {
+                const int s = t * a.k + j0 + j, row = j0 + j < a.k ? slot_row[s] : -1;
+                v[j] = row >= 0 ? __ldcg(reinterpret_cast<const float4*>(y + row * kRows)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                w[j] = row >= 0 ? slot_w[s] : 0.0f;
+            }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = t0 + 8 * i, s = t * a.k + j0 + j;
-                    const int row = t < a.T && j0 + j < a.k ? slot_row[s] : -1;
-                    v[i][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    w[i][j] = 0.0f;
-                    if (row >= 0) {
-                        v[i][j] = __ldcg(reinterpret_cast<const float4*>(y + row * kRows + f));
-                        w[i][j] = slot_w[s];
-                    }
-                }
-#pragma unroll
-            for (int i = 0; i < TP; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sum[i].x = fmaf(w[i][j], v[i][j].x, sum[i].x);
-                    sum[i].y = fmaf(w[i][j], v[i][j].y, sum[i].y);
-                    sum[i].z = fmaf(w[i][j], v[i][j].z, sum[i].z);
-                    sum[i].w = fmaf(w[i][j], v[i][j].w, sum[i].w);
-                }
+            for (int j = 0; j < 4; ++j) {
+                sum.x = fmaf(w[j], v[j].x, sum.x);
+                sum.y = fmaf(w[j], v[j].y, sum.y);
+                sum.z = fmaf(w[j], v[j].z, sum.z);
+                sum.w = fmaf(w[j], v[j].w, sum.w);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < TP; ++i) {
-            const int t = t0 + 8 * i;
-            if (t < a.T && f0 + f < a.p[1].F)
-                *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(t) * a.p[1].F + f0 + f) =
-                    make_uint2(moe::pack_bf16x2(sum[i].x, sum[i].y), moe::pack_bf16x2(sum[i].z, sum[i].w));
-        }
+        *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(t) * F + f) =
+            make_uint2(moe::pack_bf16x2(sum.x, sum.y), moe::pack_bf16x2(sum.z, sum.w));
     }
 }
 
 // One product on one of the two finishing warps: every other unit.
 template <bool FIRST, int NBMAX>
-__device__ __forceinline__ void finish(const Product& p, const Args& a, const Sums<NBMAX>* red, const float* slot_w, const short* slot_row,
-                                       int& count) {
+__device__ __forceinline__ void finish(const Product& p, const Args& a, const Sums<NBMAX>* red, int& count) {
     const int lane = threadIdx.x & 31, g = lane >> 2, own = (threadIdx.x >> 5) - kProduct, rows_all = a.T * a.k;
     const int chunks = chunks_of(a);
-    // Columns whose units have been stored but not yet counted, in lanes 0 to waiting - 1:
-    // a fence and an atomic take longer than a short unit.
-    constexpr int kWaiting = 4;
-    int column = 0, waiting = 0;
-    const auto count_in = [&]() {
-        __threadfence();
-        __syncwarp();
-        const bool last = lane < waiting && atomicAdd(&a.arrived[column], 1) == chunks - 1;
-        unsigned mine = __ballot_sync(0xffffffffu, last);
-        waiting = 0;
-        if (mine == 0) return;
-        __threadfence();
-#pragma unroll 1
-        for (; mine; mine &= mine - 1) {   // the last of this column's units sums every token's rows
-            const int f = __shfl_sync(0xffffffffu, column, __ffs(mine) - 1);
-            sum_rows<NBMAX == 1 ? 1 : 4>(a, slot_w, slot_row, a.part + static_cast<int64_t>(f) * rows_all * kRows, f * kRows);
-        }
-    };
     for (Run<FIRST> u(chunks, p.F); u.left > 0; u.next(), ++count) {
         const int turn = count & 1, f0 = u.f0();
         if (turn != own) continue;
@@ -708,11 +694,7 @@ __device__ __forceinline__ void finish(const Product& p, const Args& a, const Su
             }
         }
         bar_arrive(kEmpty + turn);
-        if (FIRST) continue;
-        if (lane == waiting) column = u.f;
-        if (++waiting == kWaiting) count_in();
     }
-    if (!FIRST && waiting) count_in();
 }
 
 // NBMAX: the most groups of 8 rows of a chunk (a.xrows <= 8 NBMAX).
@@ -740,7 +722,6 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     }
     moe::wait_for_primary();   // the plan
     __syncthreads();
-    const int chunks = chunks_of(a);
     if (warp == kProduct + 2) {
         int slot = 0;
         uint32_t turn = 0;
@@ -770,35 +751,15 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
             slot_w[s] = __ldcg(&a.plan->slot_w[s]);
             slot_row[s] = static_cast<short>(min(static_cast<int>(__ldcg(&a.plan->slot_row[s])), a.T * a.k - 1));
         }
-        asm volatile("bar.sync 6, 64;" ::: "memory");
         int count = 0;
-        finish<true, NBMAX>(a.p[0], a, red, slot_w, slot_row, count);
-        // every row of h is written before any is read
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) atomicAdd(&a.plan->done, 1u);
-        if (own == 0) {
-            const unsigned all = 2 * gridDim.x;
-            const uint64_t t0 = moe::global_timer_ns();
-            for (unsigned i = 1;; ++i) {
-                unsigned done;
-                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(done) : "l"(&a.plan->done) : "memory");
-                if (done >= all) break;
-                if ((i & 63u) == 0 && (S.abort_flag || moe::global_timer_ns() - t0 > kWaitNs)) {
-                    if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
-                    S.abort_flag = 1;
-                    break;
-                }
-            }
-            __threadfence();
-            bar_arrive(kReady);
-        }
-        finish<false, NBMAX>(a.p[1], a, red, slot_w, slot_row, count);
+        finish<true, NBMAX>(a.p[0], a, red, count);
+        meet(a, S, &a.plan->met[0], own);   // every row of h is written before any is read
+        if (own == 0) bar_arrive(kReady);
+        finish<false, NBMAX>(a.p[1], a, red, count);
+        meet(a, S, &a.plan->met[1], own);
     }
-    if (chunks == 0)   // no token has an expert
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < static_cast<int64_t>(a.T) * a.p[1].F;
-             i += static_cast<int64_t>(gridDim.x) * kThreads)
-            a.out[i] = __float2bfloat16_rn(0.0f);
+    __syncthreads();
+    sum_rows(a, slot_w, slot_row);
 }
 
 constexpr size_t kSmem = 227 * 1024, kLeastRing = 96 * 1024;
@@ -929,7 +890,7 @@ bool supported(const moe_forward_args* a) {
 }
 
 struct Layout {
-    size_t plan, arrived, h, part, total;
+    size_t plan, h, part, total;
 };
 
 Layout layout(const moe_forward_args* a) {
@@ -942,7 +903,6 @@ Layout layout(const moe_forward_args* a) {
     };
     const size_t rows = static_cast<size_t>(a->T) * a->k, columns = (a->H + kRows - 1) / kRows;
     l.plan = take(sizeof(Plan));
-    l.arrived = take(columns * sizeof(int));
     l.h = take(rows * a->I * 2);
     l.part = take(columns * rows * kRows * sizeof(float));
     l.total = off;
@@ -971,14 +931,10 @@ extern "C" moe_status_t moe_forward_few(const moe_forward_args* a, void* ws, siz
     int* err = moe::device_error_word();
     if (!err) return MOE_ERR_CUDA;
     auto* base = static_cast<uint8_t*>(ws);
-    const int columns = (a->H + kRows - 1) / kRows;
     auto* plan = reinterpret_cast<Plan*>(base + l.plan);
-    auto* arrived = reinterpret_cast<int*>(base + l.arrived);
-    const Route r{a->logits, a->expert_bias, a->sentinel_mask, a->topk_ids, a->topk_w, a->T,   a->E,
-                  a->k,      a->renormalize, 0,                plan,        arrived,   columns, err};
+    const Route r{a->logits, a->expert_bias, a->sentinel_mask, a->topk_ids, a->topk_w, a->T, a->E, a->k, a->renormalize, 0, plan, err};
     Args args{};
     args.plan = plan;
-    args.arrived = arrived;
     args.h = reinterpret_cast<__nv_bfloat16*>(base + l.h);
     args.part = reinterpret_cast<float*>(base + l.part);
     args.out = static_cast<__nv_bfloat16*>(a->out);
