@@ -30,7 +30,8 @@
 // 128 columns is multiplied by their block's scale in fp32.  x and h are not
 // quantised: it would save no weight bytes, and cost accuracy.
 //
-// h is rounded to bf16, the type of the MMA's operand.  The second product leaves
+// h is rounded once, to the MMA's operand: to bf16, or from fp32 to the scaled fp16
+// (8 and 11 significant bits).  The second product leaves
 // fp32 rows y; when all blocks are done each sums its share of the tokens' rows, in
 // slot order, and rounds once.  (Sums by whichever block brought the last of a
 // column's units fell to those that were behind already: 292 us instead of REPLACE64
@@ -275,9 +276,17 @@ __device__ __forceinline__ int scale_exponent(int bits) {
     const int e = bits >> 7;
     return e == 255 || bits == 0 ? 0 : min(141 - max(e, 1), 126);
 }
-__device__ __forceinline__ uint32_t scaled_f16x2(uint32_t two, float f) {
-    const __half2 h = __floats2half2_rn(moe::bf16_lo(two) * f, moe::bf16_hi(two) * f);
+__device__ __forceinline__ uint32_t scaled_f16x2(float lo, float hi, float f) {
+    const __half2 h = __floats2half2_rn(lo * f, hi * f);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The largest magnitude of 8 bf16, or of 4 fp32 cut to bf16, as bits.
+__device__ __forceinline__ int largest_bf16(uint4 v) {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    return static_cast<int>(max(m & 0xFFFFu, m >> 16));
+}
+__device__ __forceinline__ int largest_f32(uint4 v) {
+    return static_cast<int>(max(max(v.x & 0x7FFFFFFFu, v.y & 0x7FFFFFFFu), max(v.z & 0x7FFFFFFFu, v.w & 0x7FFFFFFFu)) >> 16);
 }
 
 // The weights' tiles: `whole` copies kTiles of them at once, [tile][row][128 bytes] in
@@ -289,7 +298,7 @@ struct Maps {
 
 // One of the two products, y = W x, for all experts.
 struct Product {
-    const __nv_bfloat16* x;   // [rows, K]: x [T, K], or h [T*k, K]
+    const void* x;            // [rows, K]: x [T, K], or h [T*k, K] (FP8: fp32)
     const float* scales;      // FP8: a scale per 128 x 128 block of W
     int K, F;                 // columns and features of W: [E, 2F, K] (first) or [E, F, K]
     int whole;                // columns in whole tiles
@@ -299,7 +308,7 @@ struct Product {
 struct Args {
     Product p[2];
     Plan* plan;
-    __nv_bfloat16* h;         // [T*k, F of the first]
+    void* h;                  // [T*k, F of the first]
     float* part;              // y [ceil(F / 16), T*k, 16], F of the second, then summed into
     __nv_bfloat16* out;       // [T, F of the second]
     int T, E, k;
@@ -424,6 +433,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
     const int g = lane >> 2, c = lane & 3;
     constexpr int kXRow = FP8 ? 2 * kRowBytes : kRowBytes;   // of a tile's columns of a row of x
     constexpr int kVectors = kXRow / 16;
+    constexpr bool kWide = FP8 && !FIRST;   // h in fp32
     const int mine = p.steps / 2;                             // this warp's steps of a unit
     uint8_t* const xs = xcols + static_cast<size_t>(warp) * mine * a.xrows * kXRow;
     // Tiles are swizzled: vector j of row r is at j ^ (r mod 8).  Lane l takes vectors
@@ -447,23 +457,23 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
     // This warp's columns of the chunk's rows of x: [step][row][half][8 vectors], swizzled
     // like the tiles; an FP8 vector of weights meets two of x, the halves.  FP8: scaled
     // by a power of two per row to at most 2^15 and held in fp16, which loses nothing of
-    // a bf16 within 2^29 of the largest, and of the others less than 2^-39 of that; a
-    // row with infinities or NaN is not scaled.  A few rows, two vectors each, on their
+    // a bf16 within 2^29 of the largest, and of the others less than 2^-39 of that; h, in
+    // fp32, is rounded to its 11 bits.  A row with infinities or NaN is not scaled.  A few rows, two vectors each, on their
     // way at a time; FP8 looks at them once for the scale and once to convert them.
     const auto take_x = [&]() {
-        constexpr int NR = NBMAX == 1 ? 2 : 4, NV = 2;
+        constexpr int NW = kWide ? 2 : 1, NR = NBMAX == 1 ? 2 : 4, NV = 2 / NW;
         const int vectors = mine * kVectors;
         __syncwarp();
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += NR) {
             const uint4* from[NR];
-            int bits[NR];   // the largest magnitude, in bf16
+            int bits[NR];   // the largest magnitude's upper half, as a bf16
             float f[NR];
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
                 const int r = min(r0 + j, rows - 1);
                 const int row = FIRST ? (r ? min(a.plan->token[row0 + r], a.T - 1) : token0) : row0 + r;
-                from[j] = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(row) * p.K);
+                from[j] = static_cast<const uint4*>(p.x) + static_cast<int64_t>(row) * (p.K / 8) * NW;
                 bits[j] = 0;
             }
 #pragma unroll 1
@@ -477,14 +487,16 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
                     }
 #pragma unroll 1
                 for (int i0 = lane; i0 < vectors; i0 += 32 * NV) {
-                    uint4 v[NR][NV];
+                    uint4 v[NR][NV][NW];
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         const int at = i0 + 32 * i, step = 2 * (at / kVectors) + half;
                         const int k = (step < p.whole_steps ? step * kColumns<FP8> : p.whole) + tile * kTileColumns<FP8> + 8 * (at % kVectors);
                         const bool in = at < vectors && k < (step < p.whole_steps ? p.whole : p.K);
 #pragma unroll
-                        for (int j = 0; j < NR; ++j) v[j][i] = in ? from[j][k / 8] : make_uint4(0, 0, 0, 0);
+                        for (int j = 0; j < NR; ++j)
+#pragma unroll
+                            for (int w = 0; w < NW; ++w) v[j][i][w] = in ? from[j][k / 8 * NW + w] : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
@@ -492,12 +504,18 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
 #pragma unroll
                         for (int j = 0; j < NR; ++j) {
                             const int r = r0 + j;
-                            uint4 t = v[j][i];
+                            uint4 t = v[j][i][0];
                             if (look == 0) {
-                                const uint32_t m = __vmaxu2(__vmaxu2(t.x & 0x7FFF7FFFu, t.y & 0x7FFF7FFFu), __vmaxu2(t.z & 0x7FFF7FFFu, t.w & 0x7FFF7FFFu));
-                                bits[j] = max(bits[j], static_cast<int>(max(m & 0xFFFFu, m >> 16)));
+                                bits[j] = max(bits[j], kWide ? max(largest_f32(t), largest_f32(v[j][i][NW - 1])) : largest_bf16(t));
                             } else if (at < vectors && r < rows) {
-                                if (FP8) t = make_uint4(scaled_f16x2(t.x, f[j]), scaled_f16x2(t.y, f[j]), scaled_f16x2(t.z, f[j]), scaled_f16x2(t.w, f[j]));
+                                if (kWide) {
+                                    const uint4 u = v[j][i][NW - 1];
+                                    t = make_uint4(scaled_f16x2(__uint_as_float(t.x), __uint_as_float(t.y), f[j]), scaled_f16x2(__uint_as_float(t.z), __uint_as_float(t.w), f[j]),
+                                                   scaled_f16x2(__uint_as_float(u.x), __uint_as_float(u.y), f[j]), scaled_f16x2(__uint_as_float(u.z), __uint_as_float(u.w), f[j]));
+                                } else if (FP8) {
+                                    t = make_uint4(scaled_f16x2(moe::bf16_lo(t.x), moe::bf16_hi(t.x), f[j]), scaled_f16x2(moe::bf16_lo(t.y), moe::bf16_hi(t.y), f[j]),
+                                                   scaled_f16x2(moe::bf16_lo(t.z), moe::bf16_hi(t.z), f[j]), scaled_f16x2(moe::bf16_lo(t.w), moe::bf16_hi(t.w), f[j]));
+                                }
                                 const int to = FP8 ? (q & 1) * kRowBytes + ((q / 2) ^ (r & 7)) * 16 : (q ^ (r & 7)) * 16;
                                 *reinterpret_cast<uint4*>(xs + ((at / kVectors) * a.xrows + r) * kXRow + to) = t;
                             }
@@ -658,7 +676,7 @@ __device__ __forceinline__ void sum_rows(const Args& a, const float* slot_w, con
 }
 
 // One product on one of the two finishing warps: every other unit.
-template <bool FIRST, int NBMAX>
+template <bool FP8, bool FIRST, int NBMAX>
 __device__ __forceinline__ void finish(const Product& p, const Args& a, const Sums<NBMAX>* red, int& count) {
     const int lane = threadIdx.x & 31, g = lane >> 2, own = (threadIdx.x >> 5) - kProduct, rows_all = a.T * a.k;
     const int chunks = chunks_of(a);
@@ -683,9 +701,11 @@ __device__ __forceinline__ void finish(const Product& p, const Args& a, const Su
                 const int row = 8 * b + 2 * (lane & 3) + j;
                 if (row >= chunk.z) continue;
                 if (FIRST) {
-                    if (f0 + g < p.F)
-                        a.h[static_cast<int64_t>(chunk.y + row) * p.F + f0 + g] =
-                            __float2bfloat16_rn(top[j] / (1.0f + expf(-top[j])) * bottom[j]);
+                    const float h = top[j] / (1.0f + expf(-top[j])) * bottom[j];
+                    const int64_t at = static_cast<int64_t>(chunk.y + row) * p.F + f0 + g;
+                    if (f0 + g >= p.F) continue;
+                    if (FP8) static_cast<float*>(a.h)[at] = h;
+                    else static_cast<__nv_bfloat16*>(a.h)[at] = __float2bfloat16_rn(h);
                 } else {
                     float* y = a.part + (static_cast<int64_t>(u.f) * rows_all + chunk.y + row) * kRows;
                     y[g] = top[j];
@@ -752,10 +772,10 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
             slot_row[s] = static_cast<short>(min(static_cast<int>(__ldcg(&a.plan->slot_row[s])), a.T * a.k - 1));
         }
         int count = 0;
-        finish<true, NBMAX>(a.p[0], a, red, count);
+        finish<FP8, true, NBMAX>(a.p[0], a, red, count);
         meet(a, S, &a.plan->met[0], own);   // every row of h is written before any is read
         if (own == 0) bar_arrive(kReady);
-        finish<false, NBMAX>(a.p[1], a, red, count);
+        finish<FP8, false, NBMAX>(a.p[1], a, red, count);
         meet(a, S, &a.plan->met[1], own);
     }
     __syncthreads();
@@ -767,7 +787,7 @@ constexpr size_t kSmem = 227 * 1024, kLeastRing = 96 * 1024;
 constexpr size_t kLightSmem = 2 * kMaxE * 4 + kMaxE * 4 + kMaxSlots * 2 + kLight * kMaxE * 4 + 64 + 1024;
 
 template <bool FP8>
-Product product(const __nv_bfloat16* x, const float* scales, int K, int F) {
+Product product(const void* x, const float* scales, int K, int F) {
     Product p{x, scales, K, F, K / kTileColumns<FP8> * kTileColumns<FP8>, 0, 0};
     p.whole_steps = (p.whole + kColumns<FP8> - 1) / kColumns<FP8>;
     p.steps = (p.whole_steps + (p.whole < K) + 1) / 2 * 2;
@@ -870,7 +890,7 @@ moe_status_t launch(const moe_forward_args* f, Route r, Args a, const Maps& m1, 
 
 template <bool FP8>
 moe_status_t run(const moe_forward_args* f, const Route& r, Args a, cudaStream_t s) {
-    a.p[0] = product<FP8>(static_cast<const __nv_bfloat16*>(f->x), f->W1_scales, f->H, f->I);
+    a.p[0] = product<FP8>(f->x, f->W1_scales, f->H, f->I);
     a.p[1] = product<FP8>(a.h, f->W2_scales, f->I, f->H);
     Maps m1, m2;
     if (!weight_maps(&m1, FP8, true, f->W1, f->E, f->I, f->H) || !weight_maps(&m2, FP8, false, f->W2, f->E, f->H, f->I)) return MOE_ERR_CUDA;
@@ -903,7 +923,7 @@ Layout layout(const moe_forward_args* a) {
     };
     const size_t rows = static_cast<size_t>(a->T) * a->k, columns = (a->H + kRows - 1) / kRows;
     l.plan = take(sizeof(Plan));
-    l.h = take(rows * a->I * 2);
+    l.h = take(rows * a->I * (a->dtype == MOE_FP8_E4M3_B128 ? 4 : 2));
     l.part = take(columns * rows * kRows * sizeof(float));
     l.total = off;
     return l;
@@ -935,7 +955,7 @@ extern "C" moe_status_t moe_forward_few(const moe_forward_args* a, void* ws, siz
     const Route r{a->logits, a->expert_bias, a->sentinel_mask, a->topk_ids, a->topk_w, a->T, a->E, a->k, a->renormalize, 0, plan, err};
     Args args{};
     args.plan = plan;
-    args.h = reinterpret_cast<__nv_bfloat16*>(base + l.h);
+    args.h = base + l.h;
     args.part = reinterpret_cast<float*>(base + l.part);
     args.out = static_cast<__nv_bfloat16*>(a->out);
     args.T = a->T, args.E = a->E, args.k = a->k;

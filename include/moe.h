@@ -640,13 +640,14 @@ moe_status_t moe_forward(const moe_forward_args* args, void* ws, size_t ws_bytes
 
 /*
  * moe_forward_few -- moe_forward for a few tokens: generating a token at a time
- * for each sequence of a batch.  Two kernels in all: routing, permutation and
- * the weighted sum take none of their own, and the weights of the experts that
+ * for each sequence of a batch.  Two kernels in all, one for the routing and one
+ * (a cooperative launch) for everything else; the weights of the experts that
  * some token picked are streamed once.  Same arguments and routing as
  * moe_forward; out[t] = sum over j of topk_w[t, j] * W2[e] h in fp32, in slot
- * order, rounded to bf16 once, h = silu(g) * u rounded to bf16.
+ * order, rounded to bf16 once; h = silu(g) * u is rounded to bf16 in between, and
+ * for FP8 to 11 bits.
  * MOE_FP8_E4M3_B128: the weights are e4m3 with block scales as in moe_forward,
- * but x and h stay bf16 (moe_forward quantises both), so the results lie
+ * but x and h are not quantised (as moe_forward's are), so the results lie
  * closer to the unquantised layer's than moe_forward's do.
  * Results do not equal moe_forward's bit for bit (it rounds each expert's rows to
  * bf16 before it sums them).  A token without live slots gets a zero row.  ids
