@@ -83,6 +83,7 @@ _SIGS = {
     "moe_cross_entropy_backward": (_S, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
     "moe_swiglu": (_S, [_P, _P, _I, _I, _I, _P, _P]),
     "moe_combine": (_S, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_sample": (_S, [_I, _P, _L, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_forward_workspace_size": (_Z, [C.POINTER(ForwardArgs)]),
     "moe_forward": (_S, [C.POINTER(ForwardArgs), _P, _Z, _P]),
     "moe_forward_few_workspace_size": (_Z, [C.POINTER(ForwardArgs)]),
@@ -349,6 +350,11 @@ def moe_forward_few_workspace_size(args: ForwardArgs) -> int:
 
 def moe_forward_few(args: ForwardArgs, ws, ws_bytes, stream=None):
     _check(lib().moe_forward_few(C.byref(args), _p(ws), ws_bytes, _stream(stream)), "moe_forward_few")
+
+
+def moe_sample(dtype, logits, ld, rows, V, temperature, top_k, top_p, min_p, u, token, logprob, stream=None):
+    _check(lib().moe_sample(dtype, _p(logits), ld, rows, V, _p(temperature), _p(top_k), _p(top_p), _p(min_p), _p(u),
+                            _p(token), _p(logprob), _stream(stream)), "moe_sample")
 
 
 # ---------------------------------------------------------------- torch helpers

@@ -80,7 +80,7 @@ typedef enum {
     MOE_BF16 = 0,          /* bf16 operands, fp32 accumulation */
     MOE_FP8_E4M3_B128 = 1, /* e4m3 operands; activations scaled per row per 128
                               columns, weights per 128x128 block; fp32 scales */
-    MOE_F32 = 2            /* fp32 (layer norm only) */
+    MOE_F32 = 2            /* fp32 (layer norm and sampling only) */
 } moe_dtype_t;
 
 typedef enum {
@@ -659,6 +659,38 @@ moe_status_t moe_forward(const moe_forward_args* args, void* ws, size_t ws_bytes
 size_t moe_forward_few_workspace_size(const moe_forward_args* args);
 moe_status_t moe_forward_few(const moe_forward_args* args, void* ws, size_t ws_bytes,
                              moe_stream_t stream);
+
+/*
+ * moe_sample -- the token that each row of logits gives, behind the layer and the
+ * vocabulary's product: temperature, top-k, top-p and min-p by row, drawn with a
+ * given uniform number.  Per row, with L the largest logit, w_i = exp((l_i - L) /
+ * temperature) and the tokens in the order of (logit descending, index
+ * ascending):
+ *   top-k  keeps the first top_k tokens (top_k <= 0 or >= V: all);
+ *   top-p  of these the shortest prefix whose sum of w is at least top_p times
+ *          that of all of these, the first token at least (top_p >= 1: all);
+ *   min-p  those with w_i >= min_p (above 1: as 1; <= 0: all).
+ * token is the first kept one, in the order of the vocabulary, at which the
+ * running sum of the kept w exceeds u times their sum; logprob the logarithm of
+ * its w over that sum.  Sums are exact to some 2^-37, so that tokens are those of
+ * the definition but where u falls that close to a boundary.
+ * temperature below 2^-126 (0, say) or NaN: the first token of the order
+ * (greedy), logprob 0.
+ * Logits of -infinity or NaN are never drawn; of +infinity, only they are, with
+ * equal weights.  A row without any other than -infinity and NaN gets token -1
+ * and logprob -infinity.  u below 0 or NaN is taken as 0, above as just below 1.
+ * dtype  MOE_BF16 or MOE_F32: logits [rows, V], row r at logits + r * ld elements
+ *        (ld >= V), aligned to their element; rows that start on 16-byte
+ *        boundaries move faster.
+ * temperature, top_p, min_p fp32 [rows], top_k int32 [rows]; each may be NULL:
+ *        temperature 1, no filter.  u fp32 [rows].
+ * token  int32 [rows];  logprob fp32 [rows] or NULL.
+ * Limits: rows >= 1, V >= 1; V <= 327680 and rows <= 2^27 (else
+ * MOE_ERR_UNSUPPORTED).  No workspace.
+ */
+moe_status_t moe_sample(moe_dtype_t dtype, const void* logits, int64_t ld, int rows, int V, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
+                        float* logprob, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
