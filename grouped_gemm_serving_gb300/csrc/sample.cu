@@ -23,6 +23,8 @@
 // draw its neighbour.
 #include <cooperative_groups.h>
 
+#include <climits>
+
 #include "common.cuh"
 
 namespace {
@@ -35,6 +37,8 @@ constexpr int kBins = 2048;
 constexpr int kBinsPerOctave = 32;   // of the first histogram: 64 octaves below the largest weight
 constexpr int kSorted = 1024;        // tokens that one block sorts
 constexpr int kMaxBlocks = 8;        // of a cluster
+constexpr int kGroups = kThreads / 8;
+constexpr int kFew = 256;            // the largest top-k whose tokens are looked for by the groups' largest
 constexpr int kMaxV = 327680;        // 40960 tokens a block: 160 KB in fp32
 
 struct Args {
@@ -105,55 +109,121 @@ struct Weight {
 // A token's place in the order, larger first: its logit's key, then its index.
 __device__ __forceinline__ uint64_t place_of(float l, int i) { return static_cast<uint64_t>(moe::order_key(l)) << 32 | static_cast<uint32_t>(~i); }
 
+// Sixteen bytes of logits.
 template <typename T>
-struct Slice;
+struct Vec;
 template <>
-struct Slice<float> {
-    static constexpr int kVec = 4;
-    __device__ static __forceinline__ void get(const void* s, int v, float (&l)[4]) {
-        const float4 x = static_cast<const float4*>(s)[v];
-        l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w;
+struct Vec<float> {
+    static constexpr int kSize = 4;
+    uint4 v;
+    __device__ __forceinline__ void unpack(float (&l)[4]) const {
+        l[0] = __uint_as_float(v.x), l[1] = __uint_as_float(v.y), l[2] = __uint_as_float(v.z), l[3] = __uint_as_float(v.w);
     }
-    __device__ static __forceinline__ void put(void* s, int v, const float (&l)[4]) { static_cast<float4*>(s)[v] = make_float4(l[0], l[1], l[2], l[3]); }
-    __device__ static __forceinline__ float value(float x) { return x; }
+    __device__ __forceinline__ void clean() {   // NaN: never drawn
+        v.x = __float_as_uint(fmaxf(__uint_as_float(v.x), -INFINITY));
+        v.y = __float_as_uint(fmaxf(__uint_as_float(v.y), -INFINITY));
+        v.z = __float_as_uint(fmaxf(__uint_as_float(v.z), -INFINITY));
+        v.w = __float_as_uint(fmaxf(__uint_as_float(v.w), -INFINITY));
+    }
+    __device__ __forceinline__ float largest() const {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    __device__ __forceinline__ void load(const float* from, int n) {   // the first n; -infinity behind them
+        const uint32_t none = 0xFF800000u;
+        v.x = n > 0 ? __float_as_uint(from[0]) : none;
+        v.y = n > 1 ? __float_as_uint(from[1]) : none;
+        v.z = n > 2 ? __float_as_uint(from[2]) : none;
+        v.w = n > 3 ? __float_as_uint(from[3]) : none;
+    }
 };
 template <>
-struct Slice<__nv_bfloat16> {
-    static constexpr int kVec = 8;
-    __device__ static __forceinline__ void get(const void* s, int v, float (&l)[8]) {
-        const uint4 x = static_cast<const uint4*>(s)[v];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+struct Vec<__nv_bfloat16> {
+    static constexpr int kSize = 8;
+    uint4 v;
+    __device__ __forceinline__ void unpack(float (&l)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             l[2 * i] = moe::bf16_lo(w[i]);
             l[2 * i + 1] = moe::bf16_hi(w[i]);
         }
     }
-    __device__ static __forceinline__ void put(void* s, int v, const float (&l)[8]) {   // values of bf16: cut in half
+    __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    __device__ __forceinline__ void clean() {
+        const uint32_t none = 0xFF80FF80u;
+        v = make_uint4(max2(v.x, none), max2(v.y, none), max2(v.z, none), max2(v.w, none));
+    }
+    __device__ __forceinline__ float largest() const {
+        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+        return fmaxf(moe::bf16_lo(m), moe::bf16_hi(m));
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16* from, int n) {
+        const auto* raw = reinterpret_cast<const uint16_t*>(from);
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(l[2 * i]), __float_as_uint(l[2 * i + 1]), 0x7632);
-        static_cast<uint4*>(s)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = 2 * i < n ? raw[2 * i] : 0xFF80u, hi = 2 * i + 1 < n ? raw[2 * i + 1] : 0xFF80u;
+            w[i] = lo | hi << 16;
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ static __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
 };
 
 struct Shared {
-    uint32_t n[kBins], lo[kBins], hi[kBins];   // histogram: tokens, and their weights in two halves
+    uint32_t lo[kBins], hi[kBins];   // histogram: weights, or ones, in two halves
     uint64_t list[kSorted];
     uint64_t powers[64];
     uint64_t warp[kWarps];
     uint64_t best[kMaxBlocks], total[kMaxBlocks];   // every block's, written by them
-    uint64_t found[3];                                // written by the block that found it
+    uint64_t found[2];                                // written by the block that found it
     uint32_t listed;
+    uint32_t key[kGroups];                            // the largest key of every 8 lanes
+    uint32_t group[kMaxBlocks * kGroups];             // every block's, written by them
+    uint32_t bound;
 };
+
+// Sorts size (a power of two) places, larger first, by the whole block.
+__device__ __noinline__ void sort_places(uint64_t* list, int size) {
+    for (int block = 2; block <= size; block *= 2)   // bitonic
+        for (int step = block / 2; step > 0; step /= 2) {
+            for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+                const int x = 2 * step * (i / step) + i % step, y = x + step;
+                const uint64_t p0 = list[x], p1 = list[y];
+                if ((p0 < p1) == ((x & block) == 0)) {
+                    list[x] = p1;
+                    list[y] = p0;
+                }
+            }
+            __syncthreads();
+        }
+}
+__device__ __forceinline__ int padded(int n) { return n <= 32 ? 32 : 1 << (32 - __clz(n - 1)); }
+
+// Running sums of two numbers a thread over the block: returns the sum up to and with
+// b.  warps: kWarps words.
+__device__ __noinline__ uint64_t running(uint64_t a, uint64_t b, uint64_t* warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t sum = a + b;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = sum;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) sum += warps[i];
+    return sum;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const Args a) {
-    using S = Slice<T>;
-    constexpr int kVec = S::kVec;
-    extern __shared__ __align__(16) uint8_t slice[];
+    constexpr int kVec = Vec<T>::kSize;
+    extern __shared__ uint4 slice[];
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -164,36 +234,48 @@ sample_kernel(const Args a) {
     const int v_begin = min(vectors, warp * each), v_end = min(vectors, v_begin + each);
     const auto remote = [&](auto* p, int r) { return cluster.map_shared_rank(p, r); };
 
-    // ---- the row into shared memory; the largest logit and its first place
-    uint64_t best = 0;
+    // ---- the row into shared memory; the largest logit and its first place, and the
+    // largest of every 8 lanes' tokens
+    uint64_t best;
     {
         const T* from = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.ld;
         const bool aligned = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
+        float most = -INFINITY;
+        int at = v_begin + lane;   // the vector that has it first
+#pragma unroll 4
         for (int v = v_begin + lane; v < v_end; v += 32) {
             const int i = i0 + v * kVec;
-            float l[kVec];
-            if (aligned && i + kVec <= a.V) {
-                S::get(from + i, 0, l);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) l[j] = i + j < a.V ? S::value(from[i + j]) : -INFINITY;
+            Vec<T> x;
+            if (aligned && i + kVec <= a.V) x.v = *reinterpret_cast<const uint4*>(from + i);
+            else x.load(from + i, a.V - i);
+            x.clean();
+            slice[v] = x.v;
+            const float m = x.largest();
+            if (m > most) {
+                most = m;
+                at = v;
             }
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                if (l[j] != l[j]) l[j] = -INFINITY;   // NaN: never drawn
-                const uint64_t p = place_of(l[j], i + j);
-                best = p > best ? p : best;
-            }
-            S::put(slice, v, l);
         }
+        uint32_t key = moe::order_key(most);
         if (tid < 64) sh.powers[tid] = kPowers[tid];
+        // the warp's first token with its largest logit
+        const uint32_t top_key = __reduce_max_sync(0xffffffffu, key);
+        int first = INT_MAX;
+        if (key == top_key && at < v_end) {
+            float l[kVec];
+            Vec<T>{slice[at]}.unpack(l);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const uint64_t o = __shfl_xor_sync(0xffffffffu, best, off);
-            best = o > best ? o : best;
+            for (int j = kVec - 1; j >= 0; --j)
+                if (moe::order_key(l[j]) == key) first = i0 + at * kVec + j;
         }
-        if (lane == 0) sh.warp[warp] = best;
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (lane == 0) sh.warp[warp] = static_cast<uint64_t>(top_key) << 32 | static_cast<uint32_t>(~first);
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
+        if ((lane & 7) == 0) sh.key[tid / 8] = key;
+        if (tid == 0) sh.listed = 0;
         __syncthreads();
+        for (int i = tid; i < blocks * kGroups; i += kThreads) *remote(&sh.group[rank * kGroups + i % kGroups], i / kGroups) = sh.key[i % kGroups];
         if (tid < blocks) {
             best = sh.warp[0];
             for (int i = 1; i < kWarps; ++i) best = sh.warp[i] > best ? sh.warp[i] : best;
@@ -226,7 +308,7 @@ sample_kernel(const Args a) {
         uint64_t mine = 0;
         for (int v = v_begin + lane; v < v_end; v += 32) {
             float l[kVec];
-            S::get(slice, v, l);
+            Vec<T>{slice[v]}.unpack(l);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) mine += fn(l[j], i0 + v * kVec + j);
         }
@@ -257,7 +339,7 @@ sample_kernel(const Args a) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j) l[j] = -INFINITY, w[j] = 0;
             if (v + lane < v_end) {
-                S::get(slice, v + lane, l);
+                Vec<T>{slice[v + lane]}.unpack(l);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     w[j] = fn(l[j], i0 + (v + lane) * kVec + j);
@@ -286,11 +368,13 @@ sample_kernel(const Args a) {
         }
     };
 
+    const auto listed_weight = [&](int i) { return weight(moe::key_value(static_cast<uint32_t>(sh.list[i] >> 32))); };
+
     // The token at which the sum in the order reaches a target: the place of the
     // last one kept.  Among the tokens at or before `cut` in the order; by_weight: the
     // target is the share p of their weights, else the number k.
     const auto cut_at = [&](uint64_t cut, bool by_weight, int k, float p) {
-        uint64_t target = static_cast<uint64_t>(k), above = 0, in_bin;
+        uint64_t target = static_cast<uint64_t>(k), above = 0;
         uint32_t low = 0, high = 0;   // keys of the bin, once known
         int shift = -1;               // -1: the first histogram, of distances to the largest
         const float scale = static_cast<float>(c) * kBinsPerOctave;
@@ -303,36 +387,31 @@ sample_kernel(const Args a) {
                 const uint32_t key = static_cast<uint32_t>(place >> 32);
                 return place >= cut && (shift < 0 || (key >= low && key <= high));
             };
-            for (int i = tid; i < kBins; i += kThreads) sh.n[i] = sh.lo[i] = sh.hi[i] = 0;
+            for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
             __syncthreads();
             for (int v = v_begin + lane; v < v_end; v += 32) {
                 float l[kVec];
-                S::get(slice, v, l);
+                Vec<T>{slice[v]}.unpack(l);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     const uint64_t place = place_of(l[j], i0 + v * kVec + j);
                     if (!inside(place)) continue;
+                    const uint64_t w = by_weight ? weight(l[j]) : 1;
+                    if (w == 0) continue;
                     const int bin = bin_of(l[j], static_cast<uint32_t>(place >> 32));
-                    atomicAdd(&sh.n[bin], 1u);
-                    if (by_weight) {
-                        const uint64_t w = weight(l[j]);
-                        const uint32_t w_lo = static_cast<uint32_t>(w);
-                        uint32_t w_hi = static_cast<uint32_t>(w >> 32);
-                        if (w_lo && atomicAdd(&sh.lo[bin], w_lo) + w_lo < w_lo) ++w_hi;   // carry
-                        if (w_hi) atomicAdd(&sh.hi[bin], w_hi);
-                    }
+                    const uint32_t w_lo = static_cast<uint32_t>(w);
+                    uint32_t w_hi = static_cast<uint32_t>(w >> 32);
+                    if (w_lo && atomicAdd(&sh.lo[bin], w_lo) + w_lo < w_lo) ++w_hi;   // carry
+                    if (w_hi) atomicAdd(&sh.hi[bin], w_hi);
                 }
             }
             cluster.sync();
             // this block's share of the bins, over all blocks; running sums over them
             const int per = kBins / blocks;   // at most kThreads
-            uint64_t n = 0, w = 0;
+            uint64_t mine = 0;
             if (tid < per)
-                for (int r = 0; r < blocks; ++r) {
-                    n += *remote(&sh.n[rank * per + tid], r);
-                    if (by_weight) w += static_cast<uint64_t>(*remote(&sh.hi[rank * per + tid], r)) * 4294967296ull + *remote(&sh.lo[rank * per + tid], r);
-                }
-            const uint64_t mine = by_weight ? w : n;
+                for (int r = 0; r < blocks; ++r)
+                    mine += static_cast<uint64_t>(*remote(&sh.hi[rank * per + tid], r)) * 4294967296ull + *remote(&sh.lo[rank * per + tid], r);
             uint64_t upto = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -361,66 +440,42 @@ sample_kernel(const Args a) {
                     uint64_t* to = remote(&sh.found[0], r);
                     to[0] = static_cast<uint64_t>(rank * per + tid);
                     to[1] = before + upto - mine;
-                    to[2] = n;
                 }
             if (tid == 0) sh.listed = 0;
             cluster.sync();
             const int bin = static_cast<int>(sh.found[0]);
             above = sh.found[1];
-            in_bin = sh.found[2];
-            const auto in_this = [&](float l, uint64_t place) { return inside(place) && bin_of(l, static_cast<uint32_t>(place >> 32)) == bin; };
-            if (in_bin <= kSorted) {   // the first block sorts them
-                for (int v = v_begin + lane; v < v_end; v += 32) {
-                    float l[kVec];
-                    S::get(slice, v, l);
+            const auto in_this = [&](float l, uint64_t place) {
+                return inside(place) && bin_of(l, static_cast<uint32_t>(place >> 32)) == bin && (!by_weight || weight(l) != 0);
+            };
+            // those in it are listed, if they are few, and sorted by the first block
+            for (int v = v_begin + lane; v < v_end; v += 32) {
+                float l[kVec];
+                Vec<T>{slice[v]}.unpack(l);
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        const uint64_t place = place_of(l[j], i0 + v * kVec + j);
-                        if (in_this(l[j], place)) {
-                            const uint32_t at = atomicAdd(remote(&sh.listed, 0), 1u);
-                            if (at < kSorted) *remote(&sh.list[at], 0) = place;
-                        }
+                for (int j = 0; j < kVec; ++j) {
+                    const uint64_t place = place_of(l[j], i0 + v * kVec + j);
+                    if (in_this(l[j], place)) {
+                        const uint32_t at = atomicAdd(remote(&sh.listed, 0), 1u);
+                        if (at < kSorted) *remote(&sh.list[at], 0) = place;
                     }
                 }
-                cluster.sync();
+            }
+            cluster.sync();
+            const uint32_t in_bin = *remote(&sh.listed, 0);
+            if (in_bin <= kSorted) {
                 if (rank == 0) {
-                    int size = 32;
-                    while (size < static_cast<int>(in_bin)) size *= 2;
-                    for (int i = tid; i < size; i += kThreads)
-                        if (i >= static_cast<int>(in_bin)) sh.list[i] = 0;
+                    const int n = static_cast<int>(in_bin), size = padded(n);
+                    for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
                     __syncthreads();
-                    for (int block = 2; block <= size; block *= 2)   // bitonic, larger first
-                        for (int step = block / 2; step > 0; step /= 2) {
-                            for (int i = tid; i < size / 2; i += kThreads) {
-                                const int x = 2 * step * (i / step) + i % step, y = x + step;
-                                const uint64_t p0 = sh.list[x], p1 = sh.list[y];
-                                if ((p0 < p1) == ((x & block) == 0)) {
-                                    sh.list[x] = p1;
-                                    sh.list[y] = p0;
-                                }
-                            }
-                            __syncthreads();
-                        }
+                    sort_places(sh.list, size);
                     if (!by_weight) {
                         if (tid == 0) sh.found[0] = sh.list[target - above - 1];
                     } else {
-                        // two tokens a thread
-                        uint64_t first = 0, second = 0;
-                        const int at = 2 * tid;
-                        if (at < static_cast<int>(in_bin)) first = weight(moe::key_value(static_cast<uint32_t>(sh.list[at] >> 32)));
-                        if (at + 1 < static_cast<int>(in_bin)) second = weight(moe::key_value(static_cast<uint32_t>(sh.list[at + 1] >> 32)));
-                        uint64_t sum = first + second;
-#pragma unroll
-                        for (int off = 1; off < 32; off <<= 1) {
-                            const uint64_t o = __shfl_up_sync(0xffffffffu, sum, off);
-                            if (lane >= off) sum += o;
-                        }
-                        if (lane == 31) sh.warp[warp] = sum;
-                        __syncthreads();
-                        for (int i = 0; i < warp; ++i) sum += sh.warp[i];
-                        sum += above;
-                        if (sum - second >= target && sum - second - first < target) sh.found[0] = sh.list[at];
-                        else if (sum >= target && sum - second < target) sh.found[0] = sh.list[at + 1];
+                        const uint64_t first = 2 * tid < n ? listed_weight(2 * tid) : 0, second = 2 * tid + 1 < n ? listed_weight(2 * tid + 1) : 0;
+                        const uint64_t upto = above + running(first, second, sh.warp);
+                        if (upto - second >= target && upto - second - first < target) sh.found[0] = sh.list[2 * tid];
+                        else if (upto >= target && upto - second < target) sh.found[0] = sh.list[2 * tid + 1];
                     }
                     __syncthreads();
                     if (tid > 0 && tid < blocks) *remote(&sh.found[0], tid) = sh.found[0];
@@ -432,7 +487,7 @@ sample_kernel(const Args a) {
             uint32_t least = 0xFFFFFFFFu, most = 0;
             for (int v = v_begin + lane; v < v_end; v += 32) {
                 float l[kVec];
-                S::get(slice, v, l);
+                Vec<T>{slice[v]}.unpack(l);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     const uint64_t place = place_of(l[j], i0 + v * kVec + j);
@@ -476,28 +531,118 @@ sample_kernel(const Args a) {
         }
     };
 
-    uint64_t cut = 0;
-    const int k = a.top_k ? a.top_k[row] : 0;
-    if (k > 0 && k < a.V) cut = cut_at(cut, false, k, 0.0f);
-    const float p = a.top_p ? a.top_p[row] : 1.0f;
-    if (p < 1.0f) cut = cut_at(cut, true, 0, p);
+    const int k = a.top_k && a.top_k[row] > 0 && a.top_k[row] < a.V ? a.top_k[row] : 0;   // 0: all
+    const float p = a.top_p ? a.top_p[row] : 1.0f, u = a.u[row];
     float least = -INFINITY;   // min-p: of the logits
     if (a.min_p && a.min_p[row] > 0.0f)
         least = __double2float_ru(static_cast<double>(top) + static_cast<double>(temperature) * log(fmin(static_cast<double>(a.min_p[row]), 1.0)));
-
-    // ---- the draw
-    const auto kept = [&](float l, int i) -> uint64_t { return l >= least && place_of(l, i) >= cut ? weight(l) : 0; };
-    const uint64_t all = sums(kept);
-    const float u = a.u[row];
-    const double at = static_cast<double>(u) * static_cast<double>(all);
-    uint64_t target = u > 0.0f ? (at < static_cast<double>(all) ? static_cast<uint64_t>(at) : all - 1) : 0;
-    if (target >= all) target = all - 1;
-    locate(kept, target, [&](float l, int i) {
+    const auto share = [&](float f, uint64_t all) { return static_cast<double>(f) * static_cast<double>(all); };
+    const auto target_of = [&](uint64_t all) {
+        const double at = share(u, all);
+        return u > 0.0f ? (at < static_cast<double>(all) ? min(static_cast<uint64_t>(at), all - 1) : all - 1) : 0;
+    };
+    const auto drawn = [&](float l, int i, uint64_t all) {
         a.token[row] = i;
         if (a.logprob)
             a.logprob[row] = static_cast<float>((l == top ? 0.0 : (static_cast<double>(l) - static_cast<double>(top)) / static_cast<double>(temperature)) -
                                                 log(static_cast<double>(all) * 0x1p-44));
-    });
+    };
+
+    // ---- A few tokens: at least q of the row's are as large as the q-th largest of the 8-lane
+    // groups' largest, and hardly more.  With top-k, k = q, those are listed and sorted,
+    // and all that follows is one block's.
+    if (k > 0 && k <= kFew) {
+        if (warp == 0) {   // the bound: all but the last bits of that key
+            uint32_t mine[kMaxBlocks * kGroups / 32];
+#pragma unroll
+            for (int i = 0; i < kMaxBlocks * kGroups / 32; ++i) mine[i] = lane + 32 * i < blocks * kGroups ? sh.group[lane + 32 * i] : 0;
+            uint32_t bound = 0;
+#pragma unroll 1
+            for (int bit = 31; bit >= 12; --bit) {
+                const uint32_t next = bound | 1u << bit;
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < kMaxBlocks * kGroups / 32; ++i) n += mine[i] >= next;
+                if (__reduce_add_sync(0xffffffffu, n) >= k) bound = next;
+            }
+            if (lane == 0) sh.bound = bound;
+        }
+        __syncthreads();
+        const uint32_t bound = sh.bound;
+        // the smallest float that has at least this key; no bound (a row of few blocks with tokens): none
+        const float from = bound > 0x007FFFFFu ? moe::key_value(bound) : -INFINITY;
+        if (from > -INFINITY)
+#pragma unroll 2
+            for (int v = v_begin + lane; v < v_end; v += 32) {
+                const Vec<T> x{slice[v]};
+                if (!(x.largest() >= from)) continue;
+                float l[kVec];
+                x.unpack(l);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (l[j] >= from) {
+                        const uint32_t at = atomicAdd(remote(&sh.listed, 0), 1u);
+                        if (at < kSorted) *remote(&sh.list[at], 0) = place_of(l[j], i0 + v * kVec + j);
+                    }
+            }
+        cluster.sync();
+        const int n = static_cast<int>(*remote(&sh.listed, 0));
+        if (n <= kSorted && n >= k) {
+            if (rank == 0) {
+                const int size = padded(n);
+                for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
+                __syncthreads();
+                sort_places(sh.list, size);
+                int m = k;   // those kept are the first m
+                uint64_t first = 2 * tid < m ? listed_weight(2 * tid) : 0, second = 2 * tid + 1 < m ? listed_weight(2 * tid + 1) : 0;
+                if (p < 1.0f) {
+                    const uint64_t upto = running(first, second, sh.warp);
+                    uint64_t sum = 0;
+                    for (int i = 0; i < kWarps; ++i) sum += sh.warp[i];
+                    const uint64_t reach = max(static_cast<uint64_t>(1), static_cast<uint64_t>(ceil(share(p, sum))));
+                    if (upto - second >= reach && upto - second - first < reach) sh.bound = 2 * tid + 1;
+                    else if (upto >= reach && upto - second < reach) sh.bound = 2 * tid + 2;
+                    __syncthreads();
+                    m = static_cast<int>(sh.bound);
+                }
+                {
+                    // in the order of the vocabulary
+                    __syncthreads();
+                    const int size2 = padded(m);
+                    for (int i = tid; i < size2; i += kThreads) {
+                        const uint64_t place = sh.list[i];
+                        const bool in = i < m && moe::key_value(static_cast<uint32_t>(place >> 32)) >= least;
+                        sh.list[i] = in ? place << 32 | place >> 32 : 0;
+                    }
+                    __syncthreads();
+                    sort_places(sh.list, size2);
+                    const auto value = [&](int i) { return moe::key_value(static_cast<uint32_t>(sh.list[i])); };
+                    first = 2 * tid < size2 && sh.list[2 * tid] ? weight(value(2 * tid)) : 0;
+                    second = 2 * tid + 1 < size2 && sh.list[2 * tid + 1] ? weight(value(2 * tid + 1)) : 0;
+                    const uint64_t upto = running(first, second, sh.warp);
+                    uint64_t sum = 0;
+                    for (int i = 0; i < kWarps; ++i) sum += sh.warp[i];
+                    const uint64_t target = target_of(sum);
+                    if (target < upto && target >= upto - first - second) {
+                        const int i = 2 * tid + (target >= upto - second ? 1 : 0);
+                        drawn(value(i), static_cast<int>(~static_cast<uint32_t>(sh.list[i] >> 32)), sum);
+                    }
+                }
+            }
+            // the others leave; the first stays until they have, who read its count
+            if (rank == 0) cluster.sync();
+            return;
+        }
+        cluster.sync();
+    }
+
+    // ---- any other row
+    uint64_t cut = 0;
+    if (k) cut = cut_at(cut, false, k, 0.0f);
+    if (p < 1.0f) cut = cut_at(cut, true, 0, p);
+    const auto kept = [&](float l, int i) -> uint64_t { return l >= least && place_of(l, i) >= cut ? weight(l) : 0; };
+    const uint64_t all = sums(kept);
+    locate(kept, target_of(all), [&](float l, int i) { drawn(l, i, all); });
     cluster.sync();   // no block leaves while another may read its sums
 }
 
@@ -511,8 +656,13 @@ moe_status_t launch(Args a, int rows, cudaStream_t s) {
         MOE_CHECK_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxV / kMaxBlocks * static_cast<int>(sizeof(T))));
         allowed[dev].store(1, std::memory_order_relaxed);
     }
-    const int blocks = kMaxBlocks;
-    a.slice = ((a.V + blocks - 1) / blocks + 7) / 8 * 8;
+    // Eight blocks a row; four where that still leaves room for two blocks an SM and there
+    // are rows enough to fill the GPU, as every block costs some 5 us of waiting: REPLACE
+    const int sms = moe::sm_count();
+    if (sms <= 0) return MOE_ERR_CUDA;
+    const auto slice_of = [&](int n) { return ((a.V + n - 1) / n + 7) / 8 * 8; };
+    const int blocks = rows >= sms / 2 && slice_of(4) * sizeof(T) + sizeof(Shared) + 1024 <= 114 * 1024 ? 4 : kMaxBlocks;
+    a.slice = slice_of(blocks);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * blocks);
     cfg.blockDim = dim3(kThreads);
