@@ -83,11 +83,12 @@ struct Weight {
     // t = (l - L) c = m / 64 + r with |r| <= 1/128, and 2^t = 2^(m / 64) e^(r ln 2): a table
     // of 64 powers and four terms of the series (as in P. Tang's table-driven
     // exponentials).  t, r and the series' first term are kept in two floats each.
+    // Some 50 instructions, without branches: they are what a row that needs the
+    // weight of every token takes its time for.
     __device__ __forceinline__ uint64_t operator()(float l) const {
-        if (l == top) return 1ull << 44;
+        if (top == INFINITY) return l == top ? 1ull << 44 : 0;   // the same for all
         const float d = l - top;
         const float p = d * ch;
-        if (!(p > -46.0f)) return 0;   // less than a unit; -infinity; NaN of infinity times 0
         const float b = d - l, de = (l - (d - b)) + (-top - b);   // d + de = l - L
         const float pe = fmaf(d, ch, -p) + fmaf(d, cl, de * ch);
         const float big = 12582912.0f;   // 1.5 * 2^23
@@ -97,14 +98,39 @@ struct Weight {
         constexpr float kLn2 = 0.693147182f, kLn2Rest = -1.90465421e-9f;   // ln 2 in two floats
         const float y = rh * kLn2;
         const float ye = fmaf(rh, kLn2, -y) + fmaf(rh, kLn2Rest, pe * kLn2);
-        const float rest = fmaf(ye, y, ye) + y * y * fmaf(y, fmaf(y, 0.0416666679f, 0.166666672f), 0.5f);
-        const int e = __float2int_rn(y * 137438953472.0f) + __float2int_rn(rest * 137438953472.0f);   // e^.. - 1 in 2^-37
+        const float rest = fmaf(y * y, fmaf(y, fmaf(y, 0.0416666679f, 0.166666672f), 0.5f), fmaf(ye, y, ye));
+        // e^(r ln 2) - 1 in units of 2^-37
+        const int e = __float2int_rn(y * 137438953472.0f) + __float_as_int(fmaf(rest, 137438953472.0f, big)) - __float_as_int(big);
         const uint64_t power = powers[m & 63];
         const uint64_t w = power + static_cast<uint64_t>((static_cast<int64_t>(e) * static_cast<int32_t>(power >> 32)) >> 5);
-        const int shift = 18 - (m >> 6);
-        return shift < 64 ? w >> shift : 0;
+        // below 2^-45, and for -infinity and the NaN of infinity times 0, nothing
+        return p > -45.0f ? w >> (18 - (m >> 6)) : 0;
     }
 };
+
+// floor(f * n), and the least integer not below f * n, for 0 < f < 1: exact.
+__device__ __forceinline__ uint64_t share_below(float f, uint64_t n, bool& rest) {
+    const uint32_t bits = __float_as_uint(f);
+    const int e = max(static_cast<int>(bits >> 23), 1), shift = 150 - e;   // f = mantissa * 2^-shift, 24 <= shift <= 149
+    const uint64_t mantissa = (bits & 0x7FFFFFu) | (bits >> 23 ? 0x800000u : 0u);
+    const uint64_t lo = n * mantissa, hi = __umul64hi(n, mantissa);
+    if (shift >= 128) {
+        rest = true;
+        return 0;
+    }
+    if (shift >= 64) {
+        rest = lo != 0 || (shift > 64 && (hi & ((1ull << (shift - 64)) - 1)) != 0);
+        return hi >> (shift - 64);
+    }
+    rest = (lo & ((1ull << shift) - 1)) != 0;
+    return hi << (64 - shift) | lo >> shift;
+}
+__device__ __forceinline__ uint64_t share_reached(float f, uint64_t n) {
+    if (!(f > 0.0f)) return 1;   // the first token is always kept
+    bool rest;
+    const uint64_t whole = share_below(f, n, rest);
+    return max(whole + rest, static_cast<uint64_t>(1));
+}
 
 // A token's place in the order, larger first: its logit's key, then its index.
 __device__ __forceinline__ uint64_t place_of(float l, int i) { return static_cast<uint64_t>(moe::order_key(l)) << 32 | static_cast<uint32_t>(~i); }
@@ -183,6 +209,7 @@ struct Shared {
     uint32_t key[kGroups];                            // the largest key of every 8 lanes
     uint32_t group[kMaxBlocks * kGroups];             // every block's, written by them
     uint32_t bound;
+    float ch, cl, far, far_rest;
 };
 
 // Sorts size (a power of two) places, larger first, by the whole block.
@@ -234,6 +261,21 @@ sample_kernel(const Args a) {
     const int v_begin = min(vectors, warp * each), v_end = min(vectors, v_begin + each);
     const auto remote = [&](auto* p, int r) { return cluster.map_shared_rank(p, r); };
 
+    // ---- the row's settings, by one thread: a double takes an SM long
+    const float temperature = a.temperature ? a.temperature[row] : 1.0f;
+    if (tid == kThreads - 1) {
+        const double c = 1.4426950408889634 / static_cast<double>(temperature);
+        sh.ch = static_cast<float>(c);
+        sh.cl = static_cast<float>(c - static_cast<double>(sh.ch));
+        const float least = a.min_p ? a.min_p[row] : 0.0f;
+        if (least > 0.0f) {   // T ln(min-p), in two floats
+            const double t = static_cast<double>(temperature) * log(fmin(static_cast<double>(least), 1.0));
+            sh.far = static_cast<float>(t);
+            sh.far_rest = static_cast<float>(t - static_cast<double>(sh.far));
+        } else {
+            sh.far = -INFINITY;
+        }
+    }
     // ---- the row into shared memory; the largest logit and its first place, and the
     // largest of every 8 lanes' tokens
     uint64_t best;
@@ -286,7 +328,6 @@ sample_kernel(const Args a) {
         for (int r = 1; r < blocks; ++r) best = sh.best[r] > best ? sh.best[r] : best;
     }
     const float top = moe::key_value(static_cast<uint32_t>(best >> 32));
-    const float temperature = a.temperature ? a.temperature[row] : 1.0f;
     if (top == -INFINITY || !(temperature >= 1.17549435e-38f)) {   // nothing to draw from, or greedy
         if (rank == 0 && tid == 0) {
             a.token[row] = top == -INFINITY ? -1 : static_cast<int32_t>(~static_cast<uint32_t>(best));
@@ -295,11 +336,10 @@ sample_kernel(const Args a) {
         cluster.sync();   // no block leaves while another may write to it
         return;
     }
-    const double c = 1.4426950408889634 / static_cast<double>(temperature);
     Weight weight;
     weight.top = top;
-    weight.ch = static_cast<float>(c);
-    weight.cl = static_cast<float>(c - static_cast<double>(weight.ch));
+    weight.ch = sh.ch;
+    weight.cl = sh.cl;
     weight.powers = sh.powers;
 
     // fn(l, i): a count or weight of token i.  Sums over the row: every block's in
@@ -368,6 +408,8 @@ sample_kernel(const Args a) {
         }
     };
 
+    // whether a token is not behind the cut in the order
+    const auto before_cut = [&](float l, int i, float cut_l, int cut_i) { return l > cut_l || (l == cut_l && i <= cut_i); };
     const auto listed_weight = [&](int i) { return weight(moe::key_value(static_cast<uint32_t>(sh.list[i] >> 32))); };
 
     // The token at which the sum in the order reaches a target: the place of the
@@ -377,15 +419,14 @@ sample_kernel(const Args a) {
         uint64_t target = static_cast<uint64_t>(k), above = 0;
         uint32_t low = 0, high = 0;   // keys of the bin, once known
         int shift = -1;               // -1: the first histogram, of distances to the largest
-        const float scale = static_cast<float>(c) * kBinsPerOctave;
+        const float scale = sh.ch * kBinsPerOctave;
+        const float cut_l = cut ? moe::key_value(static_cast<uint32_t>(cut >> 32)) : -INFINITY;
+        const int cut_i = cut ? static_cast<int>(~static_cast<uint32_t>(cut)) : INT_MAX;
         for (;;) {
-            const auto bin_of = [&](float l, uint32_t key) {
+            const auto bin_of = [&](float l) {   // -1: outside
                 if (shift < 0) return l == -INFINITY ? kBins - 1 : min(kBins - 1, static_cast<int>((top - l) * scale));
-                return static_cast<int>((high - key) >> shift);
-            };
-            const auto inside = [&](uint64_t place) {
-                const uint32_t key = static_cast<uint32_t>(place >> 32);
-                return place >= cut && (shift < 0 || (key >= low && key <= high));
+                const uint32_t key = moe::order_key(l);
+                return key >= low && key <= high ? static_cast<int>((high - key) >> shift) : -1;
             };
             for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
             __syncthreads();
@@ -394,11 +435,9 @@ sample_kernel(const Args a) {
                 Vec<T>{slice[v]}.unpack(l);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
-                    const uint64_t place = place_of(l[j], i0 + v * kVec + j);
-                    if (!inside(place)) continue;
                     const uint64_t w = by_weight ? weight(l[j]) : 1;
-                    if (w == 0) continue;
-                    const int bin = bin_of(l[j], static_cast<uint32_t>(place >> 32));
+                    const int bin = bin_of(l[j]);
+                    if (w == 0 || bin < 0 || !before_cut(l[j], i0 + v * kVec + j, cut_l, cut_i)) continue;
                     const uint32_t w_lo = static_cast<uint32_t>(w);
                     uint32_t w_hi = static_cast<uint32_t>(w >> 32);
                     if (w_lo && atomicAdd(&sh.lo[bin], w_lo) + w_lo < w_lo) ++w_hi;   // carry
@@ -431,9 +470,8 @@ sample_kernel(const Args a) {
             if (by_weight && shift < 0) {   // the share of the sum
                 uint64_t all = 0;
                 for (int r = 0; r < blocks; ++r) all += sh.total[r];
-                target = static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(all)));
+                target = share_reached(p, all);
             }
-            if (target == 0) target = 1;   // the first token is always kept
             for (int r = 0; r < rank; ++r) before += sh.total[r];
             if (tid < per && before + upto >= target && before + upto - mine < target)
                 for (int r = 0; r < blocks; ++r) {
@@ -445,8 +483,8 @@ sample_kernel(const Args a) {
             cluster.sync();
             const int bin = static_cast<int>(sh.found[0]);
             above = sh.found[1];
-            const auto in_this = [&](float l, uint64_t place) {
-                return inside(place) && bin_of(l, static_cast<uint32_t>(place >> 32)) == bin && (!by_weight || weight(l) != 0);
+            const auto in_this = [&](float l, int i) {
+                return bin_of(l) == bin && before_cut(l, i, cut_l, cut_i) && (!by_weight || weight(l) != 0);
             };
             // those in it are listed, if they are few, and sorted by the first block
             for (int v = v_begin + lane; v < v_end; v += 32) {
@@ -454,10 +492,10 @@ sample_kernel(const Args a) {
                 Vec<T>{slice[v]}.unpack(l);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
-                    const uint64_t place = place_of(l[j], i0 + v * kVec + j);
-                    if (in_this(l[j], place)) {
+                    const int i = i0 + v * kVec + j;
+                    if (in_this(l[j], i)) {
                         const uint32_t at = atomicAdd(remote(&sh.listed, 0), 1u);
-                        if (at < kSorted) *remote(&sh.list[at], 0) = place;
+                        if (at < kSorted) *remote(&sh.list[at], 0) = place_of(l[j], i);
                     }
                 }
             }
@@ -490,9 +528,8 @@ sample_kernel(const Args a) {
                 Vec<T>{slice[v]}.unpack(l);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
-                    const uint64_t place = place_of(l[j], i0 + v * kVec + j);
-                    if (!in_this(l[j], place)) continue;
-                    const uint32_t key = static_cast<uint32_t>(place >> 32);
+                    if (!in_this(l[j], i0 + v * kVec + j)) continue;
+                    const uint32_t key = moe::order_key(l[j]);
                     least = min(least, key);
                     most = max(most, key);
                 }
@@ -517,7 +554,7 @@ sample_kernel(const Args a) {
             if (low == high) {
                 const uint64_t one = by_weight ? weight(moe::key_value(high)) : 1;
                 const uint64_t which = (target - above + one - 1) / one;   // counted from 1
-                const auto tie = [&](float l, int i) { return static_cast<uint64_t>(moe::order_key(l) == high && place_of(l, i) >= cut); };
+                const auto tie = [&](float l, int i) { return static_cast<uint64_t>(moe::order_key(l) == high && before_cut(l, i, cut_l, cut_i)); };
                 cluster.sync();   // sh.total has been read
                 sums(tie);
                 locate(tie, which - 1, [&](float l, int i) {
@@ -533,19 +570,21 @@ sample_kernel(const Args a) {
 
     const int k = a.top_k && a.top_k[row] > 0 && a.top_k[row] < a.V ? a.top_k[row] : 0;   // 0: all
     const float p = a.top_p ? a.top_p[row] : 1.0f, u = a.u[row];
-    float least = -INFINITY;   // min-p: of the logits
-    if (a.min_p && a.min_p[row] > 0.0f)
-        least = __double2float_ru(static_cast<double>(top) + static_cast<double>(temperature) * log(fmin(static_cast<double>(a.min_p[row]), 1.0)));
-    const auto share = [&](float f, uint64_t all) { return static_cast<double>(f) * static_cast<double>(all); };
-    const auto target_of = [&](uint64_t all) {
-        const double at = share(u, all);
-        return u > 0.0f ? (at < static_cast<double>(all) ? min(static_cast<uint64_t>(at), all - 1) : all - 1) : 0;
+    // min-p: the least float that is not below L + T ln(min-p)
+    float least = -INFINITY;
+    if (sh.far > -INFINITY) {
+        const float sum = top + sh.far, b = sum - top, off = (top - (sum - b)) + (sh.far - b) + sh.far_rest;
+        least = top == INFINITY || !(off > 0.0f) ? sum : nextafterf(sum, INFINITY);
+    }
+    const auto target_of = [&](uint64_t all) -> uint64_t {
+        bool rest;
+        return !(u > 0.0f) ? 0 : u < 1.0f ? share_below(u, all, rest) : all - 1;
     };
+    // logarithms of neither sign's cancel: fp32 will do
     const auto drawn = [&](float l, int i, uint64_t all) {
         a.token[row] = i;
         if (a.logprob)
-            a.logprob[row] = static_cast<float>((l == top ? 0.0 : (static_cast<double>(l) - static_cast<double>(top)) / static_cast<double>(temperature)) -
-                                                log(static_cast<double>(all) * 0x1p-44));
+            a.logprob[row] = (l == top ? 0.0f : (l - top) / temperature) - log1pf(static_cast<float>(all - (1ull << 44)) * 0x1p-44f);
     };
 
     // ---- A few tokens: at least q of the row's are as large as the q-th largest of the 8-lane
@@ -599,7 +638,7 @@ sample_kernel(const Args a) {
                     const uint64_t upto = running(first, second, sh.warp);
                     uint64_t sum = 0;
                     for (int i = 0; i < kWarps; ++i) sum += sh.warp[i];
-                    const uint64_t reach = max(static_cast<uint64_t>(1), static_cast<uint64_t>(ceil(share(p, sum))));
+                    const uint64_t reach = share_reached(p, sum);
                     if (upto - second >= reach && upto - second - first < reach) sh.bound = 2 * tid + 1;
                     else if (upto >= reach && upto - second < reach) sh.bound = 2 * tid + 2;
                     __syncthreads();
@@ -640,7 +679,9 @@ sample_kernel(const Args a) {
     uint64_t cut = 0;
     if (k) cut = cut_at(cut, false, k, 0.0f);
     if (p < 1.0f) cut = cut_at(cut, true, 0, p);
-    const auto kept = [&](float l, int i) -> uint64_t { return l >= least && place_of(l, i) >= cut ? weight(l) : 0; };
+    const float cut_l = cut ? moe::key_value(static_cast<uint32_t>(cut >> 32)) : -INFINITY;
+    const int cut_i = cut ? static_cast<int>(~static_cast<uint32_t>(cut)) : INT_MAX;
+    const auto kept = [&](float l, int i) -> uint64_t { return l >= least && before_cut(l, i, cut_l, cut_i) ? weight(l) : 0; };
     const uint64_t all = sums(kept);
     locate(kept, target_of(all), [&](float l, int i) { drawn(l, i, all); });
     cluster.sync();   // no block leaves while another may read its sums
