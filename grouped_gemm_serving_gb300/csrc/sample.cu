@@ -34,8 +34,9 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kBinsPerOctave = 32;   // of the first histogram: 64 octaves below the largest weight
+constexpr int kBinsPerOctave = 64;   // of the first histogram: 32 octaves below the largest weight
 constexpr int kSorted = 1024;        // tokens that one block sorts
+constexpr int kCounted = 128;        // or whose places it counts
 constexpr int kMaxBlocks = 8;        // of a cluster
 constexpr int kGroups = kThreads / 8;
 constexpr int kFew = 256;            // the largest top-k whose tokens are looked for by the groups' largest
@@ -214,10 +215,12 @@ struct Shared {
 
 // Sorts size (a power of two) places, larger first, by the whole block.
 __device__ __noinline__ void sort_places(uint64_t* list, int size) {
+#pragma unroll 1
     for (int block = 2; block <= size; block *= 2)   // bitonic
+#pragma unroll 1
         for (int step = block / 2; step > 0; step /= 2) {
             for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-                const int x = 2 * step * (i / step) + i % step, y = x + step;
+                const int x = 2 * i - (i & (step - 1)), y = x + step;
                 const uint64_t p0 = list[x], p1 = list[y];
                 if ((p0 < p1) == ((x & block) == 0)) {
                     list[x] = p1;
@@ -284,7 +287,7 @@ sample_kernel(const Args a) {
         const bool aligned = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
         float most = -INFINITY;
         int at = v_begin + lane;   // the vector that has it first
-#pragma unroll 4
+#pragma unroll 8
         for (int v = v_begin + lane; v < v_end; v += 32) {
             const int i = i0 + v * kVec;
             Vec<T> x;
@@ -597,7 +600,7 @@ sample_kernel(const Args a) {
             for (int i = 0; i < kMaxBlocks * kGroups / 32; ++i) mine[i] = lane + 32 * i < blocks * kGroups ? sh.group[lane + 32 * i] : 0;
             uint32_t bound = 0;
 #pragma unroll 1
-            for (int bit = 31; bit >= 12; --bit) {
+            for (int bit = 31; bit >= 16; --bit) {
                 const uint32_t next = bound | 1u << bit;
                 int n = 0;
 #pragma unroll
@@ -627,7 +630,44 @@ sample_kernel(const Args a) {
         cluster.sync();
         const int n = static_cast<int>(*remote(&sh.listed, 0));
         if (n <= kSorted && n >= k) {
-            if (rank == 0) {
+            if (rank == 0 && n <= kCounted) {
+                // so few that each token's place is counted
+                uint64_t *places = reinterpret_cast<uint64_t*>(sh.lo), *weights = places + kCounted;
+                if (tid < n) {
+                    const uint64_t place = sh.list[tid];
+                    int before = 0;
+#pragma unroll 4
+                    for (int i = 0; i < n; ++i) before += sh.list[i] > place;
+                    places[before] = place;
+                    weights[before] = before < k ? weight(moe::key_value(static_cast<uint32_t>(place >> 32))) : 0;
+                }
+                __syncthreads();
+                int m = k;   // those kept are the first m
+                if (p < 1.0f) {
+                    const uint64_t mine = tid < m ? weights[tid] : 0, upto = running(0, mine, sh.warp);
+                    uint64_t sum = 0;
+                    for (int i = 0; i < kWarps; ++i) sum += sh.warp[i];
+                    const uint64_t reach = share_reached(p, sum);
+                    if (upto >= reach && upto - mine < reach) sh.bound = tid + 1;
+                    __syncthreads();
+                    m = static_cast<int>(sh.bound);
+                }
+                if (tid < m && moe::key_value(static_cast<uint32_t>(places[tid] >> 32)) < least) weights[tid] = 0;
+                __syncthreads();
+                if (tid < m) {
+                    const uint64_t place = places[tid], mine = weights[tid];
+                    uint64_t sum = 0, before = 0;   // all, and those with lower indexes
+#pragma unroll 4
+                    for (int i = 0; i < m; ++i) {
+                        const uint64_t w = weights[i];
+                        sum += w;
+                        if (static_cast<uint32_t>(places[i]) > static_cast<uint32_t>(place)) before += w;
+                    }
+                    const uint64_t target = target_of(sum);
+                    if (target >= before && target < before + mine)
+                        drawn(moe::key_value(static_cast<uint32_t>(place >> 32)), static_cast<int>(~static_cast<uint32_t>(place)), sum);
+                }
+            } else if (rank == 0) {
                 const int size = padded(n);
                 for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
                 __syncthreads();
@@ -644,8 +684,7 @@ sample_kernel(const Args a) {
                     __syncthreads();
                     m = static_cast<int>(sh.bound);
                 }
-                {
-                    // in the order of the vocabulary
+                {   // in the order of the vocabulary
                     __syncthreads();
                     const int size2 = padded(m);
                     for (int i = tid; i < size2; i += kThreads) {
