@@ -37,8 +37,8 @@ constexpr int kBins = 2048;
 constexpr int kBinsPerOctave = 64;   // of the first histogram: 32 octaves below the largest weight
 constexpr int kSorted = 1024;        // tokens that one block sorts
 constexpr int kCounted = 128;        // or whose places it counts
-constexpr int kMaxBlocks = 8;        // of a cluster
-constexpr int kGroups = kThreads / 8;
+constexpr int kMaxBlocks = 8;        // of a cluster: 8, 4, 2 or 1
+constexpr int kGroups = kThreads;    // of lanes of the cluster: as many lanes each as it has blocks
 constexpr int kFew = 256;            // the largest top-k whose tokens are looked for by the groups' largest
 constexpr int kMaxV = 327680;        // 40960 tokens a block: 160 KB in fp32
 
@@ -207,8 +207,8 @@ struct Shared {
     uint64_t best[kMaxBlocks], total[kMaxBlocks];   // every block's, written by them
     uint64_t found[2];                                // written by the block that found it
     uint32_t listed;
-    uint32_t key[kGroups];                            // the largest key of every 8 lanes
-    uint32_t group[kMaxBlocks * kGroups];             // every block's, written by them
+    uint32_t key[kGroups];                            // the groups' largest keys, this block's
+    uint32_t group[kGroups];                          // every block's, written by them
     uint32_t bound;
     float ch, cl, far, far_rest;
 };
@@ -280,7 +280,7 @@ sample_kernel(const Args a) {
         }
     }
     // ---- the row into shared memory; the largest logit and its first place, and the
-    // largest of every 8 lanes' tokens
+    // largest of every group of lanes
     uint64_t best;
     {
         const T* from = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.ld;
@@ -315,12 +315,14 @@ sample_kernel(const Args a) {
         }
         first = __reduce_min_sync(0xffffffffu, first);
         if (lane == 0) sh.warp[warp] = static_cast<uint64_t>(top_key) << 32 | static_cast<uint32_t>(~first);
-#pragma unroll
-        for (int off = 1; off < 8; off <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
-        if ((lane & 7) == 0) sh.key[tid / 8] = key;
+        for (int off = 1; off < blocks; off <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
+        if (tid % blocks == 0) sh.key[tid / blocks] = key;
         if (tid == 0) sh.listed = 0;
         __syncthreads();
-        for (int i = tid; i < blocks * kGroups; i += kThreads) *remote(&sh.group[rank * kGroups + i % kGroups], i / kGroups) = sh.key[i % kGroups];
+        {
+            const int groups = kGroups / blocks, to = tid / groups, i = tid % groups;
+            *remote(&sh.group[rank * groups + i], to) = sh.key[i];
+        }
         if (tid < blocks) {
             best = sh.warp[0];
             for (int i = 1; i < kWarps; ++i) best = sh.warp[i] > best ? sh.warp[i] : best;
@@ -449,11 +451,17 @@ sample_kernel(const Args a) {
             }
             cluster.sync();
             // this block's share of the bins, over all blocks; running sums over them
-            const int per = kBins / blocks;   // at most kThreads
-            uint64_t mine = 0;
-            if (tid < per)
-                for (int r = 0; r < blocks; ++r)
-                    mine += static_cast<uint64_t>(*remote(&sh.hi[rank * per + tid], r)) * 4294967296ull + *remote(&sh.lo[rank * per + tid], r);
+            constexpr int kMost = kBins / kThreads;   // bins of a thread
+            const int per = kBins / blocks, each_bin = per > kThreads ? per / kThreads : 1, bin0 = rank * per + tid * each_bin;
+            uint64_t sum[kMost] = {}, mine = 0;
+            if (tid * each_bin < per)
+#pragma unroll
+                for (int i = 0; i < kMost; ++i) {
+                    if (i >= each_bin) break;
+                    for (int r = 0; r < blocks; ++r)
+                        sum[i] += static_cast<uint64_t>(*remote(&sh.hi[bin0 + i], r)) * 4294967296ull + *remote(&sh.lo[bin0 + i], r);
+                    mine += sum[i];
+                }
             uint64_t upto = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -476,12 +484,19 @@ sample_kernel(const Args a) {
                 target = share_reached(p, all);
             }
             for (int r = 0; r < rank; ++r) before += sh.total[r];
-            if (tid < per && before + upto >= target && before + upto - mine < target)
-                for (int r = 0; r < blocks; ++r) {
-                    uint64_t* to = remote(&sh.found[0], r);
-                    to[0] = static_cast<uint64_t>(rank * per + tid);
-                    to[1] = before + upto - mine;
+            if (before + upto >= target && before + upto - mine < target) {
+                uint64_t at = before + upto - mine;
+#pragma unroll
+                for (int i = 0; i < kMost; ++i) {
+                    if (at < target && at + sum[i] >= target)
+                        for (int r = 0; r < blocks; ++r) {
+                            uint64_t* to = remote(&sh.found[0], r);
+                            to[0] = static_cast<uint64_t>(bin0 + i);
+                            to[1] = at;
+                        }
+                    at += sum[i];
                 }
+            }
             if (tid == 0) sh.listed = 0;
             cluster.sync();
             const int bin = static_cast<int>(sh.found[0]);
@@ -590,21 +605,21 @@ sample_kernel(const Args a) {
             a.logprob[row] = (l == top ? 0.0f : (l - top) / temperature) - log1pf(static_cast<float>(all - (1ull << 44)) * 0x1p-44f);
     };
 
-    // ---- A few tokens: at least q of the row's are as large as the q-th largest of the 8-lane
+    // ---- A few tokens: at least q of the row's are as large as the q-th largest of the
     // groups' largest, and hardly more.  With top-k, k = q, those are listed and sorted,
     // and all that follows is one block's.
     if (k > 0 && k <= kFew) {
         if (warp == 0) {   // the bound: all but the last bits of that key
-            uint32_t mine[kMaxBlocks * kGroups / 32];
+            uint32_t mine[kGroups / 32];
 #pragma unroll
-            for (int i = 0; i < kMaxBlocks * kGroups / 32; ++i) mine[i] = lane + 32 * i < blocks * kGroups ? sh.group[lane + 32 * i] : 0;
+            for (int i = 0; i < kGroups / 32; ++i) mine[i] = sh.group[lane + 32 * i];
             uint32_t bound = 0;
 #pragma unroll 1
             for (int bit = 31; bit >= 16; --bit) {
                 const uint32_t next = bound | 1u << bit;
                 int n = 0;
 #pragma unroll
-                for (int i = 0; i < kMaxBlocks * kGroups / 32; ++i) n += mine[i] >= next;
+                for (int i = 0; i < kGroups / 32; ++i) n += mine[i] >= next;
                 if (__reduce_add_sync(0xffffffffu, n) >= k) bound = next;
             }
             if (lane == 0) sh.bound = bound;
@@ -736,12 +751,15 @@ moe_status_t launch(Args a, int rows, cudaStream_t s) {
         MOE_CHECK_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxV / kMaxBlocks * static_cast<int>(sizeof(T))));
         allowed[dev].store(1, std::memory_order_relaxed);
     }
-    // Eight blocks a row; four where that still leaves room for two blocks an SM and there
-    // are rows enough to fill the GPU, as every block costs some 5 us of waiting: REPLACE
+    // Eight blocks a row, or fewer where the GPU would not hold all rows' at once, two an
+    // SM, and still holds them so: every block waits for others some 5 us.  us with eight,
+    // and with four, for top-k of 131072 tokens in bf16: 32 rows 22, 25; 64 rows 30, 26;
+    // 256 rows 90, 65.
     const int sms = moe::sm_count();
     if (sms <= 0) return MOE_ERR_CUDA;
     const auto slice_of = [&](int n) { return ((a.V + n - 1) / n + 7) / 8 * 8; };
-    const int blocks = rows >= sms / 2 && slice_of(4) * sizeof(T) + sizeof(Shared) + 1024 <= 114 * 1024 ? 4 : kMaxBlocks;
+    int blocks = kMaxBlocks;
+    while (blocks > 1 && static_cast<int64_t>(rows) * blocks > 2 * sms && slice_of(blocks / 2) * sizeof(T) + sizeof(Shared) + 1024 <= 114 * 1024) blocks /= 2;
     a.slice = slice_of(blocks);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * blocks);
