@@ -1,29 +1,32 @@
 // moe_forward_few: the whole expert layer for a few tokens (generating a token at
-// a time for each sequence of a batch) in two kernels.
+// a time for each sequence of a batch) in one kernel up to 8 tokens, in two above.
 //
 // With e = ids[t, j] the picks of token t and w[t, j] their weights:
 //   [g | u] = W1[e] x[t],   h = silu(g) u,   out[t] = sum_j w[t, j] W2[e] h.
 // Every weight of an expert that some token picked is read once, which bounds the
 // layer: 2 operations a weight and token against 2 bytes (bf16) or 1 (e4m3).
 //
-// The first kernel, one block, routes: per expert the set of its tokens as a 64-bit
-// mask, whose bit counts are the offsets, the permutation and its inverse (row r of
-// an expert is its r-th token in ascending order).  It writes the list of chunks,
-// up to 8 or 16 rows of an expert each, the rows' tokens and the slots' rows.
+// Routing: per expert the set of its tokens as a mask, whose bit counts are the
+// offsets, the permutation and its inverse (row r of an expert is its r-th token in
+// ascending order); from it the plan, a list of chunks, up to 8 or 16 rows of an
+// expert each, the rows' tokens and the slots' rows.  Above 8 tokens a kernel of one
+// block makes it; up to 8 every block of the main kernel makes it for itself, which
+// saves that kernel and the 3 us from it to the cooperative one (a token of 32 bf16
+// experts 43.0 us instead of 45.4, of 256 e4m3 ones 70.4 instead of 73.6).
 //
-// The second, a cooperative launch of a block per SM, streams the weights of both
-// products.  A unit is 16 weight rows (8 features' gate and up rows, or 16 output
-// features) against a chunk; the units lie in expert order and every block takes a
-// run of them, first of the one product, then of the other.  A producer warp brings
-// the weights 16 KB at a time (1 KB of each row) into a ring in shared memory by TMA,
-// as eight tiles of 128 bytes by 16 rows, without regard to what the others do: when
-// the first product ends the ring is full of the second's weights.  Sixteen warps
-// multiply, a tile of every other stage each (m16n8k16 MMAs; the order of the
+// The main kernel, a cooperative launch of a block per SM, streams the weights of
+// both products.  A unit is 16 weight rows (8 features' gate and up rows, or 16
+// output features) against a chunk; the units lie in expert order and every block
+// takes a run of them, first of the one product, then of the other.  A producer warp
+// brings the weights 16 KB at a time (1 KB of each row) into a ring in shared memory
+// by TMA, as eight tiles of 128 bytes by 16 rows, without regard to what the others
+// do: when the first product ends the ring is full of the second's weights.  Sixteen
+// warps multiply, a tile of every other stage each (m16n8k16 MMAs; the order of the
 // contraction's elements within a step is the lanes' own, the same for both
 // operands), with their columns of the chunk's rows of x in shared memory for as
 // long as the chunk lasts.  Two more take turns at adding the sixteen partial sums in
 // warp order and finishing a unit while the others go on to the next.  Between the
-// products all blocks wait for each other, as each needs rows of h from many.
+// products the grid synchronises, as each block needs rows of h from many.
 //
 // FP8 weights are converted to fp16 on the way, one instruction for two of them
 // (exact), and meet x in fp16, scaled by a power of two; the partial sum of a tile's
@@ -31,11 +34,12 @@
 // quantised: it would save no weight bytes, and cost accuracy.
 //
 // h is rounded once, to the MMA's operand: to bf16, or from fp32 to the scaled fp16
-// (8 and 11 significant bits).  The second product leaves
-// fp32 rows y; when all blocks are done each sums its share of the tokens' rows, in
-// slot order, and rounds once.  (Sums by whichever block brought the last of a
-// column's units fell to those that were behind already: 292 us instead of REPLACE64
-// for 64 tokens of 32 experts, 109 instead of REPLACE11 for 11 of 128.)
+// (8 and 11 significant bits).  The second product leaves fp32 rows y; the grid
+// synchronises again, and each block sums its share of the tokens' rows, in slot
+// order, and rounds once.  (Sums by whichever block brought the last of a column's
+// units fell to those that were behind already: 292 us instead of 279 for 64 tokens
+// of 32 experts, 109 instead of 99 for 11 of 128.)
+#include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
 #include <climits>
@@ -62,20 +66,22 @@ constexpr int kMaxT = 64;                       // tokens: the bits of a mask
 constexpr int kMaxSlots = 1024;
 constexpr int kMaxE = 256;
 constexpr int kMaxK = 32768;                    // columns of a product: a row of x takes 2 bytes each of a block
-// Threads of the routing kernel; up to kLight tokens few enough, and little enough
-// shared memory, that the second kernel's block fits beside it on its SM.
-constexpr int kRouteThreads = 1024, kLightThreads = 128, kLight = 8;
+constexpr int kRouteThreads = 1024;
+constexpr int kLight = 8;                       // tokens up to which the main kernel routes
+constexpr int kLightSlots = kLight * 32;
 
-// What the first kernel leaves for the second, in the workspace.
-struct Plan {
+// How the tokens are laid out.
+template <int SLOTS>
+struct PlanOf {
     int chunks;
-    unsigned met[2];              // finishing warps that are done with the first product, and with the second
-    int pad;
-    int4 chunk[kMaxSlots];        // expert, first row, rows, first row's token
-    float slot_w[kMaxSlots];
-    short slot_row[kMaxSlots];    // -1: a sentinel
-    uint8_t token[kMaxSlots];     // a row's token
+    int pad[3];
+    int4 chunk[SLOTS];        // expert, first row, rows, first row's token
+    float slot_w[SLOTS];
+    short slot_row[SLOTS];    // -1: a sentinel
+    uint8_t token[SLOTS];     // a row's token
 };
+using Plan = PlanOf<kMaxSlots>;       // the routing kernel's, in the workspace
+using LightPlan = PlanOf<kLightSlots>;   // a block's own, in shared memory
 
 struct Route {
     const float* logits;
@@ -85,18 +91,16 @@ struct Route {
     float* w;
     int T, E, k, renormalize;
     int chunk_rows;
-    Plan* plan;
     int* err;
 };
 
 // A token's k picks on one warp, moe_route_sort's bit for bit: the largest of
-// row[e], e < E (logit and bias), ties to the lower id.  Lane j < k returns the id of the j-th and
-// its weight in w; a NaN is never picked, and a pick that too many of them left
-// unfilled is INT_MAX.  row is in shared memory and is
-// overwritten.  Every lane keeps the best
-// of its own experts; where one is taken all lanes look for the next among that
-// lane's.  Small loops on purpose: all this runs once, and instructions that come from L2 for
-// one use cost more than they do.
+// row[e], e < E (logit and bias), ties to the lower id.  Lane j < k returns the id of
+// the j-th and its weight in w; a NaN is never picked, and a pick that too many of
+// them left unfilled is INT_MAX.  row is in shared memory and is overwritten.  Every
+// lane keeps the best of its own experts; where one is taken all lanes look for the
+// next among that lane's.  Small loops on purpose: all this runs once, and
+// instructions that come from L2 for one use cost more than they do.
 __device__ __forceinline__ int picks(float* row, int E, int k, int renormalize, float& w) {
     const int lane = threadIdx.x & 31;
     uint32_t best = 0;
@@ -144,19 +148,14 @@ __device__ __forceinline__ int picks(float* row, int E, int k, int renormalize, 
     return my_id;
 }
 
-// One block routes all tokens, a warp each at a time, and zeroes the second kernel's
-// counters.  Dynamic shared memory: the logits, with their biases.
-__global__ void __launch_bounds__(kRouteThreads)
-few_route_kernel(const Route a) {
-    extern __shared__ __align__(16) float logits[];   // [T, E]
-    __shared__ uint32_t tokens[kMaxE][2];             // the expert's tokens
-    __shared__ int base[kMaxE];                       // its first row
-    __shared__ short slot_id[kMaxSlots];
-    __shared__ int sums[kMaxE / 32];
+// A block's threads route all tokens, a warp each at a time: the experts' masks of
+// tokens, the slots' ids and weights.  logits: T * E floats of shared memory.  `record`:
+// write the picks and weights out, and report invalid ones.  Between two barriers of
+// the block's own.
+__device__ __forceinline__ void route(const Route& a, float* logits, uint32_t (*tokens)[2], short* slot_id, float* slot_w, bool record) {
     const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < 2 * kMaxE; i += threads) (&tokens[0][0])[i] = 0;
-    moe::wait_for_primary();   // what wrote the logits or ids
-    moe::launch_dependents();
+#pragma unroll 1
+    for (int i = tid; i < 2 * a.E; i += threads) (&tokens[0][0])[i] = 0;
     if (a.logits) {
 #pragma unroll 4
         for (int i = tid; i < a.T * a.E; i += threads) {
@@ -164,7 +163,6 @@ few_route_kernel(const Route a) {
             logits[i] = a.bias ? l + a.bias[i % a.E] : l;
         }
     }
-    if (tid < 2) a.plan->met[tid] = 0;
     __syncthreads();
     const auto take = [&](int t, int s, int id, bool changed) {
         if (a.mask && a.mask[s]) {
@@ -172,11 +170,11 @@ few_route_kernel(const Route a) {
             id = a.E;
         }
         if (id < 0 || id > a.E) {
-            moe::raise_device_error(a.err, MOE_DEVERR_ROUTE);
+            if (record) moe::raise_device_error(a.err, MOE_DEVERR_ROUTE);
             changed = true;
             id = a.E;
         }
-        if (changed && a.ids) a.ids[s] = id;
+        if (record && changed && a.ids) a.ids[s] = id;
         slot_id[s] = static_cast<short>(id);
         if (id < a.E) atomicOr(&tokens[id][t >> 5], 1u << (t & 31));
     };
@@ -187,64 +185,80 @@ few_route_kernel(const Route a) {
             const int id = picks(logits + t * a.E, a.E, a.k, a.renormalize, w);
             if (lane < a.k) {
                 const int s = t * a.k + lane;
-                a.plan->slot_w[s] = w;
-                if (a.w) a.w[s] = w;
+                slot_w[s] = w;
+                if (record && a.w) a.w[s] = w;
                 take(t, s, id, true);
             }
         }
     } else {
+#pragma unroll 1
         for (int s = tid; s < a.T * a.k; s += threads) {
-            a.plan->slot_w[s] = a.w[s];
+            slot_w[s] = a.w[s];
             take(s / a.k, s, a.ids[s], false);
         }
     }
-    __syncthreads();
-    // rows (low half) and chunks (high half) of the experts up to e, in blocks of 32 experts
-    const auto rows_of = [&](int e) { return e < a.E ? __popc(tokens[e][0]) + __popc(tokens[e][1]) : 0; };
-    const auto chunks_of = [&](int n) { return n > a.chunk_rows ? (n + a.chunk_rows - 1) / a.chunk_rows : (n > 0); };
+}
+
+__device__ __forceinline__ int rows_of(const uint32_t (*tokens)[2], int e) { return __popc(tokens[e][0]) + __popc(tokens[e][1]); }
+
+// One warp lays out the experts one behind the other: base, and the plan's chunks and
+// rows' tokens.
+template <int SLOTS>
+__device__ __forceinline__ void lay_out(const Route& a, const uint32_t (*tokens)[2], short* base, PlanOf<SLOTS>& plan) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;   // rows (low half) and chunks (high half) of the experts so far
 #pragma unroll 1
-    for (int block = warp; block < kMaxE / 32; block += threads / 32) {
-        const int n = rows_of(32 * block + lane);
-        int all = n | chunks_of(n) << 16;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-        if (lane == 0) sums[block] = all;
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int block = warp; block < kMaxE / 32; block += threads / 32) {
-        const int e = 32 * block + lane, n = rows_of(e), c = chunks_of(n);
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane, n = e < a.E ? rows_of(tokens, e) : 0;
+        const int c = n > a.chunk_rows ? (n + a.chunk_rows - 1) / a.chunk_rows : (n > 0);
         int upto = n | c << 16;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int below = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += below;
         }
-#pragma unroll 1
-        for (int i = 0; i < block; ++i) upto += sums[i];
-        if (e == kMaxE - 1) a.plan->chunks = upto >> 16;
+        const int all = __shfl_sync(0xffffffffu, upto, 31);
         if (n) {
-            const int row = (upto & 0xFFFF) - n, first = (upto >> 16) - c;
-            base[e] = row;
+            const int row = ((before + upto) & 0xFFFF) - n;
+            int chunk = ((before + upto) >> 16) - c;
+            base[e] = static_cast<short>(row);
             uint64_t left = tokens[e][0] | static_cast<uint64_t>(tokens[e][1]) << 32;
+            int in_chunk = 0;
 #pragma unroll 1
             for (int r = 0; r < n; ++r, left &= left - 1) {
-                const int t = __ffsll(left) - 1, i = r / a.chunk_rows;
-                a.plan->token[row + r] = static_cast<uint8_t>(t);
-                if (r == i * a.chunk_rows) a.plan->chunk[first + i] = make_int4(e, row + r, min(a.chunk_rows, n - r), t);
+                const int t = __ffsll(left) - 1;
+                plan.token[row + r] = static_cast<uint8_t>(t);
+                if (in_chunk == 0) plan.chunk[chunk++] = make_int4(e, row + r, min(a.chunk_rows, n - r), t);
+                if (++in_chunk == a.chunk_rows) in_chunk = 0;
             }
         }
+        before += all;
     }
+    if (lane == 0) plan.chunks = before >> 16;
+    __syncwarp();
+}
+
+// The row of slot s among its expert's, -1 for a sentinel.
+__device__ __forceinline__ short row_of_slot(const Route& a, const uint32_t (*tokens)[2], const short* base, const short* slot_id, int s) {
+    const int id = slot_id[s], t = s / a.k;
+    if (id >= a.E) return -1;
+    const uint32_t below = (1u << (t & 31)) - 1;
+    return static_cast<short>(base[id] + (t < 32 ? __popc(tokens[id][0] & below) : __popc(tokens[id][0]) + __popc(tokens[id][1] & below)));
+}
+
+// Dynamic shared memory: the logits, with their biases.
+__global__ void __launch_bounds__(kRouteThreads)
+few_route_kernel(const Route a, Plan* plan) {
+    extern __shared__ __align__(16) float logits[];
+    __shared__ uint32_t tokens[kMaxE][2];
+    __shared__ short base[kMaxE], slot_id[kMaxSlots];
+    moe::wait_for_primary();   // what wrote the logits or ids
+    moe::launch_dependents();
+    route(a, logits, tokens, slot_id, plan->slot_w, true);
     __syncthreads();
-    for (int s = tid; s < a.T * a.k; s += threads) {
-        const int id = slot_id[s], t = s / a.k;
-        int row = -1;
-        if (id < a.E) {   // the row of token t among the expert's
-            const uint32_t below = (1u << (t & 31)) - 1;
-            row = base[id] + (t < 32 ? __popc(tokens[id][0] & below) : __popc(tokens[id][0]) + __popc(tokens[id][1] & below));
-        }
-        a.plan->slot_row[s] = static_cast<short>(row);
-    }
+    if (threadIdx.x < 32) lay_out(a, tokens, base, *plan);
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.T * a.k; s += kRouteThreads) plan->slot_row[s] = row_of_slot(a, tokens, base, slot_id, s);
 }
 
 template <bool F16>
@@ -307,7 +321,8 @@ struct Product {
 
 struct Args {
     Product p[2];
-    Plan* plan;
+    Route route;              // up to kLight tokens
+    const Plan* plan;         // above
     void* h;                  // [T*k, F of the first]
     float* part;              // y [ceil(F / 16), T*k, 16], F of the second, then summed into
     __nv_bfloat16* out;       // [T, F of the second]
@@ -317,8 +332,8 @@ struct Args {
 };
 
 // Named barriers between the warps that multiply and those that finish, two of
-// each kind for the two buffers of partial sums, and one for the second product.
-constexpr int kFull = 1, kEmpty = 3, kReady = 5, kBarThreads = 32 * (kProduct + 1);
+// each kind for the two buffers of partial sums, and one for the block's own plan.
+constexpr int kFull = 1, kEmpty = 3, kLaidOut = 5, kBarThreads = 32 * (kProduct + 1);
 __device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kBarThreads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBarThreads) : "memory"); }
 
@@ -329,9 +344,11 @@ struct Ring {
 
 // What the plan says, within bounds whatever it says: calls that share a workspace
 // by mistake get wrong results, not wrong addresses.
-__device__ __forceinline__ int chunks_of(const Args& a) { return max(0, min(a.plan->chunks, a.T * a.k)); }
-__device__ __forceinline__ int4 chunk_of(const Args& a, int i) {   // expert, first row, rows, first row's token
-    int4 c = __ldcg(&a.plan->chunk[i]);
+template <int SLOTS>
+__device__ __forceinline__ int chunks_of(const Args& a, const PlanOf<SLOTS>& plan) { return max(0, min(plan.chunks, a.T * a.k)); }
+template <int SLOTS>
+__device__ __forceinline__ int4 chunk_of(const Args& a, const PlanOf<SLOTS>& plan, int i) {   // expert, first row, rows, first row's token
+    int4 c = plan.chunk[i];
     c.x = max(0, min(c.x, a.E - 1));
     c.z = max(1, min(c.z, a.xrows));
     c.y = max(0, min(c.y, a.T * a.k - c.z));
@@ -344,6 +361,7 @@ template <bool FIRST>
 struct Run {
     static constexpr int kFeatures = FIRST ? kRows / 2 : kRows;
     int chunk, f, per, left;   // feature block f of `per`
+    Run() = default;
     __device__ __forceinline__ Run(int chunks, int F) {
         per = (F + kFeatures - 1) / kFeatures;
         const int64_t units = static_cast<int64_t>(chunks) * per;
@@ -362,23 +380,37 @@ struct Run {
     }
 };
 
-template <bool FP8, bool FIRST>
-__device__ __forceinline__ void produce(const Maps& maps, const Product& p, const Args& a, Ring& S, uint32_t ring, int& slot,
-                                        uint32_t& turn, int64_t& filled, bool& gave_up) {
-    const int chunks = chunks_of(a);
-    int at = -1, e = 0;
-    for (Run<FIRST> u(chunks, p.F); u.left > 0 && !gave_up; u.next()) {
-        if (u.chunk != at) {
-            at = u.chunk;
-            e = chunk_of(a, at).x;
+// The producer's place in its unit and in the ring.
+struct Filled {
+    int step, slot;
+    uint32_t turn;
+    int stages;     // filled so far
+    bool gave_up;
+};
+
+// Fills the stages of run u, up to stage number `until`.
+template <bool FP8, bool FIRST, typename P>
+__device__ __forceinline__ void produce(const Maps& maps, const Product& p, const Args& a, const P& plan, Ring& S, uint32_t ring, Run<FIRST>& u,
+                                        Filled& at, int until) {
+    int chunk = -1, e = 0;
+    for (; u.left > 0; u.next(), at.step = 0) {
+        if (u.chunk != chunk) {
+            chunk = u.chunk;
+            e = chunk_of(a, plan, chunk).x;
         }
         const int f0 = u.f0();
-        for (int step = 0; step < p.steps; ++step, ++filled) {
-            if (filled >= a.stages && !moe::mbar_wait(moe::smem_u32(&S.empty[slot]), turn ^ 1u, &S.abort_flag, kWaitNs)) {
-                gave_up = true;
-                break;
+        for (; at.step < p.steps; ++at.step, ++at.stages) {
+            if (at.stages == until) return;
+            const int step = at.step;
+            if (at.stages >= a.stages && !moe::mbar_wait(moe::smem_u32(&S.empty[at.slot]), at.turn ^ 1u, &S.abort_flag, kWaitNs)) {
+                if (moe::elect_one()) {
+                    if (!S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
+                    S.abort_flag = 1;
+                }
+                at.gave_up = true;
+                return;
             }
-            const uint32_t bar = moe::smem_u32(&S.full[slot]), dst = ring + slot * kStageBytes;
+            const uint32_t bar = moe::smem_u32(&S.full[at.slot]), dst = ring + at.slot * kStageBytes;
             if (moe::elect_one()) {
                 if (step < p.whole_steps) {   // tiles past the last one come as zeros
                     moe::mbar_arrive_expect_tx(bar, kStageBytes);
@@ -393,9 +425,9 @@ __device__ __forceinline__ void produce(const Maps& maps, const Product& p, cons
                 }
             }
             __syncwarp();
-            if (++slot == a.stages) {
-                slot = 0;
-                turn ^= 1u;
+            if (++at.slot == a.stages) {
+                at.slot = 0;
+                at.turn ^= 1u;
             }
         }
     }
@@ -426,8 +458,8 @@ struct Place {
 // would run ahead of phases that were others' to take.  `first`: the number of the
 // product's first stage; `count`: units before, whose partial sums took the buffers
 // in turn.
-template <bool FP8, bool FIRST, int NBMAX>
-__device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& S, const uint8_t* ring, Sums<NBMAX>* red, uint8_t* xcols,
+template <bool FP8, bool FIRST, int NBMAX, typename P>
+__device__ __forceinline__ void multiply(const Product& p, const Args& a, const P& plan, Ring& S, const uint8_t* ring, Sums<NBMAX>* red, uint8_t* xcols,
                                          float (&unscale)[kProduct][8 * NBMAX], Place& place, int first, int& count) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = warp % kTiles, half = warp / kTiles;
     const int g = lane >> 2, c = lane & 3;
@@ -472,7 +504,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
                 const int r = min(r0 + j, rows - 1);
-                const int row = FIRST ? (r ? min(a.plan->token[row0 + r], a.T - 1) : token0) : row0 + r;
+                const int row = FIRST ? (r ? min(static_cast<int>(plan.token[row0 + r]), a.T - 1) : token0) : row0 + r;
                 from[j] = static_cast<const uint4*>(p.x) + static_cast<int64_t>(row) * (p.K / 8) * NW;
                 bits[j] = 0;
             }
@@ -527,10 +559,10 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
         __syncwarp();
     };
     int stage = first;
-    for (Run<FIRST> u(chunks_of(a), p.F); u.left > 0; u.next(), stage += p.steps, ++count) {
+    for (Run<FIRST> u(chunks_of(a, plan), p.F); u.left > 0; u.next(), stage += p.steps, ++count) {
         if (u.chunk != held) {
             held = u.chunk;
-            const int4 chunk = chunk_of(a, held);
+            const int4 chunk = chunk_of(a, plan, held);
             e = chunk.x;
             row0 = chunk.y;
             rows = chunk.z;
@@ -620,29 +652,6 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, Ring& 
     }
 }
 
-// All blocks wait here for each other, each with its two finishing warps, behind
-// what they have written; own == 0 waits for all the others'.
-__device__ __forceinline__ void meet(const Args& a, Ring& S, unsigned* arrived, int own) {
-    const int lane = threadIdx.x & 31;
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) atomicAdd(arrived, 1u);
-    if (own != 0) return;
-    const unsigned all = 2 * gridDim.x;
-    const uint64_t t0 = moe::global_timer_ns();
-    for (unsigned i = 1;; ++i) {
-        unsigned now;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(arrived) : "memory");
-        if (now >= all) break;
-        if ((i & 63u) == 0 && (S.abort_flag || moe::global_timer_ns() - t0 > kWaitNs)) {
-            if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
-            S.abort_flag = 1;
-            break;
-        }
-    }
-    __threadfence();
-}
-
 // This block's share of the tokens' sums: a thread takes 4 features of a token and
 // adds its slots' rows in their order, four loads on their way at a time.
 __device__ __forceinline__ void sum_rows(const Args& a, const float* slot_w, const short* slot_row) {
@@ -676,14 +685,13 @@ __device__ __forceinline__ void sum_rows(const Args& a, const float* slot_w, con
 }
 
 // One product on one of the two finishing warps: every other unit.
-template <bool FP8, bool FIRST, int NBMAX>
-__device__ __forceinline__ void finish(const Product& p, const Args& a, const Sums<NBMAX>* red, int& count) {
+template <bool FP8, bool FIRST, int NBMAX, typename P>
+__device__ __forceinline__ void finish(const Product& p, const Args& a, const P& plan, const Sums<NBMAX>* red, int& count) {
     const int lane = threadIdx.x & 31, g = lane >> 2, own = (threadIdx.x >> 5) - kProduct, rows_all = a.T * a.k;
-    const int chunks = chunks_of(a);
-    for (Run<FIRST> u(chunks, p.F); u.left > 0; u.next(), ++count) {
+    for (Run<FIRST> u(chunks_of(a, plan), p.F); u.left > 0; u.next(), ++count) {
         const int turn = count & 1, f0 = u.f0();
         if (turn != own) continue;
-        const int4 chunk = chunk_of(a, u.chunk);
+        const int4 chunk = chunk_of(a, plan, u.chunk);
         bar_sync(kFull + turn);
         for (int b = 0; 8 * b < chunk.z; ++b) {
             float4 s = red[turn][b][0][lane];
@@ -717,6 +725,20 @@ __device__ __forceinline__ void finish(const Product& p, const Args& a, const Su
     }
 }
 
+// What every block keeps of the routing: all of it up to kLight tokens (NBMAX 1), else
+// the slots' rows and weights.
+template <int NBMAX>
+struct Kept {
+    LightPlan plan;
+    uint32_t tokens[kMaxE][2];
+    short base[kMaxE], slot_id[kLightSlots];
+};
+template <>
+struct Kept<2> {
+    float slot_w[kMaxSlots];
+    short slot_row[kMaxSlots];
+};
+
 // NBMAX: the most groups of 8 rows of a chunk (a.xrows <= 8 NBMAX).
 template <bool FP8, int NBMAX>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -727,8 +749,11 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     uint8_t* xcols = ring + a.stages * kStageBytes + 2 * sizeof(Sums<NBMAX>);
     __shared__ Ring S;
     __shared__ float unscale[kProduct][8 * NBMAX];   // FP8: of a warp's columns of a row of x
-    __shared__ float slot_w[kMaxSlots];
-    __shared__ short slot_row[kMaxSlots];
+    __shared__ Kept<NBMAX> kept;
+    __shared__ Filled parked;       // the producer's while the grid synchronises, out of
+    __shared__ Run<false> parked_run;   // the others' registers
+    constexpr bool kRoutes = NBMAX == 1;
+    const auto grid = cooperative_groups::this_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warp == kProduct + 2 && lane == 0) {
         S.abort_flag = 0;
@@ -740,51 +765,77 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
         moe::prefetch_tensormap(&m1.whole);
         moe::prefetch_tensormap(&m2.whole);
     }
-    moe::wait_for_primary();   // the plan
-    __syncthreads();
-    if (warp == kProduct + 2) {
-        int slot = 0;
-        uint32_t turn = 0;
-        int64_t filled = 0;
-        bool gave_up = false;
-        produce<FP8, true>(m1, a.p[0], a, S, moe::smem_u32(ring), slot, turn, filled, gave_up);
-        if (!gave_up) produce<FP8, false>(m2, a.p[1], a, S, moe::smem_u32(ring), slot, turn, filled, gave_up);
-        if (gave_up) {   // no copy may land after the block has ended
-            if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
-            S.abort_flag = 1;
-            int never = 0;
-            for (int i = 0; i < a.stages && i < filled; ++i)
-                moe::mbar_wait(moe::smem_u32(&S.full[i]), static_cast<uint32_t>((filled - 1 - i) / a.stages) & 1u, &never, kWaitNs / 16);
-        }
-    } else if (warp < kProduct) {
-        Place place{0, 0, 0};
-        int count = 0;
-        multiply<FP8, true, NBMAX>(a.p[0], a, S, ring, red, xcols, unscale, place, 0, count);
-        const int first = count * a.p[0].steps;
-        bar_sync(kReady);
-        multiply<FP8, false, NBMAX>(a.p[1], a, S, ring, red, xcols, unscale, place, first, count);
-        // the finishing warps arrive once for every unit: take the last two as well
-        for (int i = max(0, count - 2); i < count; ++i) bar_sync(kEmpty + (i & 1));
-    } else {
-        const int own = warp - kProduct;
-        for (int s = 32 * own + lane; s < a.T * a.k; s += 64) {
-            slot_w[s] = __ldcg(&a.plan->slot_w[s]);
-            slot_row[s] = static_cast<short>(min(static_cast<int>(__ldcg(&a.plan->slot_row[s])), a.T * a.k - 1));
-        }
-        int count = 0;
-        finish<FP8, true, NBMAX>(a.p[0], a, red, count);
-        meet(a, S, &a.plan->met[0], own);   // every row of h is written before any is read
-        if (own == 0) bar_arrive(kReady);
-        finish<FP8, false, NBMAX>(a.p[1], a, red, count);
-        meet(a, S, &a.plan->met[1], own);
+    if constexpr (kRoutes) {
+        route(a.route, reinterpret_cast<float*>(ring), kept.tokens, kept.slot_id, kept.plan.slot_w, blockIdx.x == 0);
+        moe::fence_proxy_async();   // the ring's first copies follow the logits
     }
     __syncthreads();
-    sum_rows(a, slot_w, slot_row);
+    const auto& plan = [&]() -> const auto& {
+        if constexpr (kRoutes) return kept.plan;
+        else return *a.plan;
+    }();
+    if constexpr (kRoutes) {
+        if (warp == kProduct + 2) {   // the weights wait for no more than this
+            lay_out(a.route, kept.tokens, kept.base, kept.plan);
+            asm volatile("bar.arrive %0, %1;" ::"n"(kLaidOut), "n"(kThreads) : "memory");
+        } else {
+            asm volatile("bar.sync %0, %1;" ::"n"(kLaidOut), "n"(kThreads) : "memory");
+        }
+    }
+    Place place{0, 0, 0};
+    int count = 0;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+        if (warp == kProduct + 2) {
+            Filled at{0, 0, 0, 0, false};
+            Run<false> second(chunks_of(a, plan), a.p[1].F);
+            if (part == 0) {
+                Run<true> u(chunks_of(a, plan), a.p[0].F);
+                produce<FP8, true>(m1, a.p[0], a, plan, S, moe::smem_u32(ring), u, at, INT_MAX);
+            } else {
+                at = parked;
+                second = parked_run;
+            }
+            // before the grid has synchronised, as much of the second product as the ring holds
+            if (!at.gave_up)
+                produce<FP8, false>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
+            if (part == 0 && lane == 0) {
+                parked = at;
+                parked_run = second;
+            } else if (at.gave_up) {   // no copy may land after the block has ended
+                int never = 0;
+                for (int i = 0; i < a.stages && i < at.stages; ++i)
+                    moe::mbar_wait(moe::smem_u32(&S.full[i]), static_cast<uint32_t>((at.stages - 1 - i) / a.stages) & 1u, &never, kWaitNs / 16);
+            }
+        } else if (warp < kProduct) {
+            if (part == 0) {
+                multiply<FP8, true, NBMAX>(a.p[0], a, plan, S, ring, red, xcols, unscale, place, 0, count);
+            } else {
+                multiply<FP8, false, NBMAX>(a.p[1], a, plan, S, ring, red, xcols, unscale, place, count * a.p[0].steps, count);
+                // the finishing warps arrive once for every unit: take the last two as well
+                for (int i = max(0, count - 2); i < count; ++i) bar_sync(kEmpty + (i & 1));
+            }
+        } else if (part == 0) {
+            const int own = warp - kProduct;
+            for (int s = 32 * own + lane; s < a.T * a.k; s += 64) {
+                if constexpr (kRoutes) {
+                    kept.plan.slot_row[s] = row_of_slot(a.route, kept.tokens, kept.base, kept.slot_id, s);
+                } else {
+                    kept.slot_w[s] = plan.slot_w[s];
+                    kept.slot_row[s] = static_cast<short>(min(static_cast<int>(plan.slot_row[s]), a.T * a.k - 1));
+                }
+            }
+            finish<FP8, true, NBMAX>(a.p[0], a, plan, red, count);
+        } else {
+            finish<FP8, false, NBMAX>(a.p[1], a, plan, red, count);
+        }
+        grid.sync();   // every row of h, and then of y, is written before any is read
+    }
+    if constexpr (kRoutes) sum_rows(a, kept.plan.slot_w, kept.plan.slot_row);
+    else sum_rows(a, kept.slot_w, kept.slot_row);
 }
 
 constexpr size_t kSmem = 227 * 1024, kLeastRing = 96 * 1024;
-// What the routing kernel of up to kLight tokens takes of it, its 1 KB of overhead too.
-constexpr size_t kLightSmem = 2 * kMaxE * 4 + kMaxE * 4 + kMaxSlots * 2 + kLight * kMaxE * 4 + 64 + 1024;
 
 template <bool FP8>
 Product product(const void* x, const float* scales, int K, int F) {
@@ -800,12 +851,11 @@ template <bool FP8, int NBMAX>
 size_t shape(int T, const Product (&p)[2], int& xrows, int& stages) {
     const size_t steps = p[0].steps > p[1].steps ? p[0].steps : p[1].steps;
     const size_t row = steps / 2 * kProduct * kRowBytes * (FP8 ? 2 : 1);   // of x, all warps
-    const size_t fixed = sizeof(Ring) + kProduct * 8 * NBMAX * sizeof(float) + kMaxSlots * (sizeof(float) + sizeof(short)) + 64 + 1024;
-    const size_t all = T <= kLight ? kSmem - kLightSmem : kSmem;
-    const size_t sums = 2 * sizeof(Sums<NBMAX>), most = (all - fixed - sums - kLeastRing) / row;
+    const size_t fixed = sizeof(Ring) + kProduct * 8 * NBMAX * sizeof(float) + sizeof(Kept<NBMAX>) + 128 + 1024;
+    const size_t sums = 2 * sizeof(Sums<NBMAX>), most = (kSmem - fixed - sums - kLeastRing) / row;
     xrows = T < 8 * NBMAX ? T : 8 * NBMAX;
     if (most < static_cast<size_t>(xrows)) xrows = static_cast<int>(most);
-    const size_t n = (all - fixed - sums - xrows * row) / kStageBytes;
+    const size_t n = (kSmem - fixed - sums - xrows * row) / kStageBytes;
     stages = static_cast<int>(n < kMaxStages ? n / 2 * 2 : kMaxStages);   // even, at least 4
     return 1024 + static_cast<size_t>(stages) * kStageBytes + sums + xrows * row;
 }
@@ -855,18 +905,21 @@ bool weight_maps(Maps* m, bool fp8, bool gated, const void* W, int E, int F, int
 }
 
 template <bool FP8, int NBMAX>
-moe_status_t launch(const moe_forward_args* f, Route r, Args a, const Maps& m1, const Maps& m2, cudaStream_t s) {
+moe_status_t launch(const moe_forward_args* f, Route r, Plan* plan, Args a, const Maps& m1, const Maps& m2, cudaStream_t s) {
     static std::atomic<int> allowed[moe::kMaxDevices];
     const auto kernel = few_layer_kernel<FP8, NBMAX>;
     const int sms = moe::sm_count();
     if (sms <= 0 || !allow_smem(reinterpret_cast<const void*>(kernel), allowed)) return MOE_ERR_CUDA;
     const size_t smem = shape<FP8, NBMAX>(f->T, a.p, a.xrows, a.stages);
     r.chunk_rows = a.xrows;
-    static std::atomic<int> route_allowed[moe::kMaxDevices];
-    if (!allow_smem(reinterpret_cast<const void*>(few_route_kernel), route_allowed)) return MOE_ERR_CUDA;
-    const size_t logits = f->logits ? static_cast<size_t>(f->T) * f->E * sizeof(float) : 0;
-    const moe_status_t st = moe::launch_after(few_route_kernel, dim3(1), f->T <= kLight ? kLightThreads : kRouteThreads, logits, s, r);
-    if (st != MOE_OK) return st;
+    a.route = r;
+    if (f->T > kLight) {
+        static std::atomic<int> route_allowed[moe::kMaxDevices];
+        if (!allow_smem(reinterpret_cast<const void*>(few_route_kernel), route_allowed)) return MOE_ERR_CUDA;
+        const size_t logits = f->logits ? static_cast<size_t>(f->T) * f->E * sizeof(float) : 0;
+        const moe_status_t st = moe::launch_after(few_route_kernel, dim3(1), kRouteThreads, logits, s, r, plan);
+        if (st != MOE_OK) return st;
+    }
     // a block per SM, or per unit of the first product if every slot has an expert of its own
     const int64_t units = static_cast<int64_t>((a.p[0].F + kRows / 2 - 1) / (kRows / 2)) * (f->T * f->k < f->E ? f->T * f->k : f->E);
     cudaLaunchConfig_t cfg = {};
@@ -874,13 +927,11 @@ moe_status_t launch(const moe_forward_args* f, Route r, Args a, const Maps& m1, 
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;   // its blocks wait for one another
     attr[0].val.cooperative = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, m1, m2, a) != cudaSuccess) {
         (void)cudaGetLastError();
         return MOE_ERR_CUDA;
@@ -889,12 +940,12 @@ moe_status_t launch(const moe_forward_args* f, Route r, Args a, const Maps& m1, 
 }
 
 template <bool FP8>
-moe_status_t run(const moe_forward_args* f, const Route& r, Args a, cudaStream_t s) {
+moe_status_t run(const moe_forward_args* f, const Route& r, Plan* plan, Args a, cudaStream_t s) {
     a.p[0] = product<FP8>(f->x, f->W1_scales, f->H, f->I);
     a.p[1] = product<FP8>(a.h, f->W2_scales, f->I, f->H);
     Maps m1, m2;
     if (!weight_maps(&m1, FP8, true, f->W1, f->E, f->I, f->H) || !weight_maps(&m2, FP8, false, f->W2, f->E, f->H, f->I)) return MOE_ERR_CUDA;
-    return f->T <= 8 ? launch<FP8, 1>(f, r, a, m1, m2, s) : launch<FP8, 2>(f, r, a, m1, m2, s);
+    return f->T <= kLight ? launch<FP8, 1>(f, r, plan, a, m1, m2, s) : launch<FP8, 2>(f, r, plan, a, m1, m2, s);
 }
 
 bool valid_sizes(const moe_forward_args* a) {
@@ -952,7 +1003,7 @@ extern "C" moe_status_t moe_forward_few(const moe_forward_args* a, void* ws, siz
     if (!err) return MOE_ERR_CUDA;
     auto* base = static_cast<uint8_t*>(ws);
     auto* plan = reinterpret_cast<Plan*>(base + l.plan);
-    const Route r{a->logits, a->expert_bias, a->sentinel_mask, a->topk_ids, a->topk_w, a->T, a->E, a->k, a->renormalize, 0, plan, err};
+    const Route r{a->logits, a->expert_bias, a->sentinel_mask, a->topk_ids, a->topk_w, a->T, a->E, a->k, a->renormalize, 0, err};
     Args args{};
     args.plan = plan;
     args.h = base + l.h;
@@ -961,5 +1012,5 @@ extern "C" moe_status_t moe_forward_few(const moe_forward_args* a, void* ws, siz
     args.T = a->T, args.E = a->E, args.k = a->k;
     args.err = err;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return fp8 ? run<true>(a, r, args, s) : run<false>(a, r, args, s);
+    return fp8 ? run<true>(a, r, plan, args, s) : run<false>(a, r, plan, args, s);
 }
