@@ -34,9 +34,11 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kBinsPerOctave = 64;   // of the first histogram: 32 octaves below the largest weight
+constexpr int kOctaves = 20;         // below the largest weight that the first histogram divides
+constexpr int kShare = kBins / kWarps;
 constexpr int kSorted = 1024;        // tokens that one block sorts
-constexpr int kCounted = 128;        // or whose places it counts
+constexpr int kCounted = kThreads;   // or whose places it counts
+constexpr int kCountedFirst = 128;   // where dividing them is open too
 constexpr int kMaxBlocks = 8;        // of a cluster: 8, 4, 2 or 1
 constexpr int kGroups = kThreads;    // of lanes of the cluster: as many lanes each as it has blocks
 constexpr int kFew = 256;            // the largest top-k whose tokens are looked for by the groups' largest
@@ -205,11 +207,12 @@ struct Shared {
     uint64_t powers[64];
     uint64_t warp[kWarps];
     uint64_t best[kMaxBlocks], total[kMaxBlocks];   // every block's, written by them
-    uint64_t found[2];                                // written by the block that found it
+    uint64_t found[2];
+    uint64_t share[kMaxBlocks][kWarps];               // every block's sums of kShare bins each, written by them
     uint32_t listed;
     uint32_t key[kGroups];                            // the groups' largest keys, this block's
     uint32_t group[kGroups];                          // every block's, written by them
-    uint32_t bound;
+    int kept;
     float ch, cl, far, far_rest;
 };
 
@@ -347,13 +350,15 @@ sample_kernel(const Args a) {
     weight.cl = sh.cl;
     weight.powers = sh.powers;
 
-    // fn(l, i): a count or weight of token i.  Sums over the row: every block's in
-    // sh.total, the warps' in sh.warp.
-    const auto sums = [&](auto fn) {
+    // fn(l, i): a count or weight of token i, nothing below `from`.  Sums over the row:
+    // every block's in sh.total, the warps' in sh.warp.
+    const auto sums = [&](float from, auto fn) {
         uint64_t mine = 0;
         for (int v = v_begin + lane; v < v_end; v += 32) {
+            const Vec<T> x{slice[v]};
+            if (x.largest() < from) continue;
             float l[kVec];
-            Vec<T>{slice[v]}.unpack(l);
+            x.unpack(l);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) mine += fn(l[j], i0 + v * kVec + j);
         }
@@ -371,51 +376,128 @@ sample_kernel(const Args a) {
         for (int r = 0; r < blocks; ++r) all += sh.total[r];
         return all;
     };
-    // After sums(fn): calls take(l, i) on the thread that holds the first token at which
-    // the running sum exceeds `target`.
+    // After sums of fn: calls take(l, i) on a thread that has found the first token at
+    // which the running sum exceeds `target`.  Its block looks for it among the tokens
+    // of its warp, two a thread at a time.
     const auto locate = [&](auto fn, uint64_t target, auto take) {
         uint64_t before = 0;
         for (int r = 0; r < rank; ++r) before += sh.total[r];
-        for (int i = 0; i < warp; ++i) before += sh.warp[i];
-        if (target < before || target >= before + sh.warp[warp]) return;
-        for (int v = v_begin; v < v_end; v += 32) {
-            float l[kVec];
-            uint64_t w[kVec], mine = 0;
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) l[j] = -INFINITY, w[j] = 0;
-            if (v + lane < v_end) {
-                Vec<T>{slice[v + lane]}.unpack(l);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    w[j] = fn(l[j], i0 + (v + lane) * kVec + j);
-                    mine += w[j];
-                }
-            }
-            uint64_t upto = mine;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint64_t o = __shfl_up_sync(0xffffffffu, upto, off);
-                if (lane >= off) upto += o;
-            }
-            const uint64_t all = __shfl_sync(0xffffffffu, upto, 31);
-            if (target < before + all) {
-                uint64_t at = before + upto - mine;
-                if (target >= at && target < at + mine) {
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        if (target >= at && target < at + w[j]) take(l[j], i0 + (v + lane) * kVec + j);
-                        at += w[j];
-                    }
-                }
-                return;
-            }
-            before += all;
+        if (target < before || target - before >= sh.total[rank]) return;
+        int w = 0;
+        for (; w < kWarps - 1 && target >= before + sh.warp[w]; ++w) before += sh.warp[w];
+        const T* tokens = reinterpret_cast<const T*>(slice);
+        const int end = min(vectors, (w + 1) * each) * kVec;
+        for (int t0 = w * each * kVec; t0 < end; t0 += 2 * kThreads) {
+            const int t = t0 + 2 * tid;   // and t + 1: end is even
+            const float l0 = t < end ? static_cast<float>(tokens[t]) : -INFINITY, l1 = t < end ? static_cast<float>(tokens[t + 1]) : -INFINITY;
+            const uint64_t w0 = t < end ? fn(l0, i0 + t) : 0, w1 = t < end ? fn(l1, i0 + t + 1) : 0;
+            const uint64_t upto = before + running(w0, w1, sh.warp);
+            if (target < upto && target >= upto - w1) take(l1, i0 + t + 1);
+            else if (target < upto - w1 && target >= upto - w1 - w0) take(l0, i0 + t);
+            for (int i = 0; i < kWarps; ++i) before += sh.warp[i];
+            if (target < before) return;
         }
     };
 
     // whether a token is not behind the cut in the order
-    const auto before_cut = [&](float l, int i, float cut_l, int cut_i) { return l > cut_l || (l == cut_l && i <= cut_i); };
-    const auto listed_weight = [&](int i) { return weight(moe::key_value(static_cast<uint32_t>(sh.list[i] >> 32))); };
+    const auto before_cut = [&](float l, int i, float cut_l, int cut_i) { return l >= cut_l && (l > cut_l || i <= cut_i); };
+    const auto weight_at = [&](uint64_t place) { return weight(moe::key_value(static_cast<uint32_t>(place >> 32))); };
+    // A block lists tokens for itself; after a cluster.sync, the number of all blocks',
+    // and, if they are at most kSorted, the first block takes them together.
+    const auto list = [&](float l, int i) {
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < kSorted) sh.list[at] = place_of(l, i);
+    };
+    const auto take_listed = [&]() {
+        int upto[kMaxBlocks];
+#pragma unroll
+        for (int r = 0; r < kMaxBlocks; ++r) upto[r] = r < blocks ? static_cast<int>(*remote(&sh.listed, r)) : 0;
+#pragma unroll
+        for (int r = 1; r < kMaxBlocks; ++r) upto[r] += upto[r - 1];
+        const int n = upto[kMaxBlocks - 1];
+        if (rank == 0 && n <= kSorted) {
+            for (int i = upto[0] + tid; i < n; i += kThreads) {
+                int r = 0, first = 0;
+#pragma unroll
+                for (int q = 0; q < kMaxBlocks - 1; ++q)
+                    if (i >= upto[q]) r = q + 1, first = upto[q];
+                sh.list[i] = *remote(&sh.list[i - first], r);
+            }
+            __syncthreads();
+        }
+        return n;
+    };
+    // n places in order, by one block: few are counted, into the histogram's place;
+    // more are sorted where they are.
+    const auto count_places = [&](const uint64_t* from, int n) -> const uint64_t* {
+        auto* places = reinterpret_cast<uint64_t*>(sh.lo);
+        if (tid < n) {
+            const uint64_t place = from[tid];
+            int before = 0;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) before += from[i] > place;
+            places[before] = place;
+        }
+        __syncthreads();
+        return places;
+    };
+    const auto sort_list = [&](int n) -> const uint64_t* {
+        const int size = padded(n);
+        for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
+        __syncthreads();
+        sort_places(sh.list, size);
+        return sh.list;
+    };
+    // Of n listed places, by one block, those around the one that reaches a target, in
+    // order, and their number and the sum before them: more than a few are divided by
+    // their keys first (1000 of them: 2 us, against 7 for sorting them), unless many
+    // are alike.
+    const auto around = [&](int& n, bool by_weight, uint64_t target, uint64_t& above) -> const uint64_t* {
+        if (n <= kCountedFirst) return count_places(sh.list, n);
+        uint32_t low = 0xFFFFFFFFu, high = 0;
+        for (int i = tid; i < n; i += kThreads) {
+            const uint32_t key = static_cast<uint32_t>(sh.list[i] >> 32);
+            low = min(low, key);
+            high = max(high, key);
+        }
+        low = __reduce_min_sync(0xffffffffu, low);
+        high = __reduce_max_sync(0xffffffffu, high);
+        if (lane == 0) sh.warp[warp] = static_cast<uint64_t>(low) << 32 | high;
+        sh.lo[tid] = sh.hi[tid] = 0;   // a bin a thread
+        if (tid == 0) sh.kept = 0;
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) {
+            low = min(low, static_cast<uint32_t>(sh.warp[i] >> 32));
+            high = max(high, static_cast<uint32_t>(sh.warp[i]));
+        }
+        const int shift = max(0, 32 - __clz(high - low) - 9);
+        static_assert(kThreads == 1 << 9, "as many bins");
+        const auto bin_of = [&](uint64_t place) { return static_cast<int>((high - static_cast<uint32_t>(place >> 32)) >> shift); };
+        for (int i = tid; i < n; i += kThreads) {
+            const uint64_t w = by_weight ? weight_at(sh.list[i]) : 1;
+            const uint32_t lo = static_cast<uint32_t>(w), was = atomicAdd(&sh.lo[bin_of(sh.list[i])], lo);
+            atomicAdd(&sh.hi[bin_of(sh.list[i])], static_cast<uint32_t>(w >> 32) + (was + lo < was));
+        }
+        __syncthreads();
+        const uint64_t mine = static_cast<uint64_t>(sh.hi[tid]) << 32 | sh.lo[tid], upto = above + running(0, mine, sh.warp);
+        if (upto >= target && upto - mine < target) {
+            sh.found[0] = tid;
+            sh.found[1] = upto - mine;
+        }
+        __syncthreads();
+        auto* few = reinterpret_cast<uint64_t*>(sh.hi + kThreads);   // behind the bins
+        static_assert(2 * kCounted <= kBins && kThreads + 2 * kCounted <= kBins, "room for both");
+        for (int i = tid; i < n; i += kThreads)
+            if (bin_of(sh.list[i]) == static_cast<int>(sh.found[0])) {
+                const int at = atomicAdd(&sh.kept, 1);
+                if (at < kCounted) few[at] = sh.list[i];
+            }
+        __syncthreads();
+        if (sh.kept > kCounted) return sort_list(n);
+        n = sh.kept;
+        above = sh.found[1];
+        return count_places(few, n);
+    };
 
     // The token at which the sum in the order reaches a target: the place of the
     // last one kept.  Among the tokens at or before `cut` in the order; by_weight: the
@@ -424,114 +506,138 @@ sample_kernel(const Args a) {
         uint64_t target = static_cast<uint64_t>(k), above = 0;
         uint32_t low = 0, high = 0;   // keys of the bin, once known
         int shift = -1;               // -1: the first histogram, of distances to the largest
-        const float scale = sh.ch * kBinsPerOctave;
+        const float scale = sh.ch * (static_cast<float>(kBins) / kOctaves);
         const float cut_l = cut ? moe::key_value(static_cast<uint32_t>(cut >> 32)) : -INFINITY;
         const int cut_i = cut ? static_cast<int>(~static_cast<uint32_t>(cut)) : INT_MAX;
         for (;;) {
+            // to the nearest; what is not a number (of an infinite largest) in the last
+            const auto first_bin_of = [&](float l) { return __float_as_int(fminf((top - l) * scale, kBins - 1) + 12582912.0f) - __float_as_int(12582912.0f); };
             const auto bin_of = [&](float l) {   // -1: outside
-                if (shift < 0) return l == -INFINITY ? kBins - 1 : min(kBins - 1, static_cast<int>((top - l) * scale));
+                if (shift < 0) return first_bin_of(l);
                 const uint32_t key = moe::order_key(l);
                 return key >= low && key <= high ? static_cast<int>((high - key) >> shift) : -1;
             };
             for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
             __syncthreads();
+            // The last bin has most of a steep row's tokens, which would wait for one
+            // another: its sum is what the thread's tokens have beyond those that it
+            // counts into the other bins.
+            uint64_t last = 0;
+            const bool every = shift < 0 && cut == 0;   // no token is left out
             for (int v = v_begin + lane; v < v_end; v += 32) {
                 float l[kVec];
                 Vec<T>{slice[v]}.unpack(l);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    const uint64_t w = by_weight ? weight(l[j]) : 1;
-                    const int bin = bin_of(l[j]);
-                    if (w == 0 || bin < 0 || !before_cut(l[j], i0 + v * kVec + j, cut_l, cut_i)) continue;
-                    const uint32_t w_lo = static_cast<uint32_t>(w);
-                    uint32_t w_hi = static_cast<uint32_t>(w >> 32);
-                    if (w_lo && atomicAdd(&sh.lo[bin], w_lo) + w_lo < w_lo) ++w_hi;   // carry
-                    if (w_hi) atomicAdd(&sh.hi[bin], w_hi);
+                for (int j0 = 0; j0 < kVec; j0 += 4) {   // four on their way at a time
+                    uint64_t w[4];
+                    uint32_t was[4];
+                    int bin[4], least = kBins - 1;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = by_weight ? weight(l[j0 + j]) : 1;
+                    if (every) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) bin[j] = first_bin_of(l[j0 + j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            bin[j] = bin_of(l[j0 + j]);
+                            if (bin[j] < 0 || !before_cut(l[j0 + j], i0 + v * kVec + j0 + j, cut_l, cut_i)) w[j] = 0, bin[j] = kBins - 1;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        last += w[j];
+                        least = min(least, bin[j]);
+                    }
+                    if (least == kBins - 1) continue;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (bin[j] == kBins - 1) w[j] = 0;
+                        last -= w[j];
+                        was[j] = static_cast<uint32_t>(w[j]) ? atomicAdd(&sh.lo[bin[j]], static_cast<uint32_t>(w[j])) : 0;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t carry = was[j] + static_cast<uint32_t>(w[j]) < was[j], hi = static_cast<uint32_t>(w[j] >> 32) + carry;
+                        if (hi) atomicAdd(&sh.hi[bin[j]], hi);
+                    }
                 }
             }
-            cluster.sync();
-            // this block's share of the bins, over all blocks; running sums over them
-            constexpr int kMost = kBins / kThreads;   // bins of a thread
-            const int per = kBins / blocks, each_bin = per > kThreads ? per / kThreads : 1, bin0 = rank * per + tid * each_bin;
-            uint64_t sum[kMost] = {}, mine = 0;
-            if (tid * each_bin < per)
 #pragma unroll
-                for (int i = 0; i < kMost; ++i) {
-                    if (i >= each_bin) break;
-                    for (int r = 0; r < blocks; ++r)
-                        sum[i] += static_cast<uint64_t>(*remote(&sh.hi[bin0 + i], r)) * 4294967296ull + *remote(&sh.lo[bin0 + i], r);
-                    mine += sum[i];
-                }
+            for (int off = 16; off > 0; off >>= 1) last += __shfl_xor_sync(0xffffffffu, last, off);
+            if (lane == 0 && last) {
+                const uint32_t lo = static_cast<uint32_t>(last), was = atomicAdd(&sh.lo[kBins - 1], lo);
+                atomicAdd(&sh.hi[kBins - 1], static_cast<uint32_t>(last >> 32) + (was + lo < was));
+            }
+            __syncthreads();
+            // the sums of kShare bins each, to all blocks
+            uint64_t mine = 0;
+#pragma unroll
+            for (int i = 0; i < kShare; i += 32) {
+                const int at = warp * kShare + i + lane;
+                mine += static_cast<uint64_t>(sh.hi[at]) << 32 | sh.lo[at];
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+            if (lane < blocks) *remote(&sh.share[rank][warp], lane) = mine;
+            if (tid == 0) sh.listed = 0;
+            cluster.sync();
+            // where the target is reached, the share and then the bin, every block for itself
+            mine = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxBlocks; ++r)
+                if (r < blocks && lane < kWarps) mine += sh.share[r][lane];
             uint64_t upto = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const uint64_t o = __shfl_up_sync(0xffffffffu, upto, off);
                 if (lane >= off) upto += o;
             }
-            if (lane == 31) sh.warp[warp] = upto;
-            __syncthreads();
-            for (int i = 0; i < warp; ++i) upto += sh.warp[i];
-            if (tid < blocks) {
-                uint64_t all = 0;
-                for (int i = 0; i < kWarps; ++i) all += sh.warp[i];
-                *remote(&sh.total[rank], tid) = all;
-            }
-            cluster.sync();
-            uint64_t before = above;
-            if (by_weight && shift < 0) {   // the share of the sum
-                uint64_t all = 0;
-                for (int r = 0; r < blocks; ++r) all += sh.total[r];
-                target = share_reached(p, all);
-            }
-            for (int r = 0; r < rank; ++r) before += sh.total[r];
-            if (before + upto >= target && before + upto - mine < target) {
-                uint64_t at = before + upto - mine;
+            if (by_weight && shift < 0) target = share_reached(p, __shfl_sync(0xffffffffu, upto, 31));
+            const int share = min(kWarps, __ffs(__ballot_sync(0xffffffffu, above + upto >= target))) - 1;
+            above += __shfl_sync(0xffffffffu, upto - mine, share);
+            uint64_t sum = 0;
+            if (tid < kShare) {
 #pragma unroll
-                for (int i = 0; i < kMost; ++i) {
-                    if (at < target && at + sum[i] >= target)
-                        for (int r = 0; r < blocks; ++r) {
-                            uint64_t* to = remote(&sh.found[0], r);
-                            to[0] = static_cast<uint64_t>(bin0 + i);
-                            to[1] = at;
-                        }
-                    at += sum[i];
-                }
+                for (int r = 0; r < kMaxBlocks; ++r)   // all on their way at once
+                    if (r < blocks) sum += static_cast<uint64_t>(*remote(&sh.hi[share * kShare + tid], r)) << 32 | *remote(&sh.lo[share * kShare + tid], r);
             }
-            if (tid == 0) sh.listed = 0;
-            cluster.sync();
+            upto = above + running(0, sum, sh.warp);
+            if (upto >= target && upto - sum < target) {
+                sh.found[0] = share * kShare + tid;
+                sh.found[1] = upto - sum;
+            }
+            __syncthreads();
             const int bin = static_cast<int>(sh.found[0]);
             above = sh.found[1];
             const auto in_this = [&](float l, int i) {
                 return bin_of(l) == bin && before_cut(l, i, cut_l, cut_i) && (!by_weight || weight(l) != 0);
             };
-            // those in it are listed, if they are few, and sorted by the first block
+            const auto below = [&](float l) { return shift < 0 ? bin_of(l) > bin : moe::order_key(l) < low; };
+            // those in it are listed, if they are few, and ordered by the first block
             for (int v = v_begin + lane; v < v_end; v += 32) {
+                const Vec<T> x{slice[v]};
+                if (below(x.largest())) continue;
                 float l[kVec];
-                Vec<T>{slice[v]}.unpack(l);
+                x.unpack(l);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     const int i = i0 + v * kVec + j;
-                    if (in_this(l[j], i)) {
-                        const uint32_t at = atomicAdd(remote(&sh.listed, 0), 1u);
-                        if (at < kSorted) *remote(&sh.list[at], 0) = place_of(l[j], i);
-                    }
+                    if (in_this(l[j], i)) list(l[j], i);
                 }
             }
             cluster.sync();
-            const uint32_t in_bin = *remote(&sh.listed, 0);
-            if (in_bin <= kSorted) {
+            int n = take_listed();
+            if (n <= kSorted) {
                 if (rank == 0) {
-                    const int n = static_cast<int>(in_bin), size = padded(n);
-                    for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
-                    __syncthreads();
-                    sort_places(sh.list, size);
+                    const uint64_t* ordered = around(n, by_weight, target, above);
                     if (!by_weight) {
-                        if (tid == 0) sh.found[0] = sh.list[target - above - 1];
+                        if (tid == 0) sh.found[0] = ordered[target - above - 1];
                     } else {
-                        const uint64_t first = 2 * tid < n ? listed_weight(2 * tid) : 0, second = 2 * tid + 1 < n ? listed_weight(2 * tid + 1) : 0;
+                        const uint64_t first = 2 * tid < n ? weight_at(ordered[2 * tid]) : 0, second = 2 * tid + 1 < n ? weight_at(ordered[2 * tid + 1]) : 0;
                         const uint64_t upto = above + running(first, second, sh.warp);
-                        if (upto - second >= target && upto - second - first < target) sh.found[0] = sh.list[2 * tid];
-                        else if (upto >= target && upto - second < target) sh.found[0] = sh.list[2 * tid + 1];
+                        if (upto - second >= target && upto - second - first < target) sh.found[0] = ordered[2 * tid];
+                        else if (upto >= target && upto - second < target) sh.found[0] = ordered[2 * tid + 1];
                     }
                     __syncthreads();
                     if (tid > 0 && tid < blocks) *remote(&sh.found[0], tid) = sh.found[0];
@@ -542,8 +648,10 @@ sample_kernel(const Args a) {
             // the keys in the bin, or tokens of one value
             uint32_t least = 0xFFFFFFFFu, most = 0;
             for (int v = v_begin + lane; v < v_end; v += 32) {
+                const Vec<T> x{slice[v]};
+                if (below(x.largest())) continue;
                 float l[kVec];
-                Vec<T>{slice[v]}.unpack(l);
+                x.unpack(l);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     if (!in_this(l[j], i0 + v * kVec + j)) continue;
@@ -574,7 +682,7 @@ sample_kernel(const Args a) {
                 const uint64_t which = (target - above + one - 1) / one;   // counted from 1
                 const auto tie = [&](float l, int i) { return static_cast<uint64_t>(moe::order_key(l) == high && before_cut(l, i, cut_l, cut_i)); };
                 cluster.sync();   // sh.total has been read
-                sums(tie);
+                sums(moe::key_value(high), tie);
                 locate(tie, which - 1, [&](float l, int i) {
                     for (int r = 0; r < blocks; ++r) *remote(&sh.found[0], r) = place_of(l, i);
                 });
@@ -609,23 +717,23 @@ sample_kernel(const Args a) {
     // groups' largest, and hardly more.  With top-k, k = q, those are listed and sorted,
     // and all that follows is one block's.
     if (k > 0 && k <= kFew) {
-        if (warp == 0) {   // the bound: all but the last bits of that key
-            uint32_t mine[kGroups / 32];
+        // the bound: that key's upper half, 4 bits a time, a warp for each value of them
+        uint32_t mine[kGroups / 32], bound = 0;
 #pragma unroll
-            for (int i = 0; i < kGroups / 32; ++i) mine[i] = sh.group[lane + 32 * i];
-            uint32_t bound = 0;
+        for (int i = 0; i < kGroups / 32; ++i) mine[i] = sh.group[lane + 32 * i];
 #pragma unroll 1
-            for (int bit = 31; bit >= 16; --bit) {
-                const uint32_t next = bound | 1u << bit;
-                int n = 0;
+        for (int bit = 28; bit >= 16; bit -= 4) {
+            const uint32_t next = bound | static_cast<uint32_t>(warp) << bit;
+            int n = 0;
 #pragma unroll
-                for (int i = 0; i < kGroups / 32; ++i) n += mine[i] >= next;
-                if (__reduce_add_sync(0xffffffffu, n) >= k) bound = next;
-            }
-            if (lane == 0) sh.bound = bound;
+            for (int i = 0; i < kGroups / 32; ++i) n += mine[i] >= next;
+            n = __reduce_add_sync(0xffffffffu, n);
+            uint32_t* enough = sh.key + (bit & 4 ? kWarps : 0);   // two in turn
+            if (lane == 0) enough[warp] = n >= k;
+            __syncthreads();
+            // those that enough keys reach are the first ones
+            bound |= (__popc(__ballot_sync(0xffffffffu, lane < kWarps && enough[lane % kWarps])) - 1) << bit;
         }
-        __syncthreads();
-        const uint32_t bound = sh.bound;
         // the smallest float that has at least this key; no bound (a row of few blocks with tokens): none
         const float from = bound > 0x007FFFFFu ? moe::key_value(bound) : -INFINITY;
         if (from > -INFINITY)
@@ -646,16 +754,9 @@ sample_kernel(const Args a) {
         const int n = static_cast<int>(*remote(&sh.listed, 0));
         if (n <= kSorted && n >= k) {
             if (rank == 0 && n <= kCounted) {
-                // so few that each token's place is counted
-                uint64_t *places = reinterpret_cast<uint64_t*>(sh.lo), *weights = places + kCounted;
-                if (tid < n) {
-                    const uint64_t place = sh.list[tid];
-                    int before = 0;
-#pragma unroll 4
-                    for (int i = 0; i < n; ++i) before += sh.list[i] > place;
-                    places[before] = place;
-                    weights[before] = before < k ? weight(moe::key_value(static_cast<uint32_t>(place >> 32))) : 0;
-                }
+                const uint64_t* places = count_places(sh.list, n);
+                auto* weights = reinterpret_cast<uint64_t*>(sh.hi);
+                if (tid < k) weights[tid] = weight_at(places[tid]);
                 __syncthreads();
                 int m = k;   // those kept are the first m
                 if (p < 1.0f) {
@@ -663,9 +764,9 @@ sample_kernel(const Args a) {
                     uint64_t sum = 0;
                     for (int i = 0; i < kWarps; ++i) sum += sh.warp[i];
                     const uint64_t reach = share_reached(p, sum);
-                    if (upto >= reach && upto - mine < reach) sh.bound = tid + 1;
+                    if (upto >= reach && upto - mine < reach) sh.kept = tid + 1;
                     __syncthreads();
-                    m = static_cast<int>(sh.bound);
+                    m = sh.kept;
                 }
                 if (tid < m && moe::key_value(static_cast<uint32_t>(places[tid] >> 32)) < least) weights[tid] = 0;
                 __syncthreads();
@@ -683,21 +784,18 @@ sample_kernel(const Args a) {
                         drawn(moe::key_value(static_cast<uint32_t>(place >> 32)), static_cast<int>(~static_cast<uint32_t>(place)), sum);
                 }
             } else if (rank == 0) {
-                const int size = padded(n);
-                for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
-                __syncthreads();
-                sort_places(sh.list, size);
+                sort_list(n);
                 int m = k;   // those kept are the first m
-                uint64_t first = 2 * tid < m ? listed_weight(2 * tid) : 0, second = 2 * tid + 1 < m ? listed_weight(2 * tid + 1) : 0;
+                uint64_t first = 2 * tid < m ? weight_at(sh.list[2 * tid]) : 0, second = 2 * tid + 1 < m ? weight_at(sh.list[2 * tid + 1]) : 0;
                 if (p < 1.0f) {
                     const uint64_t upto = running(first, second, sh.warp);
                     uint64_t sum = 0;
                     for (int i = 0; i < kWarps; ++i) sum += sh.warp[i];
                     const uint64_t reach = share_reached(p, sum);
-                    if (upto - second >= reach && upto - second - first < reach) sh.bound = 2 * tid + 1;
-                    else if (upto >= reach && upto - second < reach) sh.bound = 2 * tid + 2;
+                    if (upto - second >= reach && upto - second - first < reach) sh.kept = 2 * tid + 1;
+                    else if (upto >= reach && upto - second < reach) sh.kept = 2 * tid + 2;
                     __syncthreads();
-                    m = static_cast<int>(sh.bound);
+                    m = sh.kept;
                 }
                 {   // in the order of the vocabulary
                     __syncthreads();
@@ -735,8 +833,8 @@ sample_kernel(const Args a) {
     if (p < 1.0f) cut = cut_at(cut, true, 0, p);
     const float cut_l = cut ? moe::key_value(static_cast<uint32_t>(cut >> 32)) : -INFINITY;
     const int cut_i = cut ? static_cast<int>(~static_cast<uint32_t>(cut)) : INT_MAX;
-    const auto kept = [&](float l, int i) -> uint64_t { return l >= least && before_cut(l, i, cut_l, cut_i) ? weight(l) : 0; };
-    const uint64_t all = sums(kept);
+    const auto kept = [&](float l, int i) -> uint64_t { return weight(l >= least && before_cut(l, i, cut_l, cut_i) ? l : -INFINITY); };   // without a branch
+    const uint64_t all = sums(fmaxf(least, cut_l), kept);
     locate(kept, target_of(all), [&](float l, int i) { drawn(l, i, all); });
     cluster.sync();   // no block leaves while another may read its sums
 }
