@@ -829,7 +829,9 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
         } else {
             finish<FP8, false, NBMAX>(a.p[1], a, plan, red, count);
         }
-        grid.sync();   // every row of h, and then of y, is written before any is read
+        // every row of h, and then of y, is written before any is read; every block comes
+        // here, as its other waits have a limit
+        grid.sync();
     }
     if constexpr (kRoutes) sum_rows(a, kept.plan.slot_w, kept.plan.slot_row);
     else sum_rows(a, kept.slot_w, kept.slot_row);

@@ -12,9 +12,17 @@
 // The row is read once.  A cluster of blocks holds it in shared memory, a slice
 // each, and goes over it there: for the largest logit; for a histogram of the
 // logits' distance to it, of which only the bin where a cut falls is looked at
-// closer (its tokens are sorted by one block if they are few, else its range of
-// values is divided again, down to tokens of one value, which are counted); and for
-// the draw.  No pass sorts the vocabulary.
+// closer (one block orders its tokens if they are few, else its range of values is
+// divided again, down to tokens of one value, which are counted); and for the draw.
+// With top-k up to 256, one block orders the few tokens that can be among the k, and
+// does the rest with them alone.  No pass sorts the vocabulary.
+//
+// Bound by what a row's steps wait for one another, not by its bytes: 4.9 us would read
+// 64 rows of 131072 fp32 logits, which top-p takes 76 us for.  Of a row's 24 to 45 us
+// there, two rows to four SMs at a time, 2 go into loading it, 8 to 14 into the weights
+// of all tokens and their histogram (36 and some 20 issue cycles for 32 tokens), the rest
+// into eight rounds of the cluster and what one block does alone.  256 rows of bf16 with
+// top-k: 61 us (9.9 to read), 9 to 10 a row; one row of 32000 with both: 6 us.
 //
 // A draw falls to another token wherever a running sum is off by more than u is from
 // it, so sums are exact: weights are integers, multiples of 2^-44 of the largest,
@@ -34,7 +42,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kOctaves = 20;         // below the largest weight that the first histogram divides
+constexpr int kOctaves = 20;         // below the largest weight, which the first histogram divides
 constexpr int kShare = kBins / kWarps;
 constexpr int kSorted = 1024;        // tokens that one block sorts
 constexpr int kCounted = kThreads;   // or whose places it counts
@@ -86,8 +94,8 @@ struct Weight {
     // t = (l - L) c = m / 64 + r with |r| <= 1/128, and 2^t = 2^(m / 64) e^(r ln 2): a table
     // of 64 powers and four terms of the series (as in P. Tang's table-driven
     // exponentials).  t, r and the series' first term are kept in two floats each.
-    // Some 50 instructions, without branches: they are what a row that needs the
-    // weight of every token takes its time for.
+    // Without branches, 36 issue cycles for 32 tokens.  A copy of the powers for every
+    // pair of banks and rounding by addition instead of conversions took longer (37).
     __device__ __forceinline__ uint64_t operator()(float l) const {
         if (top == INFINITY) return l == top ? 1ull << 44 : 0;   // the same for all
         const float d = l - top;
@@ -520,8 +528,9 @@ sample_kernel(const Args a) {
             for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
             __syncthreads();
             // The last bin has most of a steep row's tokens, which would wait for one
-            // another: its sum is what the thread's tokens have beyond those that it
-            // counts into the other bins.
+            // another (at 32 octaves below the largest 36000 cycles for a block's 16384
+            // tokens instead of 16000): its sum is what the thread's tokens have beyond
+            // those that it counts into the other bins.
             uint64_t last = 0;
             const bool every = shift < 0 && cut == 0;   // no token is left out
             for (int v = v_begin + lane; v < v_end; v += 32) {
@@ -851,8 +860,9 @@ moe_status_t launch(Args a, int rows, cudaStream_t s) {
     }
     // Eight blocks a row, or fewer where the GPU would not hold all rows' at once, two an
     // SM, and still holds them so: every block waits for others some 5 us.  us with eight,
-    // and with four, for top-k of 131072 tokens in bf16: 32 rows 22, 25; 64 rows 30, 26;
-    // 256 rows 90, 65.
+    // and with four, for 131072 tokens in bf16: top-k, 16 rows 17, 19; 32 rows 19, 19; 64
+    // rows 27, 22; 256 rows 87, 61; top-p, 64 rows 82, 85; 256 rows 274, 244.  256 rows of
+    // 32000: eight 67, four 43, the one of the rule 26.
     const int sms = moe::sm_count();
     if (sms <= 0) return MOE_ERR_CUDA;
     const auto slice_of = [&](int n) { return ((a.V + n - 1) / n + 7) / 8 * 8; };
