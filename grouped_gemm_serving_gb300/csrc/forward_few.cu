@@ -1,5 +1,5 @@
 // moe_forward_few: the whole expert layer for a few tokens (generating a token at
-// a time for each sequence of a batch) in one kernel up to 8 tokens, in two above.
+// a time for each sequence of a batch) in one kernel up to 16 tokens, in two above.
 //
 // With e = ids[t, j] the picks of token t and w[t, j] their weights:
 //   [g | u] = W1[e] x[t],   h = silu(g) u,   out[t] = sum_j w[t, j] W2[e] h.
@@ -9,10 +9,11 @@
 // Routing: per expert the set of its tokens as a mask, whose bit counts are the
 // offsets, the permutation and its inverse (row r of an expert is its r-th token in
 // ascending order); from it the plan, a list of chunks, up to 8 or 16 rows of an
-// expert each, the rows' tokens and the slots' rows.  Above 8 tokens a kernel of one
-// block makes it; up to 8 every block of the main kernel makes it for itself, which
+// expert each, the rows' tokens and the slots' rows.  Above 16 tokens a kernel of one
+// block makes it; up to 16 every block of the main kernel makes it for itself, which
 // saves that kernel and the 3 us from it to the cooperative one (a token of 32 bf16
-// experts 43.0 us instead of 45.4, of 256 e4m3 ones 70.4 instead of 73.6).
+// experts 43.0 us instead of 45.4, of 256 e4m3 ones 70.4 instead of 73.6; 11 tokens of
+// 128 experts 84.4 instead of 86.2).
 //
 // The main kernel, a cooperative launch of a block per SM, streams the weights of
 // both products.  A unit is 16 weight rows (8 features' gate and up rows, or 16
@@ -67,7 +68,7 @@ constexpr int kMaxSlots = 1024;
 constexpr int kMaxE = 256;
 constexpr int kMaxK = 32768;                    // columns of a product: a row of x takes 2 bytes each of a block
 constexpr int kRouteThreads = 1024;
-constexpr int kLight = 8;                       // tokens up to which the main kernel routes
+constexpr int kLight = 16;                      // tokens up to which the main kernel routes
 constexpr int kLightSlots = kLight * 32;
 
 // How the tokens are laid out.
@@ -725,22 +726,23 @@ __device__ __forceinline__ void finish(const Product& p, const Args& a, const P&
     }
 }
 
-// What every block keeps of the routing: all of it up to kLight tokens (NBMAX 1), else
-// the slots' rows and weights.
-template <int NBMAX>
+// What every block keeps of the routing: all of it up to kLight tokens, else the slots'
+// rows and weights.
+template <bool ROUTES>
 struct Kept {
     LightPlan plan;
     uint32_t tokens[kMaxE][2];
     short base[kMaxE], slot_id[kLightSlots];
 };
 template <>
-struct Kept<2> {
+struct Kept<false> {
     float slot_w[kMaxSlots];
     short slot_row[kMaxSlots];
 };
 
-// NBMAX: the most groups of 8 rows of a chunk (a.xrows <= 8 NBMAX).
-template <bool FP8, int NBMAX>
+// NBMAX: the most groups of 8 rows of a chunk (a.xrows <= 8 NBMAX).  ROUTES: up to
+// kLight tokens.
+template <bool FP8, int NBMAX, bool ROUTES>
 __global__ void __launch_bounds__(kThreads, 1)
 few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m2, const Args a) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -749,10 +751,9 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     uint8_t* xcols = ring + a.stages * kStageBytes + 2 * sizeof(Sums<NBMAX>);
     __shared__ Ring S;
     __shared__ float unscale[kProduct][8 * NBMAX];   // FP8: of a warp's columns of a row of x
-    __shared__ Kept<NBMAX> kept;
+    __shared__ Kept<ROUTES> kept;
     __shared__ Filled parked;       // the producer's while the grid synchronises, out of
     __shared__ Run<false> parked_run;   // the others' registers
-    constexpr bool kRoutes = NBMAX == 1;
     const auto grid = cooperative_groups::this_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warp == kProduct + 2 && lane == 0) {
@@ -765,16 +766,16 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
         moe::prefetch_tensormap(&m1.whole);
         moe::prefetch_tensormap(&m2.whole);
     }
-    if constexpr (kRoutes) {
+    if constexpr (ROUTES) {
         route(a.route, reinterpret_cast<float*>(ring), kept.tokens, kept.slot_id, kept.plan.slot_w, blockIdx.x == 0);
         moe::fence_proxy_async();   // the ring's first copies follow the logits
     }
     __syncthreads();
     const auto& plan = [&]() -> const auto& {
-        if constexpr (kRoutes) return kept.plan;
+        if constexpr (ROUTES) return kept.plan;
         else return *a.plan;
     }();
-    if constexpr (kRoutes) {
+    if constexpr (ROUTES) {
         if (warp == kProduct + 2) {   // the weights wait for no more than this
             lay_out(a.route, kept.tokens, kept.base, kept.plan);
             asm volatile("bar.arrive %0, %1;" ::"n"(kLaidOut), "n"(kThreads) : "memory");
@@ -818,7 +819,7 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
         } else if (part == 0) {
             const int own = warp - kProduct;
             for (int s = 32 * own + lane; s < a.T * a.k; s += 64) {
-                if constexpr (kRoutes) {
+                if constexpr (ROUTES) {
                     kept.plan.slot_row[s] = row_of_slot(a.route, kept.tokens, kept.base, kept.slot_id, s);
                 } else {
                     kept.slot_w[s] = plan.slot_w[s];
@@ -833,7 +834,7 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
         // here, as its other waits have a limit
         grid.sync();
     }
-    if constexpr (kRoutes) sum_rows(a, kept.plan.slot_w, kept.plan.slot_row);
+    if constexpr (ROUTES) sum_rows(a, kept.plan.slot_w, kept.plan.slot_row);
     else sum_rows(a, kept.slot_w, kept.slot_row);
 }
 
@@ -849,11 +850,11 @@ Product product(const void* x, const float* scales, int K, int F) {
 
 // Shared memory: as deep a ring as partial sums and rows of x leave, and no fewer
 // than kLeastRing bytes: longer rows are taken fewer at a time.
-template <bool FP8, int NBMAX>
+template <bool FP8, int NBMAX, bool ROUTES>
 size_t shape(int T, const Product (&p)[2], int& xrows, int& stages) {
     const size_t steps = p[0].steps > p[1].steps ? p[0].steps : p[1].steps;
     const size_t row = steps / 2 * kProduct * kRowBytes * (FP8 ? 2 : 1);   // of x, all warps
-    const size_t fixed = sizeof(Ring) + kProduct * 8 * NBMAX * sizeof(float) + sizeof(Kept<NBMAX>) + 128 + 1024;
+    const size_t fixed = sizeof(Ring) + kProduct * 8 * NBMAX * sizeof(float) + sizeof(Kept<ROUTES>) + 128 + 1024;
     const size_t sums = 2 * sizeof(Sums<NBMAX>), most = (kSmem - fixed - sums - kLeastRing) / row;
     xrows = T < 8 * NBMAX ? T : 8 * NBMAX;
     if (most < static_cast<size_t>(xrows)) xrows = static_cast<int>(most);
@@ -906,16 +907,16 @@ bool weight_maps(Maps* m, bool fp8, bool gated, const void* W, int E, int F, int
     return ok;
 }
 
-template <bool FP8, int NBMAX>
+template <bool FP8, int NBMAX, bool ROUTES>
 moe_status_t launch(const moe_forward_args* f, Route r, Plan* plan, Args a, const Maps& m1, const Maps& m2, cudaStream_t s) {
     static std::atomic<int> allowed[moe::kMaxDevices];
-    const auto kernel = few_layer_kernel<FP8, NBMAX>;
+    const auto kernel = few_layer_kernel<FP8, NBMAX, ROUTES>;
     const int sms = moe::sm_count();
     if (sms <= 0 || !allow_smem(reinterpret_cast<const void*>(kernel), allowed)) return MOE_ERR_CUDA;
-    const size_t smem = shape<FP8, NBMAX>(f->T, a.p, a.xrows, a.stages);
+    const size_t smem = shape<FP8, NBMAX, ROUTES>(f->T, a.p, a.xrows, a.stages);
     r.chunk_rows = a.xrows;
     a.route = r;
-    if (f->T > kLight) {
+    if (!ROUTES) {
         static std::atomic<int> route_allowed[moe::kMaxDevices];
         if (!allow_smem(reinterpret_cast<const void*>(few_route_kernel), route_allowed)) return MOE_ERR_CUDA;
         const size_t logits = f->logits ? static_cast<size_t>(f->T) * f->E * sizeof(float) : 0;
@@ -947,7 +948,8 @@ moe_status_t run(const moe_forward_args* f, const Route& r, Plan* plan, Args a, 
     a.p[1] = product<FP8>(a.h, f->W2_scales, f->I, f->H);
     Maps m1, m2;
     if (!weight_maps(&m1, FP8, true, f->W1, f->E, f->I, f->H) || !weight_maps(&m2, FP8, false, f->W2, f->E, f->H, f->I)) return MOE_ERR_CUDA;
-    return f->T <= kLight ? launch<FP8, 1>(f, r, plan, a, m1, m2, s) : launch<FP8, 2>(f, r, plan, a, m1, m2, s);
+    if (f->T <= 8) return launch<FP8, 1, true>(f, r, plan, a, m1, m2, s);
+    return f->T <= kLight ? launch<FP8, 2, true>(f, r, plan, a, m1, m2, s) : launch<FP8, 2, false>(f, r, plan, a, m1, m2, s);
 }
 
 bool valid_sizes(const moe_forward_args* a) {

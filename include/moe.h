@@ -640,7 +640,7 @@ moe_status_t moe_forward(const moe_forward_args* args, void* ws, size_t ws_bytes
 
 /*
  * moe_forward_few -- moe_forward for a few tokens: generating a token at a time
- * for each sequence of a batch.  One kernel in all (a cooperative launch), above 8
+ * for each sequence of a batch.  One kernel in all (a cooperative launch), above 16
  * tokens one before it for the routing; the weights of the experts that some
  * token picked are streamed once.  Same arguments and routing as
  * moe_forward; out[t] = sum over j of topk_w[t, j] * W2[e] h in fp32, in slot
