@@ -44,6 +44,7 @@
 #include <cuda_fp8.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -341,12 +342,12 @@ __device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0
 struct Ring {
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort_flag;
+    int chunks;
 };
 
-// What the plan says, within bounds whatever it says: calls that share a workspace
-// by mistake get wrong results, not wrong addresses.
-template <int SLOTS>
-__device__ __forceinline__ int chunks_of(const Args& a, const PlanOf<SLOTS>& plan) { return max(0, min(plan.chunks, a.T * a.k)); }
+// What the plan says, within bounds whatever it says, and the number of chunks read
+// once for a block: calls that share a workspace by mistake get wrong results, not
+// wrong addresses, nor warps that wait for more units than others have.
 template <int SLOTS>
 __device__ __forceinline__ int4 chunk_of(const Args& a, const PlanOf<SLOTS>& plan, int i) {   // expert, first row, rows, first row's token
     int4 c = plan.chunk[i];
@@ -357,26 +358,72 @@ __device__ __forceinline__ int4 chunk_of(const Args& a, const PlanOf<SLOTS>& pla
     return c;
 }
 
-// A block's run of units, in order.
-template <bool FIRST>
+// A block's run of units, in order.  An expert's chunks take turns, with as many
+// features at a time as a block has units: so neighbouring blocks stream the same
+// weights at the same time for two of its chunks, and one finds them in L2: 64 tokens of
+// 32 experts take 264 us instead of 283.  Up to kLight tokens an expert has one chunk, or
+// such long rows that several follow one another (finding out cost a token 1 to 2.6 us).
+template <typename P>
+constexpr bool kTurns = std::is_same_v<P, Plan>;
+template <bool FIRST, bool TURNS>
 struct Run {
     static constexpr int kFeatures = FIRST ? kRows / 2 : kRows;
-    int chunk, f, per, left;   // feature block f of `per`
+    int chunk, f, per, left;            // feature block f of `per`
+    int chunks, turn, group, members;   // of the group, an expert's chunks; features of a turn
+    int begin, end;                     // feature blocks of this turn
     Run() = default;
-    __device__ __forceinline__ Run(int chunks, int F) {
+    template <typename P>
+    __device__ __forceinline__ Run(int n, const P& plan, int F) : chunks(n) {
         per = (F + kFeatures - 1) / kFeatures;
         const int64_t units = static_cast<int64_t>(chunks) * per;
-        const int64_t begin = units * blockIdx.x / gridDim.x;
-        left = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - begin);
-        chunk = static_cast<int>(begin / per);
-        f = static_cast<int>(begin - static_cast<int64_t>(chunk) * per);
+        const int64_t first = units * blockIdx.x / gridDim.x;
+        left = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - first);
+        chunk = static_cast<int>(first / per);
+        f = static_cast<int>(first - static_cast<int64_t>(chunk) * per);
+        if constexpr (!TURNS) return;
+        group = chunk;
+        turn = max(1, static_cast<int>((units + gridDim.x - 1) / gridDim.x));
+        while (group > 0 && group < chunks && plan.chunk[group - 1].x == plan.chunk[group].x) --group;
+        begin = 0;
+        enter(plan);
+        int at = static_cast<int>(first - static_cast<int64_t>(group) * per);   // in the group
+        while (at >= members * (end - begin) && end < per) {
+            at -= members * (end - begin);
+            begin = end;
+            end = min(per, end + turn);
+        }
+        chunk = min(group + at / (end - begin), chunks - 1);
+        f = begin + at % (end - begin);
+    }
+    // the group's size, and its first turn's end
+    template <typename P>
+    __device__ __forceinline__ void enter(const P& plan) {
+        members = 1;
+        while (group + members < chunks && plan.chunk[group + members].x == plan.chunk[group].x) ++members;
+        end = members > 1 ? min(per, turn) : per;
     }
     __device__ __forceinline__ int f0() const { return f * kFeatures; }
-    __device__ __forceinline__ void next() {
+    template <typename P>
+    __device__ __forceinline__ void next(const P& plan) {
         --left;
-        if (++f == per) {
-            f = 0;
-            ++chunk;
+        if constexpr (!TURNS) {
+            if (++f == per) {
+                f = 0;
+                ++chunk;
+            }
+            return;
+        }
+        if (++f < end) return;
+        f = begin;
+        if (++chunk < group + members) return;
+        if (end < per) {
+            chunk = group;
+            f = begin = end;
+            end = min(per, end + turn);
+        } else if (left > 0) {
+            group = chunk = min(chunk, chunks - 1);
+            f = begin = 0;
+            enter(plan);
         }
     }
 };
@@ -390,11 +437,11 @@ struct Filled {
 };
 
 // Fills the stages of run u, up to stage number `until`.
-template <bool FP8, bool FIRST, typename P>
-__device__ __forceinline__ void produce(const Maps& maps, const Product& p, const Args& a, const P& plan, Ring& S, uint32_t ring, Run<FIRST>& u,
+template <bool FP8, bool FIRST, bool TURNS, typename P>
+__device__ __forceinline__ void produce(const Maps& maps, const Product& p, const Args& a, const P& plan, Ring& S, uint32_t ring, Run<FIRST, TURNS>& u,
                                         Filled& at, int until) {
     int chunk = -1, e = 0;
-    for (; u.left > 0; u.next(), at.step = 0) {
+    for (; u.left > 0; u.next(plan), at.step = 0) {
         if (u.chunk != chunk) {
             chunk = u.chunk;
             e = chunk_of(a, plan, chunk).x;
@@ -560,7 +607,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, const 
         __syncwarp();
     };
     int stage = first;
-    for (Run<FIRST> u(chunks_of(a, plan), p.F); u.left > 0; u.next(), stage += p.steps, ++count) {
+    for (Run<FIRST, kTurns<P>> u(S.chunks, plan, p.F); u.left > 0; u.next(plan), stage += p.steps, ++count) {
         if (u.chunk != held) {
             held = u.chunk;
             const int4 chunk = chunk_of(a, plan, held);
@@ -687,9 +734,9 @@ __device__ __forceinline__ void sum_rows(const Args& a, const float* slot_w, con
 
 // One product on one of the two finishing warps: every other unit.
 template <bool FP8, bool FIRST, int NBMAX, typename P>
-__device__ __forceinline__ void finish(const Product& p, const Args& a, const P& plan, const Sums<NBMAX>* red, int& count) {
+__device__ __forceinline__ void finish(const Product& p, const Args& a, int chunks, const P& plan, const Sums<NBMAX>* red, int& count) {
     const int lane = threadIdx.x & 31, g = lane >> 2, own = (threadIdx.x >> 5) - kProduct, rows_all = a.T * a.k;
-    for (Run<FIRST> u(chunks_of(a, plan), p.F); u.left > 0; u.next(), ++count) {
+    for (Run<FIRST, kTurns<P>> u(chunks, plan, p.F); u.left > 0; u.next(plan), ++count) {
         const int turn = count & 1, f0 = u.f0();
         if (turn != own) continue;
         const int4 chunk = chunk_of(a, plan, u.chunk);
@@ -753,7 +800,7 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     __shared__ float unscale[kProduct][8 * NBMAX];   // FP8: of a warp's columns of a row of x
     __shared__ Kept<ROUTES> kept;
     __shared__ Filled parked;       // the producer's while the grid synchronises, out of
-    __shared__ Run<false> parked_run;   // the others' registers
+    __shared__ Run<false, !ROUTES> parked_run;   // the others' registers
     const auto grid = cooperative_groups::this_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warp == kProduct + 2 && lane == 0) {
@@ -766,7 +813,9 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
         moe::prefetch_tensormap(&m1.whole);
         moe::prefetch_tensormap(&m2.whole);
     }
-    if constexpr (ROUTES) {
+    if constexpr (!ROUTES) {
+        if (threadIdx.x == 0) S.chunks = max(0, min(a.plan->chunks, a.T * a.k));
+    } else {
         route(a.route, reinterpret_cast<float*>(ring), kept.tokens, kept.slot_id, kept.plan.slot_w, blockIdx.x == 0);
         moe::fence_proxy_async();   // the ring's first copies follow the logits
     }
@@ -778,6 +827,8 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     if constexpr (ROUTES) {
         if (warp == kProduct + 2) {   // the weights wait for no more than this
             lay_out(a.route, kept.tokens, kept.base, kept.plan);
+            if (lane == 0) S.chunks = kept.plan.chunks;
+            __syncwarp();
             asm volatile("bar.arrive %0, %1;" ::"n"(kLaidOut), "n"(kThreads) : "memory");
         } else {
             asm volatile("bar.sync %0, %1;" ::"n"(kLaidOut), "n"(kThreads) : "memory");
@@ -789,17 +840,17 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     for (int part = 0; part < 2; ++part) {
         if (warp == kProduct + 2) {
             Filled at{0, 0, 0, 0, false};
-            Run<false> second(chunks_of(a, plan), a.p[1].F);
+            Run<false, !ROUTES> second(S.chunks, plan, a.p[1].F);
             if (part == 0) {
-                Run<true> u(chunks_of(a, plan), a.p[0].F);
-                produce<FP8, true>(m1, a.p[0], a, plan, S, moe::smem_u32(ring), u, at, INT_MAX);
+                Run<true, !ROUTES> u(S.chunks, plan, a.p[0].F);
+                produce<FP8, true, !ROUTES>(m1, a.p[0], a, plan, S, moe::smem_u32(ring), u, at, INT_MAX);
             } else {
                 at = parked;
                 second = parked_run;
             }
             // before the grid has synchronised, as much of the second product as the ring holds
             if (!at.gave_up)
-                produce<FP8, false>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
+                produce<FP8, false, !ROUTES>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
             if (part == 0 && lane == 0) {
                 parked = at;
                 parked_run = second;
@@ -826,9 +877,9 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
                     kept.slot_row[s] = static_cast<short>(min(static_cast<int>(plan.slot_row[s]), a.T * a.k - 1));
                 }
             }
-            finish<FP8, true, NBMAX>(a.p[0], a, plan, red, count);
+            finish<FP8, true, NBMAX>(a.p[0], a, S.chunks, plan, red, count);
         } else {
-            finish<FP8, false, NBMAX>(a.p[1], a, plan, red, count);
+            finish<FP8, false, NBMAX>(a.p[1], a, S.chunks, plan, red, count);
         }
         // every row of h, and then of y, is written before any is read; every block comes
         // here, as its other waits have a limit
