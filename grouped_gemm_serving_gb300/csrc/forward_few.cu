@@ -358,13 +358,16 @@ __device__ __forceinline__ int4 chunk_of(const Args& a, const PlanOf<SLOTS>& pla
     return c;
 }
 
-// A block's run of units, in order.  An expert's chunks take turns, with as many
-// features at a time as a block has units: so neighbouring blocks stream the same
-// weights at the same time for two of its chunks, and one finds them in L2: 64 tokens of
-// 32 experts take 264 us instead of 283.  Up to kLight tokens an expert has one chunk, or
-// such long rows that several follow one another (finding out cost a token 1 to 2.6 us).
-template <typename P>
-constexpr bool kTurns = std::is_same_v<P, Plan>;
+// A block's run of units, in order.  An expert's chunks follow one another, or TURNS:
+// take turns, with as many features at a time as a block has units, so that neighbouring
+// blocks stream the same weights at the same time for two of its chunks, and one finds
+// them in L2: 64 tokens of 32 bf16 experts take 265 us instead of 283.  Not for FP8, whose
+// registers are full (us without turns and with them, H = 7168, I = 2048: 64 tokens top-4
+// of 32 experts 459, 454; 64 top-8 of 256 1347, 1377; 32 top-8 of 256 901, 912), nor up
+// to kLight tokens, where an expert has one chunk unless rows are very long (finding out
+// cost a token 1 to 2.6 us).
+template <bool FP8, typename P>
+constexpr bool kTurns = !FP8 && std::is_same_v<P, Plan>;
 template <bool FIRST, bool TURNS>
 struct Run {
     static constexpr int kFeatures = FIRST ? kRows / 2 : kRows;
@@ -607,7 +610,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, const 
         __syncwarp();
     };
     int stage = first;
-    for (Run<FIRST, kTurns<P>> u(S.chunks, plan, p.F); u.left > 0; u.next(plan), stage += p.steps, ++count) {
+    for (Run<FIRST, kTurns<FP8, P>> u(S.chunks, plan, p.F); u.left > 0; u.next(plan), stage += p.steps, ++count) {
         if (u.chunk != held) {
             held = u.chunk;
             const int4 chunk = chunk_of(a, plan, held);
@@ -736,7 +739,7 @@ __device__ __forceinline__ void sum_rows(const Args& a, const float* slot_w, con
 template <bool FP8, bool FIRST, int NBMAX, typename P>
 __device__ __forceinline__ void finish(const Product& p, const Args& a, int chunks, const P& plan, const Sums<NBMAX>* red, int& count) {
     const int lane = threadIdx.x & 31, g = lane >> 2, own = (threadIdx.x >> 5) - kProduct, rows_all = a.T * a.k;
-    for (Run<FIRST, kTurns<P>> u(chunks, plan, p.F); u.left > 0; u.next(plan), ++count) {
+    for (Run<FIRST, kTurns<FP8, P>> u(chunks, plan, p.F); u.left > 0; u.next(plan), ++count) {
         const int turn = count & 1, f0 = u.f0();
         if (turn != own) continue;
         const int4 chunk = chunk_of(a, plan, u.chunk);
@@ -799,8 +802,9 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     __shared__ Ring S;
     __shared__ float unscale[kProduct][8 * NBMAX];   // FP8: of a warp's columns of a row of x
     __shared__ Kept<ROUTES> kept;
+    constexpr bool kInTurns = !ROUTES && !FP8;
     __shared__ Filled parked;       // the producer's while the grid synchronises, out of
-    __shared__ Run<false, !ROUTES> parked_run;   // the others' registers
+    __shared__ Run<false, kInTurns> parked_run;   // the others' registers
     const auto grid = cooperative_groups::this_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warp == kProduct + 2 && lane == 0) {
@@ -840,17 +844,17 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     for (int part = 0; part < 2; ++part) {
         if (warp == kProduct + 2) {
             Filled at{0, 0, 0, 0, false};
-            Run<false, !ROUTES> second(S.chunks, plan, a.p[1].F);
+            Run<false, kInTurns> second(S.chunks, plan, a.p[1].F);
             if (part == 0) {
-                Run<true, !ROUTES> u(S.chunks, plan, a.p[0].F);
-                produce<FP8, true, !ROUTES>(m1, a.p[0], a, plan, S, moe::smem_u32(ring), u, at, INT_MAX);
+                Run<true, kInTurns> u(S.chunks, plan, a.p[0].F);
+                produce<FP8, true, kInTurns>(m1, a.p[0], a, plan, S, moe::smem_u32(ring), u, at, INT_MAX);
             } else {
                 at = parked;
                 second = parked_run;
             }
             // before the grid has synchronised, as much of the second product as the ring holds
             if (!at.gave_up)
-                produce<FP8, false, !ROUTES>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
+                produce<FP8, false, kInTurns>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
             if (part == 0 && lane == 0) {
                 parked = at;
                 parked_run = second;
