@@ -855,9 +855,11 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
             // before the grid has synchronised, as much of the second product as the ring holds
             if (!at.gave_up)
                 produce<FP8, false, kInTurns>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
-            if (part == 0 && lane == 0) {
-                parked = at;
-                parked_run = second;
+            if (part == 0) {
+                if (lane == 0) {
+                    parked = at;
+                    parked_run = second;
+                }
             } else if (at.gave_up) {   // no copy may land after the block has ended
                 int never = 0;
                 for (int i = 0; i < a.stages && i < at.stages; ++i)
