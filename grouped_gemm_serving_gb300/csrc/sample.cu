@@ -267,6 +267,7 @@ sample_kernel(const Args a) {
     extern __shared__ uint4 slice[];
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();   // waited for before the first write to another block's memory
     const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int row = blockIdx.x / blocks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int i0 = rank * a.slice;   // the slice's first token
@@ -330,6 +331,7 @@ sample_kernel(const Args a) {
         if (tid % blocks == 0) sh.key[tid / blocks] = key;
         if (tid == 0) sh.listed = 0;
         __syncthreads();
+        cluster.barrier_wait();   // all blocks have started: their shared memory is there
         {
             const int groups = kGroups / blocks, to = tid / groups, i = tid % groups;
             *remote(&sh.group[rank * groups + i], to) = sh.key[i];
