@@ -31,6 +31,7 @@
 // draw its neighbour.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <climits>
 
 #include "common.cuh"
@@ -850,6 +851,13 @@ sample_kernel(const Args a) {
     cluster.sync();   // no block leaves while another may read its sums
 }
 
+// Bytes of a row that a block may hold: an eighth of the largest vocabulary, or what lets
+// two blocks share an SM (1 KB of each block's is the system's), whichever is more: in
+// bf16 the latter.
+constexpr size_t kTwoAnSm = 114 * 1024 - 1024 - (sizeof(Shared) + 15) / 16 * 16;
+template <typename T>
+constexpr size_t kMostSlice = std::max(kMaxV / kMaxBlocks * sizeof(T), kTwoAnSm);
+
 template <typename T>
 moe_status_t launch(Args a, int rows, cudaStream_t s) {
     static std::atomic<int> allowed[moe::kMaxDevices];
@@ -857,7 +865,7 @@ moe_status_t launch(Args a, int rows, cudaStream_t s) {
     MOE_CHECK_CUDA(cudaGetDevice(&dev));
     if (dev < 0 || dev >= moe::kMaxDevices) return MOE_ERR_CUDA;
     if (!allowed[dev].load(std::memory_order_relaxed)) {
-        MOE_CHECK_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxV / kMaxBlocks * static_cast<int>(sizeof(T))));
+        MOE_CHECK_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostSlice<T>)));
         allowed[dev].store(1, std::memory_order_relaxed);
     }
     // Eight blocks a row, or fewer where the GPU would not hold all rows' at once, two an
@@ -869,7 +877,7 @@ moe_status_t launch(Args a, int rows, cudaStream_t s) {
     if (sms <= 0) return MOE_ERR_CUDA;
     const auto slice_of = [&](int n) { return ((a.V + n - 1) / n + 7) / 8 * 8; };
     int blocks = kMaxBlocks;
-    while (blocks > 1 && static_cast<int64_t>(rows) * blocks > 2 * sms && slice_of(blocks / 2) * sizeof(T) + sizeof(Shared) + 1024 <= 114 * 1024) blocks /= 2;
+    while (blocks > 1 && static_cast<int64_t>(rows) * blocks > 2 * sms && slice_of(blocks / 2) * sizeof(T) <= kTwoAnSm) blocks /= 2;
     a.slice = slice_of(blocks);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * blocks);
