@@ -25,10 +25,13 @@
 // top-k: 61 us (9.9 to read), 9 to 10 a row; one row of 32000 with both: 6 us.
 //
 // A draw falls to another token wherever a running sum is off by more than u is from
-// it, so sums are exact: weights are integers, multiples of 2^-44 of the largest,
-// that add up in any order, and good to some 2^-37 of themselves.  With weights in
-// fp32 (2^-23) one row in ten thousand of a flat distribution over 131072 tokens would
-// draw its neighbour.
+// it.  Weights are integers, multiples of 2^-45 of the largest, whose sums are exact in
+// any order (327680 of the largest fit 64 bits); each is rounded to the nearest, so it
+// is off by at most 2^-46 and by 2^-35 of itself, and V of them by V 2^-46 at the very
+// worst.  For logits that fall with the logarithm of a token's rank (60 rows of 131072,
+// computed on the host) a draw takes another token than the definition's with
+// probability 2^-21.5, 2^-17.2 in the worst row; with weights in fp32 2^-11.6 and 2^-9.7,
+// cut to multiples of 2^-44 instead of rounded 2^-15.2 and 2^-13.4.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -86,7 +89,8 @@ __constant__ uint64_t kPowers[64] = {
     0x7a92be8a92436616ull, 0x7be86fb985689ddcull, 0x7d41d96db915019dull, 0x7e9f06067a4360baull,
 };
 
-// exp((l - L) / T) in units of 2^-44, for l <= L.
+// exp((l - L) / T) in units of 2^-kUnit, to the nearest, for l <= L.
+constexpr int kUnit = 45;
 struct Weight {
     float top;       // L
     float ch, cl;    // log2(e) / T in two parts
@@ -98,7 +102,7 @@ struct Weight {
     // Without branches, 36 issue cycles for 32 tokens.  A copy of the powers for every
     // pair of banks and rounding by addition instead of conversions took longer (37).
     __device__ __forceinline__ uint64_t operator()(float l) const {
-        if (top == INFINITY) return l == top ? 1ull << 44 : 0;   // the same for all
+        if (top == INFINITY) return l == top ? 1ull << kUnit : 0;   // the same for all
         const float d = l - top;
         const float p = d * ch;
         const float b = d - l, de = (l - (d - b)) + (-top - b);   // d + de = l - L
@@ -115,8 +119,8 @@ struct Weight {
         const int e = __float2int_rn(y * 137438953472.0f) + __float_as_int(fmaf(rest, 137438953472.0f, big)) - __float_as_int(big);
         const uint64_t power = powers[m & 63];
         const uint64_t w = power + static_cast<uint64_t>((static_cast<int64_t>(e) * static_cast<int32_t>(power >> 32)) >> 5);
-        // below 2^-45, and for -infinity and the NaN of infinity times 0, nothing
-        return p > -45.0f ? w >> (18 - (m >> 6)) : 0;
+        // below half a unit, and for -infinity and the NaN of infinity times 0, nothing
+        return p > -1.0f - kUnit ? ((w >> (61 - kUnit - (m >> 6))) + 1) >> 1 : 0;
     }
 };
 
@@ -722,7 +726,7 @@ sample_kernel(const Args a) {
     const auto drawn = [&](float l, int i, uint64_t all) {
         a.token[row] = i;
         if (a.logprob)
-            a.logprob[row] = (l == top ? 0.0f : (l - top) / temperature) - log1pf(static_cast<float>(all - (1ull << 44)) * 0x1p-44f);
+            a.logprob[row] = (l == top ? 0.0f : (l - top) / temperature) - log1pf(static_cast<float>(all - (1ull << kUnit)) * (1.0f / (1ull << kUnit)));
     };
 
     // ---- A few tokens: at least q of the row's are as large as the q-th largest of the

@@ -672,8 +672,10 @@ moe_status_t moe_forward_few(const moe_forward_args* args, void* ws, size_t ws_b
  *   min-p  those with w_i >= min_p (above 1: as 1; <= 0: all).
  * token is the first kept one, in the order of the vocabulary, at which the
  * running sum of the kept w exceeds u times their sum; logprob the logarithm of
- * its w over that sum.  Sums are exact to some 2^-37, so that tokens are those of
- * the definition but where u falls that close to a boundary.
+ * its w over that sum.  Each w is rounded to the nearest multiple of 2^-45 of the
+ * largest and is good to 2^-35 of itself besides; sums of them are exact.  So tokens
+ * are those of the definition but where u (or top_p) falls within V * 2^-45 of the
+ * largest w and 2^-34 of the sum of a boundary, at the very worst.
  * temperature below 2^-126 (0, say) or NaN: the first token of the order
  * (greedy), logprob 0.
  * Logits of -infinity or NaN are never drawn; of +infinity, only they are, with
