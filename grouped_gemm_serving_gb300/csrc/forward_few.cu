@@ -453,13 +453,19 @@ __device__ __forceinline__ void produce(const Maps& maps, const Product& p, cons
         for (; at.step < p.steps; ++at.step, ++at.stages) {
             if (at.stages == until) return;
             const int step = at.step;
-            if (at.stages >= a.stages && !moe::mbar_wait(moe::smem_u32(&S.empty[at.slot]), at.turn ^ 1u, &S.abort_flag, kWaitNs)) {
-                if (moe::elect_one()) {
-                    if (!S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
-                    S.abort_flag = 1;
+            if (at.stages >= a.stages) {
+                // A warp whose wait for a full slot ran out gives the slot back all the same,
+                // behind the flag: with the flag up a slot may have a copy under way, and none
+                // is filled again.  The warp's lanes go on or give up together.
+                const bool empty = moe::mbar_wait(moe::smem_u32(&S.empty[at.slot]), at.turn ^ 1u, &S.abort_flag, kWaitNs);
+                if (!__all_sync(0xffffffffu, empty && !S.abort_flag)) {
+                    if (moe::elect_one()) {
+                        if (!S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
+                        S.abort_flag = 1;
+                    }
+                    at.gave_up = true;
+                    return;
                 }
-                at.gave_up = true;
-                return;
             }
             const uint32_t bar = moe::smem_u32(&S.full[at.slot]), dst = ring + at.slot * kStageBytes;
             if (moe::elect_one()) {
@@ -803,8 +809,8 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     __shared__ float unscale[kProduct][8 * NBMAX];   // FP8: of a warp's columns of a row of x
     __shared__ Kept<ROUTES> kept;
     constexpr bool kInTurns = !ROUTES && !FP8;
-    __shared__ Filled parked;       // the producer's while the grid synchronises, out of
-    __shared__ Run<false, kInTurns> parked_run;   // the others' registers
+    __shared__ Filled parked;       // the producer's while the grid synchronises and behind
+    __shared__ Run<false, kInTurns> parked_run;   // the products, out of the others' registers
     const auto grid = cooperative_groups::this_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warp == kProduct + 2 && lane == 0) {
@@ -855,15 +861,9 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
             // before the grid has synchronised, as much of the second product as the ring holds
             if (!at.gave_up)
                 produce<FP8, false, kInTurns>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
-            if (part == 0) {
-                if (lane == 0) {
-                    parked = at;
-                    parked_run = second;
-                }
-            } else if (at.gave_up) {   // no copy may land after the block has ended
-                int never = 0;
-                for (int i = 0; i < a.stages && i < at.stages; ++i)
-                    moe::mbar_wait(moe::smem_u32(&S.full[i]), static_cast<uint32_t>((at.stages - 1 - i) / a.stages) & 1u, &never, kWaitNs / 16);
+            if (lane == 0) {
+                parked = at;
+                if (part == 0) parked_run = second;
             }
         } else if (warp < kProduct) {
             if (part == 0) {
@@ -890,6 +890,11 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
         // every row of h, and then of y, is written before any is read; every block comes
         // here, as its other waits have a limit
         grid.sync();
+    }
+    if (warp == kProduct + 2 && S.abort_flag) {   // whichever warp raised it: no copy may land after the block has ended
+        int never = 0;
+        for (int i = 0; i < a.stages && i < parked.stages; ++i)
+            moe::mbar_wait(moe::smem_u32(&S.full[i]), static_cast<uint32_t>((parked.stages - 1 - i) / a.stages) & 1u, &never, kWaitNs / 16);
     }
     if constexpr (ROUTES) sum_rows(a, kept.plan.slot_w, kept.plan.slot_row);
     else sum_rows(a, kept.slot_w, kept.slot_row);
