@@ -286,12 +286,10 @@ __device__ __forceinline__ void f16x2_of_e4m3x4(uint32_t four, uint32_t& lo, uin
 }
 
 // FP8's scaling of x: the exponent that takes the largest magnitude (bits of a
-// bf16) to [2^14, 2^15), within what a float's exponent holds; 0 for zero and for
-// what is not finite.
-__device__ __forceinline__ int scale_exponent(int bits) {
-    const int e = bits >> 7;
-    return e == 255 || bits == 0 ? 0 : min(141 - max(e, 1), 126);
-}
+// bf16) to [2^14, 2^15), within what a float's exponent holds; 0 for zero.  Beside
+// infinities and NaN every finite value has to stay finite: their exponent is one past
+// the largest finite one's, and takes that to [2^13, 2^14).
+__device__ __forceinline__ int scale_exponent(int bits) { return bits == 0 ? 0 : min(141 - max(bits >> 7, 1), 126); }
 __device__ __forceinline__ uint32_t scaled_f16x2(float lo, float hi, float f) {
     const __half2 h = __floats2half2_rn(lo * f, hi * f);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -547,8 +545,9 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, const 
     // like the tiles; an FP8 vector of weights meets two of x, the halves.  FP8: scaled
     // by a power of two per row to at most 2^15 and held in fp16, which loses nothing of
     // a bf16 within 2^29 of the largest, and of the others less than 2^-39 of that; h, in
-    // fp32, is rounded to its 11 bits.  A row with infinities or NaN is not scaled.  A few rows, two vectors each, on their
-    // way at a time; FP8 looks at them once for the scale and once to convert them.
+    // fp32, is rounded to its 11 bits.  Beside infinities and NaN, which decide every sum,
+    // small values become zero.  A few rows, two vectors each, on their way at a time;
+    // FP8 looks at them once for the scale and once to convert them.
     const auto take_x = [&]() {
         constexpr int NW = kWide ? 2 : 1, NR = NBMAX == 1 ? 2 : 4, NV = 2 / NW;
         const int vectors = mine * kVectors;
