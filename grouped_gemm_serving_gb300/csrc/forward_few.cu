@@ -340,6 +340,7 @@ __device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0
 struct Ring {
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort_flag;
+    int sent;   // stages, once the producer has given up
     int chunks;
 };
 
@@ -429,11 +430,14 @@ struct Run {
     }
 };
 
-// The producer's place in its unit and in the ring.
+// The producer's place in its unit and in the ring.  gave_up: whether a wait of its elected
+// lane, the one that waits and sends, has run out.  The warp then goes on over its stages and
+// sends nothing, so that its lanes stay together (a vote on every stage took 64 tokens of 32
+// experts 275 us instead of 271, one on the flag too 299).
 struct Filled {
     int step, slot;
     uint32_t turn;
-    int stages;     // filled so far
+    int stages;     // so far
     bool gave_up;
 };
 
@@ -451,23 +455,14 @@ __device__ __forceinline__ void produce(const Maps& maps, const Product& p, cons
         for (; at.step < p.steps; ++at.step, ++at.stages) {
             if (at.stages == until) return;
             const int step = at.step;
-            if (at.stages >= a.stages) {
-                // A warp whose wait for a full slot ran out gives the slot back all the same,
-                // behind the flag: with the flag up a slot may have a copy under way, and none
-                // is filled again.  The warp's lanes go on or give up together.
-                const bool empty = moe::mbar_wait(moe::smem_u32(&S.empty[at.slot]), at.turn ^ 1u, &S.abort_flag, kWaitNs);
-                if (!__all_sync(0xffffffffu, empty && !S.abort_flag)) {
-                    if (moe::elect_one()) {
-                        if (!S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
-                        S.abort_flag = 1;
-                    }
-                    at.gave_up = true;
-                    return;
-                }
-            }
             const uint32_t bar = moe::smem_u32(&S.full[at.slot]), dst = ring + at.slot * kStageBytes;
-            if (moe::elect_one()) {
-                if (step < p.whole_steps) {   // tiles past the last one come as zeros
+            if (moe::elect_one() && !at.gave_up) {
+                if (at.stages >= a.stages && !moe::mbar_wait(moe::smem_u32(&S.empty[at.slot]), at.turn ^ 1u, &S.abort_flag, kWaitNs)) {
+                    if (!S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
+                    S.abort_flag = 1;
+                    S.sent = at.stages;
+                    at.gave_up = true;
+                } else if (step < p.whole_steps) {   // tiles past the last one come as zeros
                     moe::mbar_arrive_expect_tx(bar, kStageBytes);
                     if (FIRST) moe::tma_load_5d(dst, &maps.whole, bar, 0, f0, 0, step * kTiles, e);
                     else moe::tma_load_4d(dst, &maps.whole, bar, 0, f0, step * kTiles, e);
@@ -493,10 +488,13 @@ __device__ __forceinline__ void produce(const Maps& maps, const Product& p, cons
 template <int NB>
 using Sums = float4[NB][kProduct][32];   // group of 8 rows, warp, lane
 
-// Where a product warp is in the ring.
+// Where a product warp is in the ring.  gives_back: its first lane, until a wait of it has run
+// out.  From then on the warp reads slots that may have a copy under way, and as it gives none
+// back none of its slots is filled again.
 struct Place {
     int stage, slot;   // the stage's number, and its slot
     uint32_t phase;
+    bool gives_back;
     __device__ __forceinline__ void go_to(int to, int stages) {
         slot += to - stage;
         stage = to;
@@ -645,8 +643,9 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, const 
                 const int step = 2 * i + half;
                 place.go_to(stage + step, a.stages);
                 if (!moe::mbar_wait(moe::smem_u32(&S.full[place.slot]), place.phase, &S.abort_flag, kWaitNs)) {
-                    if (lane == 0 && !S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
+                    if (!S.abort_flag) moe::raise_device_error(a.err, MOE_DEVERR_TIMEOUT);
                     S.abort_flag = 1;   // what follows is not waited for as long
+                    place.gives_back = false;
                 }
                 uint4 w[2][2];   // vector, row
 #pragma unroll
@@ -656,7 +655,7 @@ __device__ __forceinline__ void multiply(const Product& p, const Args& a, const 
                     w[j][1] = *reinterpret_cast<const uint4*>(at + 8 * kRowBytes);
                 }
                 __syncwarp();
-                if (lane == 0) moe::mbar_arrive(moe::smem_u32(&S.empty[place.slot]));
+                if (place.gives_back) moe::mbar_arrive(moe::smem_u32(&S.empty[place.slot]));
                 if (step < p.whole_steps ? step * kColumns<FP8> + tile * kTileColumns<FP8> >= p.whole : step > p.whole_steps || tile > 0 || p.whole == p.K) continue;
                 const uint8_t* x = xs + i * a.xrows * kXRow;
                 float t[NB][4];
@@ -814,6 +813,7 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warp == kProduct + 2 && lane == 0) {
         S.abort_flag = 0;
+        S.sent = INT_MAX;
         for (int i = 0; i < a.stages; ++i) {
             moe::mbar_init(moe::smem_u32(&S.full[i]), 1);
             moe::mbar_init(moe::smem_u32(&S.empty[i]), kTiles);
@@ -843,7 +843,7 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
             asm volatile("bar.sync %0, %1;" ::"n"(kLaidOut), "n"(kThreads) : "memory");
         }
     }
-    Place place{0, 0, 0};
+    Place place{0, 0, 0, lane == 0};
     int count = 0;
 #pragma unroll 1
     for (int part = 0; part < 2; ++part) {
@@ -858,9 +858,8 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
                 second = parked_run;
             }
             // before the grid has synchronised, as much of the second product as the ring holds
-            if (!at.gave_up)
-                produce<FP8, false, kInTurns>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
-            if (lane == 0) {
+            produce<FP8, false, kInTurns>(m2, a.p[1], a, plan, S, moe::smem_u32(ring), second, at, part == 0 ? at.stages + a.stages : INT_MAX);
+            if (moe::elect_one()) {
                 parked = at;
                 if (part == 0) parked_run = second;
             }
@@ -892,8 +891,9 @@ few_layer_kernel(const __grid_constant__ Maps m1, const __grid_constant__ Maps m
     }
     if (warp == kProduct + 2 && S.abort_flag) {   // whichever warp raised it: no copy may land after the block has ended
         int never = 0;
-        for (int i = 0; i < a.stages && i < parked.stages; ++i)
-            moe::mbar_wait(moe::smem_u32(&S.full[i]), static_cast<uint32_t>((parked.stages - 1 - i) / a.stages) & 1u, &never, kWaitNs / 16);
+        const int sent = min(S.sent, parked.stages);
+        for (int i = 0; i < a.stages && i < sent; ++i)
+            moe::mbar_wait(moe::smem_u32(&S.full[i]), static_cast<uint32_t>((sent - 1 - i) / a.stages) & 1u, &never, kWaitNs / 16);
     }
     if constexpr (ROUTES) sum_rows(a, kept.plan.slot_w, kept.plan.slot_row);
     else sum_rows(a, kept.slot_w, kept.slot_row);

@@ -2,19 +2,20 @@
 
 On the GPU a wait ends without its phase only if copies take seconds, which no test may bring about.
 The model has the kernel's parts: barriers that count arrivals and whose waits see only a phase's
-parity, a producer of lanes that each wait for themselves, sixteen warps that take a slot every
-other stage and give it back even after a wait that ran out, copies that land in any order and as
-late as they like.  Whatever runs out when: a slot with a copy under way is not filled again, the
-producer's lanes take the same way, every role comes to its end, and no copy lands after it.
+parity; a producer, one of whose lanes waits and sends, and which after a wait that ran out goes on
+without either; sixteen warps that take a slot every other stage and, after a wait that ran out, go
+on without giving slots back; copies that land in any order and as late as they like.  Whatever
+runs out when: a slot with a copy under way is not filled again, the producer's lanes take the same
+way, every role comes to its end, and no copy lands after it.
 
-`early`, `split` and `careless` are the rules that were wrong: filling slots on after another
-warp's wait had run out, lanes that judge for themselves, and waiting for copies under way only
-where the producer's own wait ran out."""
+`early`, `split` and `careless` are rules that were wrong: slots given back after a wait that ran
+out, a producer whose lanes each wait and judge for themselves, and waiting for copies under way
+only where the producer's own wait ran out."""
 import random
 
 import pytest
 
-WARPS, LANES = 16, 2
+WARPS = 16
 
 
 class Barrier:
@@ -51,8 +52,9 @@ def ring(steps, stages, units, seed, rules=(), timeouts=2):
             raise Broken("a slot with a copy under way is filled again")
         under_way.append(slot)
 
-    warps = [dict(stage=[u * steps + 2 * i + w // 8 for u in range(units) for i in range(steps // 2)], at=0) for w in range(WARPS)]
-    sent, verdicts, gave_up = 0, [None] * LANES, False
+    lanes = 2 if "split" in rules else 1
+    warps = [dict(gives_back=True, stage=[u * steps + 2 * i + w // 8 for u in range(units) for i in range(steps // 2)], at=0) for w in range(WARPS)]
+    sent, verdicts, gave_up = 0, [None] * lanes, False
 
     def outcome(barrier, parity):
         """True, False (ran out, or saw the flag) or None: still waiting."""
@@ -81,23 +83,24 @@ def ring(steps, stages, units, seed, rules=(), timeouts=2):
             if got is None:
                 continue
             if not got:
-                abort = True          # then the slot is given back all the same
+                abort = True
+                w["gives_back"] = "early" in rules
             w["at"] += 1
-            empty[stage % stages].arrive()
+            if w["gives_back"]:
+                empty[stage % stages].arrive()
         elif who == WARPS:
             if sent == total or gave_up:
                 continue
             slot = sent % stages
             if sent >= stages:
-                for lane in range(LANES):
+                for lane in range(lanes):
                     if verdicts[lane] is None:
-                        got = outcome(empty[slot], (sent // stages & 1) ^ 1)
-                        verdicts[lane] = got if "early" in rules or got is None else got and not abort
+                        verdicts[lane] = outcome(empty[slot], (sent // stages & 1) ^ 1)
                 if None in verdicts:
                     continue
-                if "split" in rules and len(set(verdicts)) > 1:
+                if len(set(verdicts)) > 1:
                     raise Broken("the producer's lanes take different ways")
-                go, verdicts = all(verdicts), [None] * LANES
+                go, verdicts = verdicts[0], [None] * lanes
                 if not go:
                     abort = gave_up = True
                     continue
