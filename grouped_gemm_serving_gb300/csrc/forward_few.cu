@@ -3,8 +3,15 @@
 //
 // With e = ids[t, j] the picks of token t and w[t, j] their weights:
 //   [g | u] = W1[e] x[t],   h = silu(g) u,   out[t] = sum_j w[t, j] W2[e] h.
-// Every weight of an expert that some token picked is read once, which bounds the
-// layer: 2 operations a weight and token against 2 bytes (bf16) or 1 (e4m3).
+// Every weight of an expert that some token picked is streamed once for each chunk of
+// its rows, which bounds the layer: 2 operations a weight and token against 2 bytes
+// (bf16) or 1 (e4m3).  A chunk holds up to 16 rows while rows of x are short, and what
+// shared memory leaves where they are long: above 16 tokens 15 of H = 2880, 7 of 5760, 6
+// of 7168 in bf16, and 11 of 4096, 5 of 7168 in FP8 (the longer of H and I counts).  With
+// more rows an expert than that, weights come twice or more, from L2 where chunks take
+// turns (below), and moe_forward gets faster: graphs, L2 flushed before each, us of it
+// and of this, 64 tokens top-4 of 32 experts, I = 2048: bf16 H = 7168 456, 577; FP8 H =
+// 4096 221, 224, H = 7168 317, 490; and with 32 tokens 447, 438; 233, 171; 327, 298.
 //
 // Routing: per expert the set of its tokens as a mask, whose bit counts are the
 // offsets, the permutation and its inverse (row r of an expert is its r-th token in
@@ -13,7 +20,7 @@
 // block makes it; up to 16 every block of the main kernel makes it for itself, which
 // saves that kernel and the 3 us from it to the cooperative one (a token of 32 bf16
 // experts 43.0 us instead of 45.4, of 256 e4m3 ones 70.4 instead of 73.6; 11 tokens of
-// 128 experts 84.4 instead of 86.2).
+// 128 experts 84.4 instead of 86.2, in one state's picks).
 //
 // The main kernel, a cooperative launch of a block per SM, streams the weights of
 // both products.  A unit is 16 weight rows (8 features' gate and up rows, or 16
@@ -361,10 +368,10 @@ __device__ __forceinline__ int4 chunk_of(const Args& a, const PlanOf<SLOTS>& pla
 // take turns, with as many features at a time as a block has units, so that neighbouring
 // blocks stream the same weights at the same time for two of its chunks, and one finds
 // them in L2: 64 tokens of 32 bf16 experts take 265 us instead of 283.  Not for FP8, whose
-// registers are full (us without turns and with them, H = 7168, I = 2048: 64 tokens top-4
-// of 32 experts 459, 454; 64 top-8 of 256 1347, 1377; 32 top-8 of 256 901, 912), nor up
-// to kLight tokens, where an expert has one chunk unless rows are very long (finding out
-// cost a token 1 to 2.6 us).
+// registers are full (12 and 24 bytes a thread spill in its kernels with 16 rows a chunk; us
+// without turns and with them, H = 7168, I = 2048: 64 tokens top-4 of 32 experts 459, 454;
+// 64 top-8 of 256 1347, 1377; 32 top-8 of 256 901, 912), nor up to kLight tokens, where an
+// expert has one chunk unless rows are very long (finding out cost a token 1 to 2.6 us).
 template <bool FP8, typename P>
 constexpr bool kTurns = !FP8 && std::is_same_v<P, Plan>;
 template <bool FIRST, bool TURNS>

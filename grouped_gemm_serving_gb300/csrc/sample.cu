@@ -18,9 +18,9 @@
 // does the rest with them alone.  No pass sorts the vocabulary.
 //
 // Bound by what a row's steps wait for one another, not by its bytes: 4.9 us would read
-// 64 rows of 131072 fp32 logits, which top-p takes 76 us for.  Of a row's 24 to 45 us
+// 64 rows of 131072 fp32 logits, which top-p takes 78 to 84 us for.  Of a row's 24 to 45 us
 // there, two rows to four SMs at a time, 2 go into loading it, 8 to 14 into the weights
-// of all tokens and their histogram (36 and some 20 issue cycles for 32 tokens), the rest
+// of all tokens and their histogram (40 and 20 issue cycles, about, for 32 tokens), the rest
 // into eight rounds of the cluster and what one block does alone.  256 rows of bf16 with
 // top-k: 61 us (9.9 to read), 9 to 10 a row; one row of 32000 with both: 6 us.
 //
@@ -99,8 +99,9 @@ struct Weight {
     // t = (l - L) c = m / 64 + r with |r| <= 1/128, and 2^t = 2^(m / 64) e^(r ln 2): a table
     // of 64 powers and four terms of the series (as in P. Tang's table-driven
     // exponentials).  t, r and the series' first term are kept in two floats each.
-    // Without branches, 36 issue cycles for 32 tokens.  A copy of the powers for every
-    // pair of banks and rounding by addition instead of conversions took longer (37).
+    // Without branches, 36 issue cycles for 32 tokens and some four for the last rounding.
+    // A copy of the powers for every pair of banks and rounding by addition instead of
+    // conversions took longer (37).
     __device__ __forceinline__ uint64_t operator()(float l) const {
         if (top == INFINITY) return l == top ? 1ull << kUnit : 0;   // the same for all
         const float d = l - top;
