@@ -647,9 +647,10 @@ moe_status_t moe_forward(const moe_forward_args* args, void* ws, size_t ws_bytes
  * So it is the faster call while experts have few rows.  Measured (I = 2048): for
  * T*k / E up to some 4 with H = 7168 and 6 with H = 4096 or 5760; up to 3 with 128
  * experts of H = 2048, I = 768; for all T with 32 experts top-4 of H = I = 2880.
- * Above that take moe_forward.  Same arguments and routing as moe_forward; out[t] = sum over j of topk_w[t, j] * W2[e] h in fp32, in slot
- * order, rounded to bf16 once; h = silu(g) * u is rounded to bf16 in between, and
- * for FP8 to 11 bits.
+ * Above that take moe_forward.
+ * Same arguments and routing as moe_forward; out[t] = sum over j of
+ * topk_w[t, j] * W2[e] h in fp32, in slot order, rounded to bf16 once; h =
+ * silu(g) * u is rounded to bf16 in between, and for FP8 to 11 bits.
  * MOE_FP8_E4M3_B128: the weights are e4m3 with block scales as in moe_forward,
  * but x and h are not quantised (as moe_forward's are), so the results lie
  * closer to the unquantised layer's than moe_forward's do.
